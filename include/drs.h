@@ -47,8 +47,22 @@ typedef enum drs_probs_dtype {
     DRS_PROBS_FP16 = 2
 } drs_probs_dtype;
 
+/* Element types of the token operators (drs_verify_drafts and below). BF16
+ * and FP16 have the values of drs_probs_dtype. */
+typedef enum drs_dtype {
+    DRS_DTYPE_FP32 = 0,
+    DRS_DTYPE_BF16 = 1,
+    DRS_DTYPE_FP16 = 2
+} drs_dtype;
+
 /* Largest vocabulary (row length) the kernels accept (2^21). */
 #define DRS_MAX_VOCAB 2097152
+
+/* Largest sizes of the token operators: requests of drs_map_slots, tokens of
+ * drs_embed_tokens_grad, columns of an embedding row. */
+#define DRS_MAX_REQUESTS 1048576
+#define DRS_MAX_TOKENS 268435456
+#define DRS_MAX_WIDTH 1048576
 
 /*
  * Bytes of device workspace drs_row_stats needs (at least 256-byte aligned,
@@ -412,6 +426,162 @@ drs_status drs_stash_converged_logprobs(const float *logits, int64_t logits_rows
                                         int32_t *out_ids, float *out_logprobs,
                                         int32_t *out_ranks, int logits_mode, void *workspace,
                                         size_t workspace_bytes, void *stream);
+
+/*
+ * Verification of drafted tokens against the target model's probabilities
+ * (speculative sampling), with the random numbers given. The probabilities
+ * are rows as drs_row_stats writes them, or fp32 ones. Request b has
+ *   k_b = cu_drafts[b + 1] - cu_drafts[b]
+ * drafted tokens (at most max_drafts; more are not looked at), its draft j
+ * being entry r = cu_drafts[b] + j of draft_tokens, accept_u and the rows of
+ * draft. The target has one row more per request: row cu_drafts[b] + b + j
+ * is the distribution that draft j is held against, j == k_b the one after
+ * the last draft.
+ *   - Draft j is accepted when accept_u[r] * q < p, with p and q the target's
+ *     and the draft's probability of draft_tokens[r] (the product is exact;
+ *     q is 1 without draft probabilities). A token outside [0, vocab) is
+ *     refused. Drafts count up to the first refused one.
+ *   - Then one more token is drawn. After a refused draft: from the weights
+ *     max(p - q, 0) of its position (the fp32 difference), or, without
+ *     draft probabilities, from p without the refused token; where these
+ *     weights are all 0, from p. After the last draft: from p of the next
+ *     position. NaN and negative weights are 0; infinite ones are not supported.
+ *     The token is the lowest column whose running sum of weights exceeds
+ *     sample_u[b] times their total (the sums are good to about 1e-14);
+ *     -1 where there is no weight at all.
+ *
+ *   target      target_dtype [target_rows, vocab], row stride target_stride.
+ *   draft       draft_dtype [draft_rows, vocab], row stride draft_stride, or
+ *               NULL (drafts without probabilities, such as looked-up ones).
+ *   draft_rows  the number of drafted tokens; draft_tokens int64 and
+ *               accept_u fp32 [draft_rows], uniform in [0, 1). Both may be
+ *               NULL when it is 0.
+ *   cu_drafts   int32 [requests + 1].
+ *   sample_u    fp32 [requests], uniform in [0, 1).
+ *   out_tokens  int64 [requests, max_drafts + 1]: the accepted drafts, the
+ *               drawn token, then -1.
+ *   out_accepted int32 [requests]: the number of accepted drafts. A
+ *               request whose rows fall outside draft_rows or target_rows
+ *               gets -1 here and in all its tokens.
+ *
+ * A row is read at most once (two with draft probabilities): the one that
+ * the token is drawn from. No workspace. Rows that start 16-byte aligned are
+ * read faster. requests == 0 is a no-op. Returns DRS_ERR_INVALID_ARG for
+ * negative sizes, an unknown type, a stride below vocab, a null or unaligned
+ * pointer; DRS_ERR_UNSUPPORTED for vocab > DRS_MAX_VOCAB or more than
+ * 2^27 - 1 requests.
+ */
+drs_status drs_verify_drafts(const void *target, drs_dtype target_dtype, int64_t target_rows,
+                             int64_t target_stride, const void *draft, drs_dtype draft_dtype,
+                             int64_t draft_rows, int64_t draft_stride, int64_t vocab,
+                             const int64_t *draft_tokens, const int32_t *cu_drafts,
+                             int64_t requests, int32_t max_drafts, const float *accept_u,
+                             const float *sample_u, int64_t *out_tokens, int32_t *out_accepted,
+                             void *stream);
+
+/*
+ * Block tables and slot maps of a paged cache, from the requests' lengths on
+ * the GPU. Request b has lens[b] tokens in the cache and adds new_lens[b]
+ * (negative lengths are 0). Its row of the block table holds the
+ * ids of the blocks of block_size tokens that it has: columns [0, held[b]).
+ * The call makes that ceil((lens + new) / block_size) blocks: missing ones
+ * come from a ring of free block ids, blocks beyond go back to it (all of a
+ * request whose lengths are 0), both in request order. Then every new token
+ * gets its request, its position and its place in the cache.
+ *
+ *   block_table int32 [requests, max_blocks], row stride table_stride,
+ *               updated in place: columns [held[b], out_held[b]) are written,
+ *               no other.
+ *   free_ring   int32 [ring_size], updated in place. ring_state[0] (head)
+ *               and ring_state[1] (tail) count the ids ever taken and given:
+ *               the free ids are free_ring[i % ring_size] for head <= i <
+ *               tail. ring_size is at least the number of blocks of
+ *               the cache. Ids given back in a call are free from the next.
+ *   out_held    int32 [requests]: blocks now held (may be held itself).
+ *   out_ring_state int64 [2]: the counters after the call (may be ring_state
+ *               itself).
+ *   out_lacking int32 [1]: blocks that lengths asked for and did not get: the
+ *               ring ran out (a request is served when its blocks and those of
+ *               the requests before it are there, and keeps what it holds
+ *               otherwise) or the table's row has no more columns. 0 in
+ *               ordinary operation.
+ *   capacity    entries of the token arrays (a captured graph's size, say);
+ *               tokens beyond it are left out.
+ *   out_cu      int32 [requests + 1]: the first token of each request, and
+ *               the number of tokens.
+ *   out_request, out_position int32 [capacity], out_slot int64 [capacity]:
+ *               token t = out_cu[b] + j has request b, position lens[b] + j
+ *               and slot block_table[b][position / block_size] * block_size
+ *               + position % block_size, -1 where the request has no block
+ *               for it. Entries past the last token: -1, 0, -1.
+ *
+ * Arrays do not overlap except as said. One launch, no workspace; the
+ * arrays' contents cannot lead outside them. Positions are at most 2^31 - 1.
+ * Returns DRS_ERR_INVALID_ARG for sizes out of range or a null or
+ * unaligned pointer; DRS_ERR_UNSUPPORTED for more than DRS_MAX_REQUESTS
+ * requests or 2^31 - 1 tokens.
+ */
+drs_status drs_map_slots(const int32_t *lens, const int32_t *new_lens, const int32_t *held,
+                         int64_t requests, int32_t block_size, int32_t *block_table,
+                         int64_t table_stride, int32_t max_blocks, int32_t *free_ring,
+                         int64_t ring_size, const int64_t *ring_state, int64_t capacity,
+                         int32_t *out_cu, int32_t *out_request, int32_t *out_position,
+                         int64_t *out_slot, int32_t *out_held, int64_t *out_ring_state,
+                         int32_t *out_lacking, void *stream);
+
+/*
+ * The embedding lookup with scaling: out[t] = scale * table[ids[t]], the
+ * product taken in fp32 and rounded once. Rows of ids outside [0, vocab)
+ * (padding) are 0.
+ *
+ *   table       dtype [vocab, width], row stride table_stride.
+ *   ids         int32 or int64 [tokens] (id_bits 32 or 64).
+ *   out         dtype [tokens, width], row stride out_stride.
+ *
+ * tokens == 0 is a no-op. Any alignment and stride; tables whose rows
+ * start 16-byte aligned are read faster. Returns DRS_ERR_INVALID_ARG for
+ * sizes out of range, an unknown type, a stride below width or a null or
+ * unaligned pointer; DRS_ERR_UNSUPPORTED for vocab > DRS_MAX_VOCAB, width
+ * > DRS_MAX_WIDTH or too many tokens for one launch (2^31 - 1 blocks).
+ */
+drs_status drs_embed_tokens(const void *table, drs_dtype dtype, int64_t vocab, int64_t width,
+                            int64_t table_stride, const void *ids, int32_t id_bits,
+                            int64_t tokens, float scale, void *out, int64_t out_stride,
+                            void *stream);
+
+/*
+ * Bytes of device workspace drs_embed_tokens_grad needs (256-byte aligned,
+ * contents arbitrary); 0 for no tokens or sizes out of range. Same sharing
+ * rule as the row-stats workspace.
+ */
+size_t drs_embed_tokens_grad_workspace_bytes(int64_t tokens, int64_t vocab, int64_t width);
+
+/*
+ * The gradient of drs_embed_tokens with respect to its table:
+ *   grad_table[v] = (accumulate ? grad_table[v] : 0)
+ *                   + scale * sum of grad_out[t] over the tokens t with
+ *                     ids[t] == v.
+ * The sums are fp32 and are added in an order that depends on the ids alone
+ * (equal calls give equal bits); the result is rounded once.
+ * Ids outside [0, vocab) have no part in it. With accumulate only the rows of
+ * ids that occur are read and written, else every row is written.
+ *
+ *   grad_out    grad_dtype [tokens, width], row stride grad_stride.
+ *   ids, id_bits as drs_embed_tokens.
+ *   grad_table  table_dtype [vocab, width], row stride table_stride.
+ *   workspace   drs_embed_tokens_grad_workspace_bytes(tokens, vocab, width).
+ *
+ * Returns DRS_ERR_INVALID_ARG for sizes out of range, an unknown type, a
+ * stride below width, a null or unaligned pointer or a small workspace;
+ * DRS_ERR_UNSUPPORTED for sizes above DRS_MAX_TOKENS, DRS_MAX_VOCAB or
+ * DRS_MAX_WIDTH.
+ */
+drs_status drs_embed_tokens_grad(const void *grad_out, drs_dtype grad_dtype, int64_t tokens,
+                                 int64_t width, int64_t grad_stride, const void *ids,
+                                 int32_t id_bits, float scale, int accumulate,
+                                 void *grad_table, drs_dtype table_dtype, int64_t vocab,
+                                 int64_t table_stride, void *workspace, size_t workspace_bytes,
+                                 void *stream);
 
 /* Static, human-readable name of a status code. */
 const char *drs_status_string(drs_status s);

@@ -12,9 +12,12 @@ Entry points (same names as the C ABI):
   drs_row_stats_topk, drs_row_stats_topk_workspace_bytes, drs_topk_logprobs,
   drs_topk_workspace_bytes, drs_philox_gumbel, drs_scaled_logits,
   drs_stash_converged_logprobs, drs_stash_workspace_bytes,
+  drs_verify_drafts, drs_map_slots, drs_embed_tokens, drs_embed_tokens_grad,
+  drs_embed_tokens_grad_workspace_bytes,
   drs_status_string, drs_get_device_error.
 Convenience wrappers that allocate outputs: row_stats, row_stats_topk,
-topk_logprobs, philox_gumbel, stash_converged_logprobs.
+topk_logprobs, philox_gumbel, stash_converged_logprobs, verify_drafts,
+map_slots, embed_tokens, embed_tokens_grad.
 """
 from __future__ import annotations
 
@@ -30,7 +33,11 @@ DRS_ERR_CUDA = -3
 DRS_ERR_DEVICE_TIMEOUT = -4
 
 DRS_PROBS_NONE, DRS_PROBS_BF16, DRS_PROBS_FP16 = 0, 1, 2
+DRS_DTYPE_FP32, DRS_DTYPE_BF16, DRS_DTYPE_FP16 = 0, 1, 2
 DRS_MAX_VOCAB = 2097152
+DRS_MAX_REQUESTS = 1048576
+DRS_MAX_TOKENS = 268435456
+DRS_MAX_WIDTH = 1048576
 
 EXPORTED = ("drs_row_stats", "drs_row_stats_workspace_bytes", "drs_row_stats_noalloc",
             "drs_row_stats_topk", "drs_row_stats_topk_workspace_bytes", "drs_topk_logprobs",
@@ -39,7 +46,8 @@ EXPORTED = ("drs_row_stats", "drs_row_stats_workspace_bytes", "drs_row_stats_noa
             "drs_kernel_timing", "drs_kernel_times", "drs_row_stats_seeds",
             "drs_row_stats_seeds_workspace_bytes", "drs_stash_converged_logprobs",
             "drs_stash_workspace_bytes", "drs_test_two_pass",
-            "drs_row_split_plan")
+            "drs_row_split_plan", "drs_verify_drafts", "drs_map_slots", "drs_embed_tokens",
+            "drs_embed_tokens_grad", "drs_embed_tokens_grad_workspace_bytes")
 
 
 class DrsError(RuntimeError):
@@ -115,6 +123,20 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.drs_kernel_timing.restype = ctypes.c_int
     lib.drs_kernel_times.argtypes = [vp, i32, vp]
     lib.drs_kernel_times.restype = ctypes.c_int
+    lib.drs_verify_drafts.argtypes = [vp, ctypes.c_int, i64, i64, vp, ctypes.c_int, i64, i64, i64,
+                                      vp, vp, i64, i32, vp, vp, vp, vp, vp]
+    lib.drs_verify_drafts.restype = ctypes.c_int
+    lib.drs_map_slots.argtypes = [vp, vp, vp, i64, i32, vp, i64, i32, vp, i64, vp, i64, vp, vp, vp,
+                                  vp, vp, vp, vp, vp]
+    lib.drs_map_slots.restype = ctypes.c_int
+    lib.drs_embed_tokens.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i32, i64, ctypes.c_float,
+                                     vp, i64, vp]
+    lib.drs_embed_tokens.restype = ctypes.c_int
+    lib.drs_embed_tokens_grad_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.drs_embed_tokens_grad_workspace_bytes.restype = sz
+    lib.drs_embed_tokens_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i32, ctypes.c_float,
+                                          ctypes.c_int, vp, ctypes.c_int, i64, i64, vp, sz, vp]
+    lib.drs_embed_tokens_grad.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -269,6 +291,152 @@ def drs_scaled_logits(logits, temp: float, out, stream=None):
     assert logits.is_contiguous() and out.is_contiguous() and out.numel() == logits.numel()
     st = load().drs_scaled_logits(_ptr(logits), logits.numel(), temp, _ptr(out), _stream(stream))
     _check(st, "drs_scaled_logits")
+
+
+# The token operators check what the library cannot: the types, devices and
+# lengths of the arrays (ValueError). Sizes, strides and alignment are the
+# library's own checks (DrsError).
+
+def _dtype_code(t, name: str) -> int:
+    import torch
+    code = {torch.float32: DRS_DTYPE_FP32, torch.bfloat16: DRS_DTYPE_BF16,
+            torch.float16: DRS_DTYPE_FP16}.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: fp32, bf16 or fp16 expected, got {t.dtype}")
+    return code
+
+
+def _need(t, name: str, dtype, shape, device):
+    """A contiguous tensor of this type and shape on this device."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} {tuple(shape)} on {device} expected, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
+
+
+def _need_rows(t, name: str, device=None):
+    """A 2-D tensor with unit column stride (any row stride) on a GPU;
+    returns the row stride."""
+    if t.dim() != 2 or t.device.type != "cuda" or (device is not None and t.device != device):
+        raise ValueError(f"{name}: 2-D on {device or 'a CUDA device'} expected, got {t.dim()}-D on {t.device}")
+    rows, columns = t.shape
+    step, unit = t.stride()
+    if rows == 0 or columns == 0:
+        return columns
+    if columns > 1 and unit != 1:
+        raise ValueError(f"{name}: unit column stride expected, got strides {t.stride()}")
+    return step if rows > 1 else max(step, columns)
+
+
+def drs_verify_drafts(target, draft, draft_tokens, cu_drafts, accept_u, sample_u, out_tokens,
+                      out_accepted, stream=None):
+    """Launch drs_verify_drafts: target [drafts + requests, vocab], draft
+    [drafts, vocab] or None, out_tokens int64 [requests, max_drafts + 1]."""
+    import torch
+    dev = target.device
+    target_stride = _need_rows(target, "target")
+    target_code = _dtype_code(target, "target")
+    target_rows, vocab = target.shape
+    drafts = draft_tokens.numel()
+    draft_code, draft_stride = 0, 0
+    if draft is not None:
+        draft_stride = _need_rows(draft, "draft", dev)
+        draft_code = _dtype_code(draft, "draft")
+        if draft.shape != (drafts, vocab):
+            raise ValueError(f"draft: {(drafts, vocab)} expected, got {tuple(draft.shape)}")
+    requests = sample_u.numel()
+    _need(draft_tokens, "draft_tokens", torch.int64, (drafts,), dev)
+    _need(accept_u, "accept_u", torch.float32, (drafts,), dev)
+    _need(cu_drafts, "cu_drafts", torch.int32, (requests + 1,), dev)
+    _need(sample_u, "sample_u", torch.float32, (requests,), dev)
+    if out_tokens.dim() != 2 or out_tokens.shape[1] < 1:
+        raise ValueError(f"out_tokens: [requests, max_drafts + 1] expected, got {tuple(out_tokens.shape)}")
+    _need(out_tokens, "out_tokens", torch.int64, (requests, out_tokens.shape[1]), dev)
+    _need(out_accepted, "out_accepted", torch.int32, (requests,), dev)
+    st = load().drs_verify_drafts(target.data_ptr(), target_code, target_rows, target_stride,
+                                  None if draft is None else draft.data_ptr(), draft_code, drafts,
+                                  draft_stride, vocab, draft_tokens.data_ptr(), cu_drafts.data_ptr(),
+                                  requests, out_tokens.shape[1] - 1, accept_u.data_ptr(),
+                                  sample_u.data_ptr(), out_tokens.data_ptr(), out_accepted.data_ptr(),
+                                  _stream(stream))
+    _check(st, "drs_verify_drafts")
+
+
+def drs_map_slots(lens, new_lens, held, block_table, block_size: int, free_ring, ring_state, out_cu,
+                  out_request, out_position, out_slot, out_held, out_ring_state, out_lacking,
+                  stream=None):
+    """Launch drs_map_slots: int32 lengths [requests], block_table int32
+    [requests, max_blocks] (any row stride); the token arrays' length is the
+    capacity. block_table and free_ring are updated in place; out_held and
+    out_ring_state may be held and ring_state."""
+    import torch
+    dev = lens.device
+    i32, i64 = torch.int32, torch.int64
+    requests, capacity = lens.numel(), out_request.numel()
+    table_stride = _need_rows(block_table, "block_table", dev)
+    if block_table.dtype != i32 or block_table.shape[0] != requests:
+        raise ValueError(f"block_table: int32 [{requests}, max_blocks] expected, got {block_table.dtype} "
+                         f"{tuple(block_table.shape)}")
+    for t, name, dtype, n in ((lens, "lens", i32, requests), (new_lens, "new_lens", i32, requests),
+                              (held, "held", i32, requests), (free_ring, "free_ring", i32, free_ring.numel()),
+                              (ring_state, "ring_state", i64, 2), (out_cu, "out_cu", i32, requests + 1),
+                              (out_request, "out_request", i32, capacity),
+                              (out_position, "out_position", i32, capacity),
+                              (out_slot, "out_slot", i64, capacity), (out_held, "out_held", i32, requests),
+                              (out_ring_state, "out_ring_state", i64, 2), (out_lacking, "out_lacking", i32, 1)):
+        _need(t, name, dtype, (n,), dev)
+    st = load().drs_map_slots(lens.data_ptr(), new_lens.data_ptr(), held.data_ptr(), requests, block_size,
+                              block_table.data_ptr(), table_stride, block_table.shape[1],
+                              free_ring.data_ptr(), free_ring.numel(), ring_state.data_ptr(), capacity,
+                              out_cu.data_ptr(), out_request.data_ptr(), out_position.data_ptr(),
+                              out_slot.data_ptr(), out_held.data_ptr(), out_ring_state.data_ptr(),
+                              out_lacking.data_ptr(), _stream(stream))
+    _check(st, "drs_map_slots")
+
+
+def _id_bits(ids, dev) -> int:
+    import torch
+    bits = {torch.int32: 32, torch.int64: 64}.get(ids.dtype)
+    if bits is None or ids.dim() != 1 or ids.device != dev or not ids.is_contiguous():
+        raise ValueError(f"ids: contiguous 1-D int32 or int64 on {dev} expected, got {ids.dtype} "
+                         f"{tuple(ids.shape)} on {ids.device}, strides {ids.stride()}")
+    return bits
+
+
+def drs_embed_tokens(table, ids, scale: float, out, stream=None):
+    """Launch drs_embed_tokens: table [vocab, width], ids int32 or int64
+    [tokens], out [tokens, width] of the table's type."""
+    table_stride, out_stride = _need_rows(table, "table"), _need_rows(out, "out", table.device)
+    vocab, width = table.shape
+    bits = _id_bits(ids, table.device)
+    if out.dtype != table.dtype or out.shape != (ids.numel(), width):
+        raise ValueError(f"out: {table.dtype} {(ids.numel(), width)} expected, got {out.dtype} {tuple(out.shape)}")
+    st = load().drs_embed_tokens(table.data_ptr(), _dtype_code(table, "table"), vocab, width, table_stride,
+                                 ids.data_ptr(), bits, ids.numel(), scale, out.data_ptr(), out_stride,
+                                 _stream(stream))
+    _check(st, "drs_embed_tokens")
+
+
+def drs_embed_tokens_grad_workspace_bytes(tokens: int, vocab: int, width: int) -> int:
+    return int(load().drs_embed_tokens_grad_workspace_bytes(tokens, vocab, width))
+
+
+def drs_embed_tokens_grad(grad_out, ids, scale: float, accumulate: bool, grad_table, workspace=None,
+                          stream=None):
+    """Launch drs_embed_tokens_grad: grad_out [tokens, width], grad_table
+    [vocab, width] (each fp32, bf16 or fp16)."""
+    grad_stride = _need_rows(grad_out, "grad_out")
+    table_stride = _need_rows(grad_table, "grad_table", grad_out.device)
+    vocab, width = grad_table.shape
+    bits = _id_bits(ids, grad_out.device)
+    if grad_out.shape != (ids.numel(), width):
+        raise ValueError(f"grad_out: {(ids.numel(), width)} expected, got {tuple(grad_out.shape)}")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = load().drs_embed_tokens_grad(grad_out.data_ptr(), _dtype_code(grad_out, "grad_out"), ids.numel(), width,
+                                      grad_stride, ids.data_ptr(), bits, scale, 1 if accumulate else 0,
+                                      grad_table.data_ptr(), _dtype_code(grad_table, "grad_table"), vocab,
+                                      table_stride, None if workspace is None else workspace.data_ptr(),
+                                      ws_bytes, _stream(stream))
+    _check(st, "drs_embed_tokens_grad")
 
 
 KERNEL_NAMES = ("split_prep", "split_pass1", "split_merge", "split_pass2", "split_cluster",
@@ -457,3 +625,74 @@ def stash_converged_logprobs(logits, canvas_len: int, src, slots, keep, valid, t
                                  num_token_ids, token_ids, out_ids, out_logprobs, out_ranks,
                                  logits_mode, ws, stream)
     return out_ids, out_logprobs, out_ranks
+
+
+def _allocate_on(stream):
+    """Where a call on `stream` allocates: the caching allocator hands memory
+    on in the order of the stream that it was allocated on."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def verify_drafts(target_probs, draft_tokens, cu_drafts, accept_u, sample_u, max_drafts: int,
+                  draft_probs=None, out_tokens=None, out_accepted=None, stream=None):
+    """Verify drafted tokens against the target's probabilities (see
+    drs_verify_drafts); returns (tokens int64 [requests, max_drafts + 1]: the
+    accepted drafts, one more token, then -1; accepted int32 [requests])."""
+    import torch
+    requests = sample_u.numel()
+    if max_drafts < 0 or (out_tokens is not None and out_tokens.shape != (requests, max_drafts + 1)):
+        raise ValueError(f"out_tokens: [{requests}, max_drafts + 1] with max_drafts {max_drafts} expected")
+    with _allocate_on(stream):
+        if out_tokens is None:
+            out_tokens = torch.empty(requests, max_drafts + 1, dtype=torch.int64, device=target_probs.device)
+        if out_accepted is None:
+            out_accepted = torch.empty(requests, dtype=torch.int32, device=target_probs.device)
+    drs_verify_drafts(target_probs, draft_probs, draft_tokens, cu_drafts, accept_u, sample_u, out_tokens,
+                      out_accepted, stream)
+    return out_tokens, out_accepted
+
+
+def map_slots(lens, new_lens, held, block_table, block_size: int, free_ring, ring_state, capacity: int,
+              out=None, stream=None):
+    """Block tables and slot maps from the requests' lengths (see
+    drs_map_slots). Returns `out`: (cu, request, position, slot, held,
+    ring_state, lacking), allocated when not given; block_table and
+    free_ring are updated in place."""
+    import torch
+    if out is None:
+        dev, requests = lens.device, lens.numel()
+        i32, i64 = dict(dtype=torch.int32, device=dev), dict(dtype=torch.int64, device=dev)
+        with _allocate_on(stream):
+            out = (torch.empty(requests + 1, **i32), torch.empty(capacity, **i32), torch.empty(capacity, **i32),
+                   torch.empty(capacity, **i64), torch.empty(requests, **i32), torch.empty(2, **i64),
+                   torch.empty(1, **i32))
+    elif out[1].numel() != capacity:
+        raise ValueError(f"out: token arrays of {capacity} entries expected, got {out[1].numel()}")
+    drs_map_slots(lens, new_lens, held, block_table, block_size, free_ring, ring_state, *out, stream=stream)
+    return out
+
+
+def embed_tokens(table, ids, scale: float = 1.0, out=None, stream=None):
+    """scale * table[ids] (see drs_embed_tokens); rows of ids outside the
+    vocabulary are 0."""
+    import torch
+    if out is None:
+        with _allocate_on(stream):
+            out = torch.empty(ids.numel(), table.shape[1], dtype=table.dtype, device=table.device)
+    drs_embed_tokens(table, ids, scale, out, stream)
+    return out
+
+
+def embed_tokens_grad(grad_out, ids, scale: float, grad_table, accumulate: bool = False, stream=None):
+    """The gradient of embed_tokens with respect to its table, written (or
+    added) into grad_table [vocab, width], which is returned (see
+    drs_embed_tokens_grad)."""
+    import torch
+    vocab, width = grad_table.shape
+    with _allocate_on(stream):
+        ws = torch.empty(drs_embed_tokens_grad_workspace_bytes(ids.numel(), vocab, width), dtype=torch.uint8,
+                         device=grad_out.device)
+    drs_embed_tokens_grad(grad_out, ids, scale, accumulate, grad_table, ws, stream)
+    return grad_table

@@ -1,0 +1,125 @@
+// token_common.cuh -- building blocks of the token operators (verify.cu,
+// slots.cu, embed.cu, embed_grad.cu): element types, vector accesses and
+// block-wide scans.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "drs_device.cuh"
+#include "drs_internal.h"
+
+namespace drs {
+
+__host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ------------------------------------------------------------- elements
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+
+// Rounded to nearest even.
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+// 16 bytes read once: not kept in L1.
+__device__ __forceinline__ uint4 load16_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Eight consecutive elements as they lie in memory (16-byte aligned): one
+// or two 16-byte words.
+template <typename T> struct Raw8 {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            w[i] = load16_stream(reinterpret_cast<const char*>(p) + 16 * i);
+    }
+    __device__ __forceinline__ void unpack(float (&v)[8]) const;
+};
+template <> __device__ __forceinline__ void Raw8<float>::unpack(float (&v)[8]) const {
+    v[0] = __uint_as_float(w[0].x), v[1] = __uint_as_float(w[0].y);
+    v[2] = __uint_as_float(w[0].z), v[3] = __uint_as_float(w[0].w);
+    v[4] = __uint_as_float(w[1].x), v[5] = __uint_as_float(w[1].y);
+    v[6] = __uint_as_float(w[1].z), v[7] = __uint_as_float(w[1].w);
+}
+template <> __device__ __forceinline__ void Raw8<__nv_bfloat16>::unpack(float (&v)[8]) const {
+    const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // a bf16 is the upper half of its fp32
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+}
+template <> __device__ __forceinline__ void Raw8<__half>::unpack(float (&v)[8]) const {
+    const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = *reinterpret_cast<const __half2*>(&u[i]);
+        const float2 f = __half22float2(h);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+// ------------------------------------------------------------- scans
+
+template <typename T> __device__ __forceinline__ T warp_scan_inclusive(T v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const T u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+template <typename T> __device__ __forceinline__ T warp_sum(T v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// ------------------------------------------------------------- clusters
+
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Store 8 bytes into the same shared-memory variable of CTA `rank` of the
+// cluster.
+__device__ __forceinline__ void store_remote(void* local, uint32_t rank, uint64_t v) {
+    uint32_t addr;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+// ------------------------------------------------------------- host side
+
+inline bool dtype_ok(drs_dtype t) { return t == DRS_DTYPE_FP32 || t == DRS_DTYPE_BF16 || t == DRS_DTYPE_FP16; }
+inline size_t dtype_bytes(drs_dtype t) { return t == DRS_DTYPE_FP32 ? 4 : 2; }
+
+// f(T{}) for the element type that `t` names.
+template <typename F> auto with_dtype(drs_dtype t, F f) {
+    if (t == DRS_DTYPE_FP32) return f(float{});
+    if (t == DRS_DTYPE_BF16) return f(__nv_bfloat16{});
+    return f(__half{});
+}
+
+}  // namespace drs

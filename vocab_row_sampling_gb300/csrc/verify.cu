@@ -1,0 +1,431 @@
+// verify.cu -- verification of drafted tokens against the target's
+// probabilities (drs_verify_drafts).
+//
+// Speculative sampling (Leviathan, Kalman and Matias, "Fast inference from
+// transformers via speculative decoding", 2023): draft j of a request is
+// kept while u_j q_j(x_j) < p_j(x_j); the token after the kept ones is drawn
+// from max(p - q, 0) of the first refused position, or from p of the
+// position after the last draft. The draw is by inversion: the lowest
+// column whose running sum of weights exceeds u times their total.
+//
+// One launch. A thread-block cluster takes a request: every warp reads the
+// request's few drafted probabilities itself (no barrier), then the cluster's
+// CTAs sum a share of the one row (two with draft probabilities) that the
+// draw needs, exchange their totals through distributed shared memory, and
+// the CTA whose share holds the drawn column reads one warp's part of it
+// again (from L2) to find the column. Bound by memory for large batches: each
+// needed row is read once.
+//
+// Sums. A drawn column moves when the running sums are off by more than the
+// distance of u * total to a border, so they are held to about 1e-14: a
+// thread adds its weights into a pair of fp32 (the sum and the error of each
+// addition, Knuth's two-sum), and pairs are joined in fp64. An fp64 addition
+// per weight would be bound by the fp64 rate (about 0.6 T additions/s, a
+// third of what the memory delivers). The weight itself is the fp32
+// difference p - q, rounded once (relative 2^-24, exact between values of
+// near exponents).
+#include <climits>
+#include <type_traits>
+
+#include "token_common.cuh"
+
+namespace drs {
+namespace {
+
+constexpr int kVerifyThreads = 512;
+constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kMaxCluster = 16;
+constexpr int kStep = 256;  // elements a warp takes at once: 8 per lane
+
+struct NoDraft {};
+
+struct VerifyParams {
+    const void* target;
+    const void* draft;
+    const int64_t* tokens;
+    const int32_t* cu;
+    const float* accept_u;
+    const float* sample_u;
+    int64_t* out_tokens;
+    int32_t* out_accepted;
+    int64_t target_rows, target_stride, draft_rows, draft_stride;
+    int32_t vocab, max_drafts, cluster;
+};
+
+// A sum of fp32 values as s + c.
+struct PairSum {
+    float s = 0.0f, c = 0.0f;
+    __device__ __forceinline__ void add(float w) {
+        const float t = s + w;
+        const float z = t - s;
+        c += (s - (t - z)) + (w - z);
+        s = t;
+    }
+    __device__ __forceinline__ double value() const { return static_cast<double>(s) + static_cast<double>(c); }
+};
+
+// The row (or pair of rows) a request draws from. q is null where nothing
+// is subtracted; `without` is a column whose weight is 0 (-1: none).
+template <typename P, typename Q> struct Weights {
+    const P* p;
+    const Q* q;
+    int without;
+    bool vec;  // both rows start 16-byte aligned
+
+    __device__ __forceinline__ float one(int i) const {
+        float w = to_f(p[i]);
+        if constexpr (!std::is_same<Q, NoDraft>::value) {
+            if (q) w -= to_f(q[i]);
+        }
+        return i == without ? 0.0f : fmaxf(w, 0.0f);  // NaN counts as 0
+    }
+
+    // Eight columns from i on (i a multiple of 8, i + 8 <= vocab).
+    template <bool kSub> __device__ __forceinline__ void finish(const Raw8<P>& rp, const float (&qv)[8], int i,
+                                                                float (&w)[8]) const {
+        rp.unpack(w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = fmaxf(kSub ? w[e] - qv[e] : w[e], 0.0f);
+        if (!kSub && static_cast<uint32_t>(without - i) < 8u) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e == without) w[e] = 0.0f;
+        }
+    }
+
+    // Columns i .. i+7 (i a multiple of 8), 0 from `end` on.
+    __device__ __forceinline__ void load(int64_t i, int end, float (&w)[8]) const {
+        if (vec && i + 8 <= end) {
+            Raw8<P> rp;
+            rp.load(p + i);
+            if constexpr (!std::is_same<Q, NoDraft>::value) {
+                if (q) {
+                    Raw8<Q> rq;
+                    float qv[8];
+                    rq.load(q + i);
+                    rq.unpack(qv);
+                    finish<true>(rp, qv, static_cast<int>(i), w);
+                    return;
+                }
+            }
+            finish<false>(rp, w, static_cast<int>(i), w);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = i + e < end ? one(static_cast<int>(i) + e) : 0.0f;
+    }
+};
+
+// The first of n shares whose running sum (from `before` on) exceeds t, and
+// the sum before it; the last share with any mass where none does.
+__device__ __forceinline__ int pick(const double* share, int n, double t, double& before) {
+    int found = 0;
+    double run = before;
+    for (int k = 0; k < n; ++k) {
+        if (!(share[k] > 0.0)) continue;
+        found = k;
+        before = run;
+        run += share[k];
+        if (run > t) break;
+    }
+    return found;
+}
+
+// The sum of the weights of columns [begin, end), begin a multiple of kStep,
+// by one warp; every lane gets its own part.
+template <bool kSub, typename P, typename Q>
+__device__ __forceinline__ double lane_sum(const Weights<P, Q>& wt, int begin, int end, int lane) {
+    PairSum sum;
+    if (wt.vec) {
+        constexpr int kUnroll = 4;
+        int i = begin + 8 * lane;
+        for (; i + (kUnroll - 1) * kStep + 8 <= end; i += kUnroll * kStep) {
+            Raw8<P> rp[kUnroll];
+            Raw8<typename std::conditional<kSub, Q, P>::type> rq[kSub ? kUnroll : 1];
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                rp[k].load(wt.p + i + k * kStep);
+                if constexpr (kSub) rq[k].load(wt.q + i + k * kStep);
+            }
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                float qv[8], w[8];
+                if constexpr (kSub) rq[k].unpack(qv);
+                wt.template finish<kSub>(rp[k], qv, i + k * kStep, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum.add(w[e]);
+            }
+        }
+        for (; i < end; i += kStep) {
+            if (i + 8 <= end) {
+                Raw8<P> rp;
+                float qv[8], w[8];
+                rp.load(wt.p + i);
+                if constexpr (kSub) {
+                    Raw8<Q> rq;
+                    rq.load(wt.q + i);
+                    rq.unpack(qv);
+                }
+                wt.template finish<kSub>(rp, qv, i, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum.add(w[e]);
+            } else {
+                for (int e = i; e < end; ++e) sum.add(wt.one(e));
+            }
+        }
+    } else {
+        // rows off 16-byte boundaries: single elements, 8 in flight
+        int i = begin + lane;
+        for (; i + 7 * 32 < end; i += kStep) {
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = wt.one(i + 32 * e);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum.add(w[e]);
+        }
+        for (; i < end; i += 32) sum.add(wt.one(i));
+    }
+    return sum.value();
+}
+
+template <typename P, typename Q>
+__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams a) {
+    constexpr bool kDraft = !std::is_same<Q, NoDraft>::value;
+    __shared__ double s_cta[2][kMaxCluster];  // the CTAs' totals, by attempt
+    __shared__ double s_warp[kVerifyWarps];   // this CTA's warps' totals
+    __shared__ double s_scan[kVerifyWarps];
+    __shared__ int s_first, s_last;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int csize = a.cluster;
+    const int rank = csize > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int64_t b = blockIdx.x / csize;
+    const int64_t first = a.cu[b];
+    int64_t count = static_cast<int64_t>(a.cu[b + 1]) - first;
+    count = count < 0 ? 0 : count > a.max_drafts ? a.max_drafts : count;
+    int64_t* const out = a.out_tokens + b * (static_cast<int64_t>(a.max_drafts) + 1);
+    // rows outside the arrays: nothing is read (the same for the whole cluster)
+    if (first < 0 || first + count > a.draft_rows || first + b + count >= a.target_rows) {
+        if (rank == 0) {
+            for (int k = tid; k <= a.max_drafts; k += kVerifyThreads) out[k] = -1;
+            if (tid == 0) a.out_accepted[b] = -1;
+        }
+        return;
+    }
+    const P* const target = static_cast<const P*>(a.target) + (first + b) * a.target_stride;
+
+    // The accepted drafts, by every warp for itself. u q < p is decided
+    // exactly: the product of two fp32 numbers fits fp64.
+    int accepted = 0;
+    for (int base = 0; base < count; base += 32) {
+        const int j = base + lane;
+        bool ok = false;
+        if (j < count) {
+            const int64_t x = a.tokens[first + j];
+            if (x >= 0 && x < a.vocab) {
+                const float p = to_f(target[j * a.target_stride + x]);
+                float q = 1.0f;
+                if constexpr (kDraft)
+                    q = to_f(static_cast<const Q*>(a.draft)[(first + j) * a.draft_stride + x]);
+                ok = static_cast<double>(a.accept_u[first + j]) * static_cast<double>(q) < static_cast<double>(p);
+            }
+        }
+        const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+        const int n = mask == 0xffffffffu ? 32 : __ffs(~mask) - 1;
+        accepted += n;
+        if (n < 32) break;
+    }
+    const bool whole = accepted == count;
+    if (rank == 0) {
+        for (int k = tid; k <= a.max_drafts; k += kVerifyThreads)
+            if (k != accepted) out[k] = k < accepted ? a.tokens[first + k] : -1;
+        if (tid == 0) a.out_accepted[b] = accepted;
+    }
+
+    Weights<P, Q> wt;
+    wt.p = target + accepted * a.target_stride;
+    wt.q = nullptr;
+    wt.without = -1;
+    wt.vec = (reinterpret_cast<uintptr_t>(wt.p) & 15) == 0;
+    if (!whole) {
+        if constexpr (kDraft) {
+            wt.q = static_cast<const Q*>(a.draft) + (first + accepted) * a.draft_stride;
+            wt.vec = wt.vec && (reinterpret_cast<uintptr_t>(wt.q) & 15) == 0;
+        } else {
+            const int64_t x = a.tokens[first + accepted];
+            if (x >= 0 && x < a.vocab) wt.without = static_cast<int>(x);
+        }
+    }
+
+    // Each warp of the cluster owns `part` consecutive columns.
+    const int parts = csize * kVerifyWarps;
+    const int part = static_cast<int>(ceil_div(ceil_div(a.vocab, parts), kStep) * kStep);
+    double total = 0.0;
+    int used = 0;  // the attempt whose totals count
+    for (int attempt = 0; attempt < 2; ++attempt) {
+        const int64_t begin64 = static_cast<int64_t>(rank * kVerifyWarps + warp) * part;
+        const int begin = begin64 < a.vocab ? static_cast<int>(begin64) : a.vocab;
+        const int end = begin64 + part < a.vocab ? static_cast<int>(begin64 + part) : a.vocab;
+        double sum = 0.0;
+        if (begin < end) {
+            if (kDraft && wt.q) {
+                if constexpr (kDraft) sum = lane_sum<true>(wt, begin, end, lane);
+            } else {
+                sum = lane_sum<false>(wt, begin, end, lane);
+            }
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) s_warp[warp] = sum;
+        __syncthreads();
+        if (tid < csize) {
+            double cta = 0.0;
+            for (int w = 0; w < kVerifyWarps; ++w) cta += s_warp[w];
+            if (csize > 1)
+                store_remote(&s_cta[attempt][rank], tid, static_cast<uint64_t>(__double_as_longlong(cta)));
+            else
+                s_cta[attempt][0] = cta;
+        }
+        if (csize > 1) cluster_sync_all();
+        else __syncthreads();
+        total = 0.0;
+        for (int c = 0; c < csize; ++c) total += s_cta[attempt][c];
+        // A refused draft whose p never exceeds its q (rounded
+        // probabilities) draws from the target's own row.
+        if (total > 0.0 || whole || attempt == 1) break;
+        used = 1;
+        wt.q = nullptr;
+        wt.without = -1;
+        wt.vec = (reinterpret_cast<uintptr_t>(wt.p) & 15) == 0;
+    }
+    if (!(total > 0.0)) {  // no mass anywhere
+        if (rank == 0 && tid == 0) out[accepted] = -1;
+        return;
+    }
+
+    // The share that holds the drawn column: the first whose running sum
+    // exceeds t; the last one with any mass where rounding (or u >= 1)
+    // leaves none.
+    const double t = static_cast<double>(a.sample_u[b]) * total;
+    double before = 0.0;
+    const int cta = pick(s_cta[used], csize, t, before);
+    if (rank != cta) return;
+    const int w = pick(s_warp, kVerifyWarps, t, before);
+    const int begin = (rank * kVerifyWarps + w) * part;
+    const int end = begin + part < a.vocab ? begin + part : a.vocab;
+    int last = -1;  // the last column with a weight that this thread saw
+    for (int64_t at = begin; at < end; at += 8 * kVerifyThreads) {
+        const int64_t i = at + 8 * tid;
+        float v[8];
+        wt.load(i, end, v);
+        double sum = 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            sum += static_cast<double>(v[e]);
+            if (v[e] > 0.0f) last = static_cast<int>(i) + e;
+        }
+        const double scan = warp_scan_inclusive(sum, lane);
+        if (lane == 31) s_scan[warp] = scan;
+        if (tid == 0) s_first = INT_MAX;
+        __syncthreads();
+        double lower = before;
+        for (int k = 0; k < warp; ++k) lower += s_scan[k];
+        if (sum > 0.0 && lower + scan > t) atomicMin(&s_first, tid);
+        __syncthreads();
+        if (s_first == tid) {
+            double run = lower + (scan - sum);
+            int col = last;  // in this thread's eight, as its sum is positive
+            for (int e = 0; e < 8; ++e) {
+                run += static_cast<double>(v[e]);
+                if (v[e] > 0.0f && run > t) {
+                    col = static_cast<int>(i) + e;
+                    break;
+                }
+            }
+            out[accepted] = col;
+        }
+        if (s_first != INT_MAX) return;
+        for (int k = 0; k < kVerifyWarps; ++k) before += s_scan[k];
+        __syncthreads();
+    }
+    // The share's sum, added in another order, fell just short of t.
+    if (tid == 0) s_last = -1;
+    __syncthreads();
+    atomicMax(&s_last, last);
+    __syncthreads();
+    if (tid == 0) out[accepted] = s_last;
+}
+
+using VerifyKernel = void (*)(VerifyParams);
+
+template <typename P> VerifyKernel verify_kernel_for(bool draft, drs_dtype t) {
+    if (!draft) return verify_kernel<P, NoDraft>;
+    return with_dtype(t, [](auto q) -> VerifyKernel { return verify_kernel<P, decltype(q)>; });
+}
+
+}  // namespace
+}  // namespace drs
+
+extern "C" drs_status drs_verify_drafts(const void* target, drs_dtype target_dtype, int64_t target_rows,
+                                        int64_t target_stride, const void* draft, drs_dtype draft_dtype,
+                                        int64_t draft_rows, int64_t draft_stride, int64_t vocab,
+                                        const int64_t* draft_tokens, const int32_t* cu_drafts, int64_t requests,
+                                        int32_t max_drafts, const float* accept_u, const float* sample_u,
+                                        int64_t* out_tokens, int32_t* out_accepted, void* stream) {
+    using namespace drs;
+    if (requests < 0 || max_drafts < 0 || target_rows < 0 || draft_rows < 0) return DRS_ERR_INVALID_ARG;
+    if (!dtype_ok(target_dtype) || (draft && !dtype_ok(draft_dtype))) return DRS_ERR_INVALID_ARG;
+    if (vocab < 1 || target_stride < vocab || (draft && draft_stride < vocab)) return DRS_ERR_INVALID_ARG;
+    if (vocab > DRS_MAX_VOCAB || requests > INT32_MAX / kMaxCluster) return DRS_ERR_UNSUPPORTED;
+    if (requests == 0) return DRS_OK;
+    if (!target || !cu_drafts || !sample_u || !out_tokens || !out_accepted) return DRS_ERR_INVALID_ARG;
+    if (draft_rows > 0 && (!draft_tokens || !accept_u)) return DRS_ERR_INVALID_ARG;
+    if (!aligned(target, dtype_bytes(target_dtype)) || (draft && !aligned(draft, dtype_bytes(draft_dtype))) ||
+        !aligned(draft_tokens, 8) || !aligned(out_tokens, 8) || !aligned(cu_drafts, 4) || !aligned(accept_u, 4) ||
+        !aligned(sample_u, 4) || !aligned(out_accepted, 4))
+        return DRS_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    if (sms <= 0) return DRS_ERR_CUDA;
+
+    VerifyParams a{};
+    a.target = target;
+    a.draft = draft;
+    a.tokens = draft_tokens;
+    a.cu = cu_drafts;
+    a.accept_u = accept_u;
+    a.sample_u = sample_u;
+    a.out_tokens = out_tokens;
+    a.out_accepted = out_accepted;
+    a.target_rows = target_rows;
+    a.target_stride = target_stride;
+    a.draft_rows = draft_rows;
+    a.draft_stride = draft_stride;
+    a.vocab = static_cast<int32_t>(vocab);
+    a.max_drafts = max_drafts;
+    // CTAs per request: 8192 columns (16 per thread) each at least, up to 8,
+    // or 16 where 8 would leave SMs idle.
+    int cluster = 1;
+    const int most = requests * 8 < sms ? kMaxCluster : 8;
+    while (cluster < most && vocab > 8192 * cluster) cluster *= 2;
+    a.cluster = cluster;
+
+    const bool has_draft = draft != nullptr;
+    const VerifyKernel kernel = with_dtype(target_dtype, [&](auto p) -> VerifyKernel {
+        return verify_kernel_for<decltype(p)>(has_draft, draft_dtype);
+    });
+    if (cluster > 8 &&
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed,
+                             1) != cudaSuccess)
+        return DRS_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(requests * cluster));
+    cfg.blockDim = dim3(kVerifyThreads);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, a));
+}
