@@ -21,6 +21,7 @@ map_slots, embed_tokens, embed_tokens_grad.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -297,18 +298,32 @@ def drs_scaled_logits(logits, temp: float, out, stream=None):
 # lengths of the arrays (ValueError). Sizes, strides and alignment are the
 # library's own checks (DrsError).
 
+_dtype_codes = {}
+
+
 def _dtype_code(t, name: str) -> int:
-    import torch
-    code = {torch.float32: DRS_DTYPE_FP32, torch.bfloat16: DRS_DTYPE_BF16,
-            torch.float16: DRS_DTYPE_FP16}.get(t.dtype)
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float32: DRS_DTYPE_FP32, torch.bfloat16: DRS_DTYPE_BF16,
+                             torch.float16: DRS_DTYPE_FP16})
+    code = _dtype_codes.get(t.dtype)
     if code is None:
         raise ValueError(f"{name}: fp32, bf16 or fp16 expected, got {t.dtype}")
     return code
 
 
+def _raw_stream(stream, device) -> int:
+    """The stream of a call: torch.cuda.current_stream() alone takes 3 us,
+    more than a launch."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _need(t, name: str, dtype, shape, device):
     """A contiguous tensor of this type and shape on this device."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype} {tuple(shape)} on {device} expected, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
@@ -316,13 +331,13 @@ def _need(t, name: str, dtype, shape, device):
 def _need_rows(t, name: str, device=None):
     """A 2-D tensor with unit column stride (any row stride) on a GPU;
     returns the row stride."""
-    if t.dim() != 2 or t.device.type != "cuda" or (device is not None and t.device != device):
+    if t.dim() != 2 or not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name}: 2-D on {device or 'a CUDA device'} expected, got {t.dim()}-D on {t.device}")
     rows, columns = t.shape
     step, unit = t.stride()
     if rows == 0 or columns == 0:
         return columns
-    if columns > 1 and unit != 1:
+    if unit != 1 and columns > 1:
         raise ValueError(f"{name}: unit column stride expected, got strides {t.stride()}")
     return step if rows > 1 else max(step, columns)
 
@@ -357,7 +372,7 @@ def drs_verify_drafts(target, draft, draft_tokens, cu_drafts, accept_u, sample_u
                                   draft_stride, vocab, draft_tokens.data_ptr(), cu_drafts.data_ptr(),
                                   requests, out_tokens.shape[1] - 1, accept_u.data_ptr(),
                                   sample_u.data_ptr(), out_tokens.data_ptr(), out_accepted.data_ptr(),
-                                  _stream(stream))
+                                  _raw_stream(stream, dev))
     _check(st, "drs_verify_drafts")
 
 
@@ -389,7 +404,7 @@ def drs_map_slots(lens, new_lens, held, block_table, block_size: int, free_ring,
                               free_ring.data_ptr(), free_ring.numel(), ring_state.data_ptr(), capacity,
                               out_cu.data_ptr(), out_request.data_ptr(), out_position.data_ptr(),
                               out_slot.data_ptr(), out_held.data_ptr(), out_ring_state.data_ptr(),
-                              out_lacking.data_ptr(), _stream(stream))
+                              out_lacking.data_ptr(), _raw_stream(stream, dev))
     _check(st, "drs_map_slots")
 
 
@@ -412,7 +427,7 @@ def drs_embed_tokens(table, ids, scale: float, out, stream=None):
         raise ValueError(f"out: {table.dtype} {(ids.numel(), width)} expected, got {out.dtype} {tuple(out.shape)}")
     st = load().drs_embed_tokens(table.data_ptr(), _dtype_code(table, "table"), vocab, width, table_stride,
                                  ids.data_ptr(), bits, ids.numel(), scale, out.data_ptr(), out_stride,
-                                 _stream(stream))
+                                 _raw_stream(stream, table.device))
     _check(st, "drs_embed_tokens")
 
 
@@ -435,7 +450,7 @@ def drs_embed_tokens_grad(grad_out, ids, scale: float, accumulate: bool, grad_ta
                                       grad_stride, ids.data_ptr(), bits, scale, 1 if accumulate else 0,
                                       grad_table.data_ptr(), _dtype_code(grad_table, "grad_table"), vocab,
                                       table_stride, None if workspace is None else workspace.data_ptr(),
-                                      ws_bytes, _stream(stream))
+                                      ws_bytes, _raw_stream(stream, grad_out.device))
     _check(st, "drs_embed_tokens_grad")
 
 
@@ -630,9 +645,10 @@ def stash_converged_logprobs(logits, canvas_len: int, src, slots, keep, valid, t
 def _allocate_on(stream):
     """Where a call on `stream` allocates: the caching allocator hands memory
     on in the order of the stream that it was allocated on."""
-    import contextlib
+    if stream is None:
+        return contextlib.nullcontext()
     import torch
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return torch.cuda.stream(stream)
 
 
 def verify_drafts(target_probs, draft_tokens, cu_drafts, accept_u, sample_u, max_drafts: int,

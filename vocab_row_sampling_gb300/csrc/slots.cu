@@ -1,16 +1,17 @@
 // slots.cu -- block tables and slot maps from request lengths
 // (drs_map_slots).
 //
-// One launch of one thread-block cluster: the call is a few prefix sums over
-// the requests and one look-up per token, bound by latency, and a cluster's
-// barriers order its phases without a second launch or a workspace.
+// The requests are the work of one thread-block cluster: a few prefix sums,
+// bound by latency, whose phases a cluster's barriers order without further
+// launches or a workspace.
 //   1. every CTA sums its share of the requests: new tokens, blocks to take
 //      from the ring of free blocks, blocks to give back; the CTAs exchange
 //      their sums through distributed shared memory;
 //   2. every CTA writes its requests' offsets and counts and moves their
-//      blocks between the table and the ring;
-//   3. every CTA finds the request of its share of the tokens by binary
-//      search and looks up its block.
+//      blocks between the table and the ring.
+// The tokens then find their request in the offsets and look up their block,
+// a warp taking a run of them: in the same launch where there are few, in a
+// launch over all SMs (a programmatic dependent one) where there are many.
 // All sums are 64-bit integers in request order, so the blocks that a
 // request gets do not depend on how the work is split.
 #include <climits>
@@ -20,7 +21,7 @@
 namespace drs {
 namespace {
 
-constexpr int kSlotThreads = 1024;
+constexpr int kSlotThreads = 512;
 constexpr int kSlotWarps = kSlotThreads / 32;
 constexpr int kSlotCluster = 16;
 
@@ -42,6 +43,12 @@ struct SlotParams {
     int32_t requests, max_blocks, block, cluster;
 };
 
+// 64-bit divisions take about 100 instructions; almost every length fits 32.
+__device__ __forceinline__ int64_t quotient(int64_t x, int32_t d) {
+    if (static_cast<uint64_t>(x) >> 32) return x / d;
+    return static_cast<uint32_t>(x) / static_cast<uint32_t>(d);
+}
+
 struct Sums {
     int64_t tokens, take, give;
     __device__ __forceinline__ Sums& operator+=(const Sums& o) {
@@ -62,7 +69,7 @@ struct Request {
         r.len = max(a.lens[b], 0);
         r.fresh = max(a.new_lens[b], 0);
         r.held = min(max(a.held[b], 0), a.max_blocks);
-        r.want = (r.len + r.fresh + a.block - 1) / a.block;
+        r.want = quotient(r.len + r.fresh + a.block - 1, a.block);
         r.need = static_cast<int32_t>(min(r.want, static_cast<int64_t>(a.max_blocks)));
         return r;
     }
@@ -71,13 +78,91 @@ struct Request {
     }
 };
 
-// A place of the ring, for any 64-bit counter.
-__device__ __forceinline__ int64_t ring_place(int64_t counter, int64_t size) {
-    return static_cast<int64_t>(static_cast<uint64_t>(counter) % static_cast<uint64_t>(size));
+// The place `offset` entries after `place` in the ring. Offsets are below
+// the ring's size where its counters are consistent.
+__device__ __forceinline__ int64_t ring_place(int64_t place, int64_t offset, int64_t size) {
+    int64_t at = place + offset;
+    if (at >= size) {
+        at -= size;
+        if (at >= size) at %= size;
+    }
+    return at;
 }
 
-__global__ void __launch_bounds__(kSlotThreads) slots_kernel(const SlotParams a) {
+constexpr int kOwnMoves = 4;  // blocks of a request that its thread moves by itself
+
+// The tokens of warp `w` of `warps`: a run of groups of 32. What the cluster
+// wrote is read from L2.
+__device__ __forceinline__ void map_tokens(const SlotParams& a, int w, int warps, int lane) {
+    const int groups = static_cast<int>(ceil_div(a.capacity, 32));
+    const int per = groups / warps, rest = groups % warps;
+    const int g0 = w * per + min(w, rest), g1 = g0 + per + (w < rest);
+    if (g0 >= g1) return;
+    const int32_t total = __ldcg(a.out_cu + a.requests);
+    // the request of the first token, the last b with out_cu[b] <= t: each
+    // step takes 32 probes
+    int b = 0;
+    if (static_cast<int64_t>(g0) * 32 < total) {
+        for (int n = a.requests; n > 1;) {
+            const int step = (n + 31) / 32;
+            const int at = lane * step;
+            const bool below = at < n && __ldcg(a.out_cu + b + at) <= g0 * 32;
+            const int hit = __popc(__ballot_sync(0xffffffffu, below)) - 1;  // lane 0 is below
+            b += hit * step;
+            n = min(step, n - hit * step);
+        }
+    }
+    int32_t start = __ldcg(a.out_cu + b);
+    for (int g = g0; g < g1; ++g) {
+        const int64_t t = static_cast<int64_t>(g) * 32 + lane;
+        int32_t request = -1, position = 0;
+        int64_t slot = -1;
+        if (static_cast<int64_t>(g) * 32 < total) {
+            // the next 32 offsets; a token's request follows from how many
+            // of them are not above it
+            const int32_t next = b + 1 + lane <= a.requests ? __ldcg(a.out_cu + b + 1 + lane) : INT_MAX;
+            int n = 0;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1)
+                if (__shfl_sync(0xffffffffu, next, n + s - 1) <= t) n += s;
+            request = b + n;
+            int32_t first = __shfl_sync(0xffffffffu, next, n > 0 ? n - 1 : 0);
+            if (n == 0) first = start;
+            if (__shfl_sync(0xffffffffu, next, 31) <= t && t < total) {
+                // over 31 requests without tokens between two tokens
+                int below = request, above = a.requests;
+                while (above - below > 1) {
+                    const int mid = below + (above - below) / 2;
+                    if (__ldcg(a.out_cu + mid) <= t) below = mid;
+                    else above = mid;
+                }
+                request = below;
+                first = __ldcg(a.out_cu + below);
+            }
+            if (t < total) {
+                const int64_t at = max(a.lens[request], 0) + (t - first);
+                position = static_cast<int32_t>(min(at, static_cast<int64_t>(INT_MAX)));
+                const int64_t col = quotient(at, a.block);
+                if (col < __ldcg(a.out_held + request))
+                    slot = static_cast<int64_t>(__ldcg(a.table + request * a.table_stride + col)) * a.block +
+                           (at - col * a.block);
+            } else {
+                request = -1;
+            }
+            b = max(__shfl_sync(0xffffffffu, request, 31), b);
+            start = __shfl_sync(0xffffffffu, first, 31);
+        }
+        if (t < a.capacity) {
+            a.out_request[t] = request;
+            a.out_position[t] = position;
+            a.out_slot[t] = slot;
+        }
+    }
+}
+
+template <bool kTokens> __global__ void __launch_bounds__(kSlotThreads) slots_kernel(const SlotParams a) {
     __shared__ Sums s_warp[kSlotWarps];
+    __shared__ Sums s_all;
     __shared__ int64_t s_cta[kSlotCluster][3];  // every CTA's sums
     __shared__ int64_t s_end[kSlotCluster][2];  // blocks taken and lacking, by CTA
     __shared__ unsigned long long s_taken, s_lacking;
@@ -92,6 +177,7 @@ __global__ void __launch_bounds__(kSlotThreads) slots_kernel(const SlotParams a)
     const int b0 = min(lo + static_cast<int64_t>(tid) * run, static_cast<int64_t>(hi));
     const int b1 = min(b0 + run, hi);
 
+    if constexpr (!kTokens) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t head = a.state[0], tail = a.state[1];
     int64_t avail = tail - head;
     avail = avail < 0 ? 0 : avail > a.ring_size ? a.ring_size : avail;
@@ -103,31 +189,48 @@ __global__ void __launch_bounds__(kSlotThreads) slots_kernel(const SlotParams a)
     Sums at{warp_scan_inclusive(mine.tokens, lane), warp_scan_inclusive(mine.take, lane),
             warp_scan_inclusive(mine.give, lane)};
     if (lane == 31) s_warp[warp] = at;
-    __syncthreads();
     at.tokens -= mine.tokens, at.take -= mine.take, at.give -= mine.give;
-    Sums all{0, 0, 0};
-    for (int w = 0; w < kSlotWarps; ++w) {
-        if (w < warp) at += s_warp[w];
-        all += s_warp[w];
-    }
-    if (tid < csize) {
-        const int64_t v[3] = {all.tokens, all.take, all.give};
-        for (int i = 0; i < 3; ++i) {
-            if (csize > 1) store_remote(&s_cta[rank][i], tid, static_cast<uint64_t>(v[i]));
-            else s_cta[0][i] = v[i];
+    __syncthreads();
+    if (warp == 0) {  // the warps' sums become the sums before them
+        const Sums own = lane < kSlotWarps ? s_warp[lane] : Sums{0, 0, 0};
+        const Sums upto{warp_scan_inclusive(own.tokens, lane), warp_scan_inclusive(own.take, lane),
+                        warp_scan_inclusive(own.give, lane)};
+        if (lane < kSlotWarps) s_warp[lane] = Sums{upto.tokens - own.tokens, upto.take - own.take, upto.give - own.give};
+        if (csize > 1) {
+            const Sums all{__shfl_sync(0xffffffffu, upto.tokens, 31), __shfl_sync(0xffffffffu, upto.take, 31),
+                           __shfl_sync(0xffffffffu, upto.give, 31)};
+            if (lane < csize) {
+                store_remote(&s_cta[rank][0], lane, static_cast<uint64_t>(all.tokens));
+                store_remote(&s_cta[rank][1], lane, static_cast<uint64_t>(all.take));
+                store_remote(&s_cta[rank][2], lane, static_cast<uint64_t>(all.give));
+            }
+        } else if (lane == 31) {
+            s_all = upto;
         }
     }
-    if (csize > 1) cluster_sync_all();
-    else __syncthreads();
-    all = Sums{0, 0, 0};
-    for (int c = 0; c < csize; ++c) {
-        const Sums s{s_cta[c][0], s_cta[c][1], s_cta[c][2]};
-        if (c < rank) at += s;
-        all += s;
+    if (csize > 1) {
+        cluster_sync_all();
+        if (warp == 0) {  // and the sums of the CTAs before this one
+            const Sums own = lane < csize ? Sums{s_cta[lane][0], s_cta[lane][1], s_cta[lane][2]} : Sums{0, 0, 0};
+            const Sums upto{warp_scan_inclusive(own.tokens, lane), warp_scan_inclusive(own.take, lane),
+                            warp_scan_inclusive(own.give, lane)};
+            Sums before{__shfl_up_sync(0xffffffffu, upto.tokens, 1), __shfl_up_sync(0xffffffffu, upto.take, 1),
+                        __shfl_up_sync(0xffffffffu, upto.give, 1)};
+            if (lane == 31) s_all = upto;
+            if (lane == 0) before = Sums{0, 0, 0};
+            const Sums add{__shfl_sync(0xffffffffu, before.tokens, rank), __shfl_sync(0xffffffffu, before.take, rank),
+                           __shfl_sync(0xffffffffu, before.give, rank)};
+            if (lane < kSlotWarps) s_warp[lane] += add;
+        }
     }
+    __syncthreads();
+    at += s_warp[warp];
+    const Sums all = s_all;
 
     // 2. the requests' outputs and the moves of blocks. Warps stay whole:
     // long moves are made by all lanes.
+    const int64_t head_at = static_cast<int64_t>(static_cast<uint64_t>(head) % static_cast<uint64_t>(a.ring_size));
+    const int64_t tail_at = static_cast<int64_t>(static_cast<uint64_t>(tail) % static_cast<uint64_t>(a.ring_size));
     int64_t taken = 0, lacking = 0;
     for (int k = 0; k < run; ++k) {
         const int b = b0 + k;
@@ -145,24 +248,38 @@ __global__ void __launch_bounds__(kSlotThreads) slots_kernel(const SlotParams a)
             a.out_cu[b] = static_cast<int32_t>(min(at.tokens, a.capacity));
             a.out_held[b] = now;
         }
-        const int32_t moves = have ? max(now - r.held, 0) + max(r.held - r.need, 0) : 0;
-        for (uint32_t todo = __ballot_sync(0xffffffffu, moves > 0); todo; todo &= todo - 1) {
+        // blocks taken: ring -> columns [held, now); given: columns [need, held) -> ring
+        const bool takes = now > r.held;
+        const int32_t moves = have ? takes ? now - r.held : max(r.held - r.need, 0) : 0;
+        const int32_t col = takes ? r.held : r.need;
+        const int64_t from = takes ? at.take : at.give;
+        int32_t* const row = a.table + b * a.table_stride + col;
+        int32_t ids[kOwnMoves];
+#pragma unroll
+        for (int i = 0; i < kOwnMoves; ++i)
+            if (i < moves) ids[i] = takes ? a.ring[ring_place(head_at, from + i, a.ring_size)] : row[i];
+#pragma unroll
+        for (int i = 0; i < kOwnMoves; ++i)
+            if (i < moves) (takes ? row[i] : a.ring[ring_place(tail_at, from + i, a.ring_size)]) = ids[i];
+        for (uint32_t todo = __ballot_sync(0xffffffffu, moves > kOwnMoves); todo; todo &= todo - 1) {
             const int src = __ffs(todo) - 1;
+            const bool take = __shfl_sync(0xffffffffu, static_cast<int>(takes), src);
             const int32_t n = __shfl_sync(0xffffffffu, moves, src);
-            const int32_t held = __shfl_sync(0xffffffffu, r.held, src);
-            const int32_t need = __shfl_sync(0xffffffffu, r.need, src);
-            const int64_t from = head + __shfl_sync(0xffffffffu, at.take, src);
-            const int64_t to = tail + __shfl_sync(0xffffffffu, at.give, src);
-            int32_t* const row = a.table + __shfl_sync(0xffffffffu, b, src) * a.table_stride;
-            for (int32_t i = lane; i < n; i += 32) {
-                if (need > held) row[held + i] = a.ring[ring_place(from + i, a.ring_size)];
-                else a.ring[ring_place(to + i, a.ring_size)] = row[need + i];
+            const int64_t base = __shfl_sync(0xffffffffu, from, src);
+            int32_t* const there = a.table + __shfl_sync(0xffffffffu, b, src) * a.table_stride +
+                                   __shfl_sync(0xffffffffu, col, src);
+            for (int32_t i = kOwnMoves + lane; i < n; i += 32) {
+                if (take) there[i] = a.ring[ring_place(head_at, base + i, a.ring_size)];
+                else a.ring[ring_place(tail_at, base + i, a.ring_size)] = there[i];
             }
         }
         at += s;
     }
-    if (taken) atomicAdd(&s_taken, static_cast<unsigned long long>(taken));
-    if (lacking) atomicAdd(&s_lacking, static_cast<unsigned long long>(lacking));
+    taken = warp_sum(taken), lacking = warp_sum(lacking);
+    if (lane == 0) {
+        if (taken) atomicAdd(&s_taken, static_cast<unsigned long long>(taken));
+        if (lacking) atomicAdd(&s_lacking, static_cast<unsigned long long>(lacking));
+    }
     if (rank == 0 && tid == 0) a.out_cu[a.requests] = static_cast<int32_t>(min(all.tokens, a.capacity));
     __syncthreads();
     if (tid < 2) {
@@ -179,31 +296,15 @@ __global__ void __launch_bounds__(kSlotThreads) slots_kernel(const SlotParams a)
         a.out_state[1] = tail + all.give;
         *a.out_lacking = static_cast<int32_t>(min(sum[1], static_cast<int64_t>(INT_MAX)));
     }
+    if constexpr (kTokens) map_tokens(a, rank * kSlotWarps + warp, csize * kSlotWarps, lane);
+}
 
-    // 3. the tokens. What the cluster wrote is read from L2.
-    const int64_t total = min(all.tokens, a.capacity);
-    const int64_t step = static_cast<int64_t>(csize) * kSlotThreads;
-    for (int64_t t = static_cast<int64_t>(rank) * kSlotThreads + tid; t < a.capacity; t += step) {
-        int32_t request = -1, position = 0;
-        int64_t slot = -1;
-        if (t < total) {
-            int below = 0, above = a.requests;  // out_cu[below] <= t < out_cu[above]
-            while (above - below > 1) {
-                const int mid = below + (above - below) / 2;
-                if (__ldcg(a.out_cu + mid) <= t) below = mid;
-                else above = mid;
-            }
-            request = below;
-            const int64_t at_token = max(a.lens[below], 0) + (t - __ldcg(a.out_cu + below));
-            position = static_cast<int32_t>(min(at_token, static_cast<int64_t>(INT_MAX)));
-            const int64_t col = at_token / a.block;
-            if (col < __ldcg(a.out_held + below))
-                slot = static_cast<int64_t>(__ldcg(a.table + below * a.table_stride + col)) * a.block + at_token % a.block;
-        }
-        a.out_request[t] = request;
-        a.out_position[t] = position;
-        a.out_slot[t] = slot;
-    }
+constexpr int kTokenThreads = 256;
+constexpr int kTokenWarps = kTokenThreads / 32;
+
+__global__ void __launch_bounds__(kTokenThreads) slot_tokens_kernel(const SlotParams a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    map_tokens(a, blockIdx.x * kTokenWarps + (threadIdx.x >> 5), gridDim.x * kTokenWarps, threadIdx.x & 31);
 }
 
 }  // namespace
@@ -253,13 +354,16 @@ extern "C" drs_status drs_map_slots(const int32_t* lens, const int32_t* new_lens
     a.requests = static_cast<int32_t>(requests);
     a.max_blocks = max_blocks;
     a.block = block_size;
-    const int64_t work = capacity > requests ? capacity : requests;
+    // Few tokens: one launch, 32 of them per warp until the cluster is full.
+    // Many: the cluster for the requests, then a launch for the tokens.
+    const bool apart = capacity > kSlotCluster * kSlotThreads;
+    const int64_t work = !apart && capacity > requests ? capacity : requests;
     int cluster = 1;
     while (cluster < kSlotCluster && work > static_cast<int64_t>(cluster) * kSlotThreads) cluster *= 2;
     a.cluster = cluster;
-    if (cluster > 8 &&
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(slots_kernel),
-                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    const auto kernel = apart ? slots_kernel<false> : slots_kernel<true>;
+    if (cluster > 8 && cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                            cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return DRS_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(cluster));
@@ -272,5 +376,20 @@ extern "C" drs_status drs_map_slots(const int32_t* lens, const int32_t* new_lens
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cuda_status(cudaLaunchKernelEx(&cfg, slots_kernel, a));
+    if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return DRS_ERR_CUDA;
+    if (!apart) return DRS_OK;
+    const int sms = sm_count();
+    if (sms <= 0) return DRS_ERR_CUDA;
+    // up to 8 CTAs per SM, a group of 32 tokens per warp at least
+    const int64_t blocks = ceil_div(capacity, 32 * kTokenWarps);
+    cudaLaunchConfig_t next{};
+    next.gridDim = dim3(static_cast<unsigned>(blocks < sms * 8 ? blocks : sms * 8));
+    next.blockDim = dim3(kTokenThreads);
+    next.stream = cfg.stream;
+    cudaLaunchAttribute dependent[1];
+    dependent[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    dependent[0].val.programmaticStreamSerializationAllowed = 1;
+    next.attrs = dependent;
+    next.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&next, slot_tokens_kernel, a));
 }

@@ -90,6 +90,65 @@ template <typename T> __device__ __forceinline__ T warp_sum(T v) {
     return v;
 }
 
+// ------------------------------------------------------------- pairs
+
+// A number as the sum s + c of two fp32, |c| at most half a step of s
+// (about 48 bits). fp64 would hold more, but this GPU issues one fp64
+// instruction per SM in 16 cycles, and these take one cycle each.
+struct Pair {
+    float s, c;
+};
+
+// s + c == a + b exactly (Knuth's two-sum).
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+    const float s = a + b;
+    const float z = s - a;
+    return Pair{s, (a - (s - z)) + (b - z)};
+}
+
+__device__ __forceinline__ Pair normalized(float s, float c) {
+    const float h = s + c;
+    return Pair{h, c - (h - s)};
+}
+
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+    const Pair t = two_sum(a.s, b.s);
+    return normalized(t.s, t.c + (a.c + b.c));
+}
+
+__device__ __forceinline__ Pair operator*(float u, Pair a) {
+    const float h = u * a.s;
+    return normalized(h, fmaf(u, a.s, -h) + u * a.c);
+}
+
+__device__ __forceinline__ bool operator>(Pair a, Pair b) { return (a.s - b.s) + (a.c - b.c) > 0.0f; }
+
+__device__ __forceinline__ Pair shfl_up(Pair v, int o) {
+    return Pair{__shfl_up_sync(0xffffffffu, v.s, o), __shfl_up_sync(0xffffffffu, v.c, o)};
+}
+
+__device__ __forceinline__ Pair shfl(Pair v, int lane) {
+    return Pair{__shfl_sync(0xffffffffu, v.s, lane), __shfl_sync(0xffffffffu, v.c, lane)};
+}
+
+// Inclusive scan over the first n lanes (n a power of two).
+__device__ __forceinline__ Pair warp_scan_pair(Pair v, int lane, int n = 32) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        if (o >= n) break;
+        const Pair u = shfl_up(v, o);
+        if (lane >= o) v = u + v;
+    }
+    return v;
+}
+
+__device__ __forceinline__ Pair warp_sum_pair(Pair v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v = v + Pair{__shfl_xor_sync(0xffffffffu, v.s, o), __shfl_xor_sync(0xffffffffu, v.c, o)};
+    return v;
+}
+
 // ------------------------------------------------------------- clusters
 
 __device__ __forceinline__ void cluster_sync_all() {

@@ -17,13 +17,12 @@
 // needed row is read once.
 //
 // Sums. A drawn column moves when the running sums are off by more than the
-// distance of u * total to a border, so they are held to about 1e-14: a
-// thread adds its weights into a pair of fp32 (the sum and the error of each
-// addition, Knuth's two-sum), and pairs are joined in fp64. An fp64 addition
-// per weight would be bound by the fp64 rate (about 0.6 T additions/s, a
-// third of what the memory delivers). The weight itself is the fp32
-// difference p - q, rounded once (relative 2^-24, exact between values of
-// near exponents).
+// distance of u * total to a border, so they are held to about 2^-46: all
+// sums are pairs of fp32 (the sum and the errors of the additions). fp64 sums
+// took most of the kernel's time (165 us for 256 requests of 262144 columns):
+// this GPU issues one fp64 instruction per SM in 16 cycles. The weight
+// itself is the fp32 difference p - q, rounded once (relative 2^-24, exact
+// between values of near exponents).
 #include <climits>
 #include <type_traits>
 
@@ -32,7 +31,7 @@
 namespace drs {
 namespace {
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kStep = 256;  // elements a warp takes at once: 8 per lane
@@ -52,16 +51,15 @@ struct VerifyParams {
     int32_t vocab, max_drafts, cluster;
 };
 
-// A sum of fp32 values as s + c.
+// A running sum of fp32 values: the errors of the additions add up in c.
 struct PairSum {
     float s = 0.0f, c = 0.0f;
     __device__ __forceinline__ void add(float w) {
-        const float t = s + w;
-        const float z = t - s;
-        c += (s - (t - z)) + (w - z);
-        s = t;
+        const Pair t = two_sum(s, w);
+        s = t.s;
+        c += t.c;
     }
-    __device__ __forceinline__ double value() const { return static_cast<double>(s) + static_cast<double>(c); }
+    __device__ __forceinline__ Pair value() const { return normalized(s, c); }
 };
 
 // The row (or pair of rows) a request draws from. q is null where nothing
@@ -116,25 +114,24 @@ template <typename P, typename Q> struct Weights {
     }
 };
 
-// The first of n shares whose running sum (from `before` on) exceeds t, and
-// the sum before it; the last share with any mass where none does.
-__device__ __forceinline__ int pick(const double* share, int n, double t, double& before) {
-    int found = 0;
-    double run = before;
-    for (int k = 0; k < n; ++k) {
-        if (!(share[k] > 0.0)) continue;
-        found = k;
-        before = run;
-        run += share[k];
-        if (run > t) break;
-    }
+// The first of n shares (a power of two, one per lane) whose running sum
+// from `before` on exceeds t, and in `before` the sum before it; the last
+// share with any mass where none does.
+__device__ __forceinline__ int pick(const Pair* share, int n, int lane, Pair t, Pair& before) {
+    const Pair mine = lane < n ? share[lane] : Pair{0.0f, 0.0f};
+    const Pair upto = before + warp_scan_pair(mine, lane, n);
+    const bool some = lane < n && mine.s > 0.0f;
+    const uint32_t over = __ballot_sync(0xffffffffu, some && upto > t), any = __ballot_sync(0xffffffffu, some);
+    const int found = over ? __ffs(over) - 1 : 31 - __clz(any);
+    const Pair lower = shfl(upto, found > 0 ? found - 1 : 0);
+    if (found > 0) before = lower;
     return found;
 }
 
 // The sum of the weights of columns [begin, end), begin a multiple of kStep,
 // by one warp; every lane gets its own part.
 template <bool kSub, typename P, typename Q>
-__device__ __forceinline__ double lane_sum(const Weights<P, Q>& wt, int begin, int end, int lane) {
+__device__ __forceinline__ Pair lane_sum(const Weights<P, Q>& wt, int begin, int end, int lane) {
     PairSum sum;
     if (wt.vec) {
         constexpr int kUnroll = 4;
@@ -191,9 +188,9 @@ __device__ __forceinline__ double lane_sum(const Weights<P, Q>& wt, int begin, i
 template <typename P, typename Q>
 __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams a) {
     constexpr bool kDraft = !std::is_same<Q, NoDraft>::value;
-    __shared__ double s_cta[2][kMaxCluster];  // the CTAs' totals, by attempt
-    __shared__ double s_warp[kVerifyWarps];   // this CTA's warps' totals
-    __shared__ double s_scan[kVerifyWarps];
+    __shared__ __align__(8) Pair s_cta[2][kMaxCluster];  // the CTAs' totals, by attempt
+    __shared__ Pair s_warp[kVerifyWarps];                // this CTA's warps' totals
+    __shared__ Pair s_scan[kVerifyWarps];
     __shared__ int s_first, s_last;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -215,7 +212,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     const P* const target = static_cast<const P*>(a.target) + (first + b) * a.target_stride;
 
     // The accepted drafts, by every warp for itself. u q < p is decided
-    // exactly: the product of two fp32 numbers fits fp64.
+    // exactly, from the product and its rounding error; both sides are taken
+    // times 2^100, which keeps the error clear of underflow.
     int accepted = 0;
     for (int base = 0; base < count; base += 32) {
         const int j = base + lane;
@@ -223,11 +221,13 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         if (j < count) {
             const int64_t x = a.tokens[first + j];
             if (x >= 0 && x < a.vocab) {
-                const float p = to_f(target[j * a.target_stride + x]);
-                float q = 1.0f;
+                const float p = to_f(target[j * a.target_stride + x]) * 0x1p100f;
+                const float u = a.accept_u[first + j];
+                float q = 0x1p100f;
                 if constexpr (kDraft)
-                    q = to_f(static_cast<const Q*>(a.draft)[(first + j) * a.draft_stride + x]);
-                ok = static_cast<double>(a.accept_u[first + j]) * static_cast<double>(q) < static_cast<double>(p);
+                    q = to_f(static_cast<const Q*>(a.draft)[(first + j) * a.draft_stride + x]) * 0x1p100f;
+                const float h = u * q;
+                ok = h < p || (h == p && fmaf(u, q, -h) < 0.0f);
             }
         }
         const uint32_t mask = __ballot_sync(0xffffffffu, ok);
@@ -260,13 +260,13 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     // Each warp of the cluster owns `part` consecutive columns.
     const int parts = csize * kVerifyWarps;
     const int part = static_cast<int>(ceil_div(ceil_div(a.vocab, parts), kStep) * kStep);
-    double total = 0.0;
+    Pair total{0.0f, 0.0f};
     int used = 0;  // the attempt whose totals count
     for (int attempt = 0; attempt < 2; ++attempt) {
         const int64_t begin64 = static_cast<int64_t>(rank * kVerifyWarps + warp) * part;
         const int begin = begin64 < a.vocab ? static_cast<int>(begin64) : a.vocab;
         const int end = begin64 + part < a.vocab ? static_cast<int>(begin64 + part) : a.vocab;
-        double sum = 0.0;
+        Pair sum{0.0f, 0.0f};
         if (begin < end) {
             if (kDraft && wt.q) {
                 if constexpr (kDraft) sum = lane_sum<true>(wt, begin, end, lane);
@@ -274,30 +274,31 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
                 sum = lane_sum<false>(wt, begin, end, lane);
             }
         }
-        sum = warp_sum(sum);
+        sum = warp_sum_pair(sum);
         if (lane == 0) s_warp[warp] = sum;
         __syncthreads();
-        if (tid < csize) {
-            double cta = 0.0;
-            for (int w = 0; w < kVerifyWarps; ++w) cta += s_warp[w];
-            if (csize > 1)
-                store_remote(&s_cta[attempt][rank], tid, static_cast<uint64_t>(__double_as_longlong(cta)));
-            else
+        if (warp == 0) {
+            const Pair cta = shfl(warp_scan_pair(lane < kVerifyWarps ? s_warp[lane] : Pair{0.0f, 0.0f}, lane, kVerifyWarps),
+                                  kVerifyWarps - 1);
+            const uint64_t bits = static_cast<uint64_t>(__float_as_uint(cta.c)) << 32 | __float_as_uint(cta.s);
+            if (csize > 1) {
+                if (lane < csize) store_remote(&s_cta[attempt][rank], lane, bits);
+            } else if (lane == 0) {
                 s_cta[attempt][0] = cta;
+            }
         }
         if (csize > 1) cluster_sync_all();
         else __syncthreads();
-        total = 0.0;
-        for (int c = 0; c < csize; ++c) total += s_cta[attempt][c];
+        total = shfl(warp_scan_pair(lane < csize ? s_cta[attempt][lane] : Pair{0.0f, 0.0f}, lane, csize), csize - 1);
         // A refused draft whose p never exceeds its q (rounded
         // probabilities) draws from the target's own row.
-        if (total > 0.0 || whole || attempt == 1) break;
+        if (total.s > 0.0f || whole || attempt == 1) break;
         used = 1;
         wt.q = nullptr;
         wt.without = -1;
         wt.vec = (reinterpret_cast<uintptr_t>(wt.p) & 15) == 0;
     }
-    if (!(total > 0.0)) {  // no mass anywhere
+    if (!(total.s > 0.0f)) {  // no mass anywhere
         if (rank == 0 && tid == 0) out[accepted] = -1;
         return;
     }
@@ -305,11 +306,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
     // The share that holds the drawn column: the first whose running sum
     // exceeds t; the last one with any mass where rounding (or u >= 1)
     // leaves none.
-    const double t = static_cast<double>(a.sample_u[b]) * total;
-    double before = 0.0;
-    const int cta = pick(s_cta[used], csize, t, before);
+    const Pair t = a.sample_u[b] * total;
+    Pair before{0.0f, 0.0f};
+    const int cta = pick(s_cta[used], csize, lane, t, before);
     if (rank != cta) return;
-    const int w = pick(s_warp, kVerifyWarps, t, before);
+    const int w = pick(s_warp, kVerifyWarps, lane, t, before);
     const int begin = (rank * kVerifyWarps + w) * part;
     const int end = begin + part < a.vocab ? begin + part : a.vocab;
     int last = -1;  // the last column with a weight that this thread saw
@@ -317,25 +318,26 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         const int64_t i = at + 8 * tid;
         float v[8];
         wt.load(i, end, v);
-        double sum = 0.0;
+        PairSum own;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            sum += static_cast<double>(v[e]);
+            own.add(v[e]);
             if (v[e] > 0.0f) last = static_cast<int>(i) + e;
         }
-        const double scan = warp_scan_inclusive(sum, lane);
+        const Pair sum = own.value(), scan = warp_scan_pair(sum, lane);
         if (lane == 31) s_scan[warp] = scan;
         if (tid == 0) s_first = INT_MAX;
         __syncthreads();
-        double lower = before;
-        for (int k = 0; k < warp; ++k) lower += s_scan[k];
-        if (sum > 0.0 && lower + scan > t) atomicMin(&s_first, tid);
+        Pair lower = before;
+        for (int k = 0; k < warp; ++k) lower = lower + s_scan[k];
+        if (sum.s > 0.0f && lower + scan > t) atomicMin(&s_first, tid);
+        const Pair left = shfl_up(scan, 1);
         __syncthreads();
         if (s_first == tid) {
-            double run = lower + (scan - sum);
+            Pair run = lane > 0 ? lower + left : lower;
             int col = last;  // in this thread's eight, as its sum is positive
             for (int e = 0; e < 8; ++e) {
-                run += static_cast<double>(v[e]);
+                run = run + Pair{v[e], 0.0f};
                 if (v[e] > 0.0f && run > t) {
                     col = static_cast<int>(i) + e;
                     break;
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
             out[accepted] = col;
         }
         if (s_first != INT_MAX) return;
-        for (int k = 0; k < kVerifyWarps; ++k) before += s_scan[k];
+        for (int k = 0; k < kVerifyWarps; ++k) before = before + s_scan[k];
         __syncthreads();
     }
     // The share's sum, added in another order, fell just short of t.
