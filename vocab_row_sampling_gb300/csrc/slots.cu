@@ -89,7 +89,16 @@ __device__ __forceinline__ int64_t ring_place(int64_t place, int64_t offset, int
     return at;
 }
 
-constexpr int kOwnMoves = 4;  // blocks of a request that its thread moves by itself
+constexpr int kOwnMoves = 4;    // blocks of a request that its thread moves by itself
+constexpr int kMoveChunk = 128;  // further ones a warp moves at once, four per lane
+
+// The blocks of a request past its first kOwnMoves.
+struct LongMove {
+    int32_t* row;  // the first block's place in the table
+    int64_t from;  // its offset from the ring's head or tail
+    int32_t n;
+    bool take;
+};
 
 // The tokens of warp `w` of `warps`: a run of groups of 32. What the cluster
 // wrote is read from L2.
@@ -102,15 +111,13 @@ __device__ __forceinline__ void map_tokens(const SlotParams& a, int w, int warps
     // the request of the first token, the last b with out_cu[b] <= t: each
     // step takes 32 probes
     int b = 0;
-    if (static_cast<int64_t>(g0) * 32 < total) {
-        for (int n = a.requests; n > 1;) {
-            const int step = (n + 31) / 32;
-            const int at = lane * step;
-            const bool below = at < n && __ldcg(a.out_cu + b + at) <= g0 * 32;
-            const int hit = __popc(__ballot_sync(0xffffffffu, below)) - 1;  // lane 0 is below
-            b += hit * step;
-            n = min(step, n - hit * step);
-        }
+    for (int n = a.requests; n > 1;) {
+        const int step = (n + 31) / 32;
+        const int at = lane * step;
+        const bool below = at < n && __ldcg(a.out_cu + b + at) <= g0 * 32;
+        const int hit = __popc(__ballot_sync(0xffffffffu, below)) - 1;  // lane 0 is below
+        b += hit * step;
+        n = min(step, n - hit * step);
     }
     int32_t start = __ldcg(a.out_cu + b);
     for (int g = g0; g < g1; ++g) {
@@ -166,6 +173,8 @@ template <bool kTokens> __global__ void __launch_bounds__(kSlotThreads) slots_ke
     __shared__ int64_t s_cta[kSlotCluster][3];  // every CTA's sums
     __shared__ int64_t s_end[kSlotCluster][2];  // blocks taken and lacking, by CTA
     __shared__ unsigned long long s_taken, s_lacking;
+    __shared__ LongMove s_move[kSlotThreads];
+    __shared__ int s_moves;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int csize = a.cluster, rank = csize > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -181,7 +190,7 @@ template <bool kTokens> __global__ void __launch_bounds__(kSlotThreads) slots_ke
     const int64_t head = a.state[0], tail = a.state[1];
     int64_t avail = tail - head;
     avail = avail < 0 ? 0 : avail > a.ring_size ? a.ring_size : avail;
-    if (tid == 0) s_taken = 0, s_lacking = 0;
+    if (tid == 0) s_taken = 0, s_lacking = 0, s_moves = 0;
 
     // 1. sums before this thread's requests
     Sums mine{0, 0, 0};
@@ -227,8 +236,9 @@ template <bool kTokens> __global__ void __launch_bounds__(kSlotThreads) slots_ke
     at += s_warp[warp];
     const Sums all = s_all;
 
-    // 2. the requests' outputs and the moves of blocks. Warps stay whole:
-    // long moves are made by all lanes.
+    // 2. the requests' outputs and the moves of blocks: a few by the
+    // request's thread, longer ones by all warps (a request that ends gives
+    // hundreds of blocks back).
     const int64_t head_at = static_cast<int64_t>(static_cast<uint64_t>(head) % static_cast<uint64_t>(a.ring_size));
     const int64_t tail_at = static_cast<int64_t>(static_cast<uint64_t>(tail) % static_cast<uint64_t>(a.ring_size));
     int64_t taken = 0, lacking = 0;
@@ -261,17 +271,29 @@ template <bool kTokens> __global__ void __launch_bounds__(kSlotThreads) slots_ke
 #pragma unroll
         for (int i = 0; i < kOwnMoves; ++i)
             if (i < moves) (takes ? row[i] : a.ring[ring_place(tail_at, from + i, a.ring_size)]) = ids[i];
-        for (uint32_t todo = __ballot_sync(0xffffffffu, moves > kOwnMoves); todo; todo &= todo - 1) {
-            const int src = __ffs(todo) - 1;
-            const bool take = __shfl_sync(0xffffffffu, static_cast<int>(takes), src);
-            const int32_t n = __shfl_sync(0xffffffffu, moves, src);
-            const int64_t base = __shfl_sync(0xffffffffu, from, src);
-            int32_t* const there = a.table + __shfl_sync(0xffffffffu, b, src) * a.table_stride +
-                                   __shfl_sync(0xffffffffu, col, src);
-            for (int32_t i = kOwnMoves + lane; i < n; i += 32) {
-                if (take) there[i] = a.ring[ring_place(head_at, base + i, a.ring_size)];
-                else a.ring[ring_place(tail_at, base + i, a.ring_size)] = there[i];
+        if (moves > kOwnMoves) s_move[atomicAdd(&s_moves, 1)] = LongMove{row, from, moves, takes};
+        __syncthreads();
+        // chunks of the long moves, dealt out to the warps
+        const int n = s_moves;
+        for (int m = 0; m < n; ++m) {
+            const LongMove e = s_move[m];
+            for (int64_t c = (warp - m) & (kSlotWarps - 1); kOwnMoves + c * kMoveChunk < e.n; c += kSlotWarps) {
+                const int64_t i = kOwnMoves + c * kMoveChunk + lane;
+                int32_t id[kMoveChunk / 32];
+#pragma unroll
+                for (int u = 0; u < kMoveChunk / 32; ++u)
+                    if (i + 32 * u < e.n)
+                        id[u] = e.take ? a.ring[ring_place(head_at, e.from + i + 32 * u, a.ring_size)] : e.row[i + 32 * u];
+#pragma unroll
+                for (int u = 0; u < kMoveChunk / 32; ++u)
+                    if (i + 32 * u < e.n)
+                        (e.take ? e.row[i + 32 * u] : a.ring[ring_place(tail_at, e.from + i + 32 * u, a.ring_size)]) = id[u];
             }
+        }
+        if (k + 1 < run) {  // the list is used again
+            __syncthreads();
+            if (tid == 0) s_moves = 0;
+            __syncthreads();
         }
         at += s;
     }
