@@ -9,9 +9,9 @@
 //      their sums through distributed shared memory;
 //   2. every CTA writes its requests' offsets and counts and moves their
 //      blocks between the table and the ring.
-// The tokens then find their request in the offsets and look up their block,
-// a warp taking a run of them: in the same launch where there are few, in a
-// launch over all SMs (a programmatic dependent one) where there are many.
+// The tokens then find their request in the offsets and look up their block:
+// in the same launch where there are few, in a launch over all SMs (a
+// programmatic dependent one) where there are many.
 // All sums are 64-bit integers in request order, so the blocks that a
 // request gets do not depend on how the work is split.
 #include <climits>
@@ -78,6 +78,13 @@ struct Request {
     }
 };
 
+// A counter of the ring as a place in it.
+__device__ __forceinline__ int64_t ring_start(int64_t counter, int64_t size) {
+    const uint64_t c = static_cast<uint64_t>(counter), n = static_cast<uint64_t>(size);
+    if ((c | n) >> 32) return static_cast<int64_t>(c % n);
+    return static_cast<uint32_t>(c) % static_cast<uint32_t>(n);
+}
+
 // The place `offset` entries after `place` in the ring. Offsets are below
 // the ring's size where its counters are consistent.
 __device__ __forceinline__ int64_t ring_place(int64_t place, int64_t offset, int64_t size) {
@@ -100,39 +107,59 @@ struct LongMove {
     bool take;
 };
 
-// The tokens of warp `w` of `warps`: a run of groups of 32. What the cluster
-// wrote is read from L2.
-__device__ __forceinline__ void map_tokens(const SlotParams& a, int w, int warps, int lane) {
+// The request, position and slot of token t of request b, whose first
+// token is `first`.
+__device__ __forceinline__ void map_token(const SlotParams& a, int64_t t, int b, int32_t first, int32_t len, int32_t now,
+                                          const int32_t* row) {
+    const int64_t at = max(len, 0) + (t - first);
+    const int64_t col = quotient(at, a.block);
+    int64_t slot = -1;
+    if (col < now) slot = static_cast<int64_t>(__ldcg(row + col)) * a.block + (at - col * a.block);
+    a.out_request[t] = b;
+    a.out_position[t] = static_cast<int32_t>(min(at, static_cast<int64_t>(INT_MAX)));
+    a.out_slot[t] = slot;
+}
+
+__device__ __forceinline__ void pad_token(const SlotParams& a, int64_t t) {
+    a.out_request[t] = -1;
+    a.out_position[t] = 0;
+    a.out_slot[t] = -1;
+}
+
+// The tokens of warp `w` of `warps`: a run of groups of 32. kSame: the
+// offsets were written by this launch and are read from L2; else by the one
+// before, and L1 serves the probes that all warps share (from L2 they took
+// 10 of 13 us at 262144 tokens: every warp asks for the same lines).
+template <bool kSame> __device__ __forceinline__ void map_tokens(const SlotParams& a, int w, int warps, int lane) {
+    const auto offset = [&](int b) { return kSame ? __ldcg(a.out_cu + b) : a.out_cu[b]; };
     const int groups = static_cast<int>(ceil_div(a.capacity, 32));
     const int per = groups / warps, rest = groups % warps;
     const int g0 = w * per + min(w, rest), g1 = g0 + per + (w < rest);
     if (g0 >= g1) return;
-    const int32_t total = __ldcg(a.out_cu + a.requests);
+    const int32_t total = offset(a.requests);
     // the request of the first token, the last b with out_cu[b] <= t: each
     // step takes 32 probes
     int b = 0;
     for (int n = a.requests; n > 1;) {
         const int step = (n + 31) / 32;
         const int at = lane * step;
-        const bool below = at < n && __ldcg(a.out_cu + b + at) <= g0 * 32;
+        const bool below = at < n && offset(b + at) <= g0 * 32;
         const int hit = __popc(__ballot_sync(0xffffffffu, below)) - 1;  // lane 0 is below
         b += hit * step;
         n = min(step, n - hit * step);
     }
-    int32_t start = __ldcg(a.out_cu + b);
+    int32_t start = offset(b);
     for (int g = g0; g < g1; ++g) {
         const int64_t t = static_cast<int64_t>(g) * 32 + lane;
-        int32_t request = -1, position = 0;
-        int64_t slot = -1;
         if (static_cast<int64_t>(g) * 32 < total) {
             // the next 32 offsets; a token's request follows from how many
             // of them are not above it
-            const int32_t next = b + 1 + lane <= a.requests ? __ldcg(a.out_cu + b + 1 + lane) : INT_MAX;
+            const int32_t next = b + 1 + lane <= a.requests ? offset(b + 1 + lane) : INT_MAX;
             int n = 0;
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1)
                 if (__shfl_sync(0xffffffffu, next, n + s - 1) <= t) n += s;
-            request = b + n;
+            int request = b + n;
             int32_t first = __shfl_sync(0xffffffffu, next, n > 0 ? n - 1 : 0);
             if (n == 0) first = start;
             if (__shfl_sync(0xffffffffu, next, 31) <= t && t < total) {
@@ -140,32 +167,24 @@ __device__ __forceinline__ void map_tokens(const SlotParams& a, int w, int warps
                 int below = request, above = a.requests;
                 while (above - below > 1) {
                     const int mid = below + (above - below) / 2;
-                    if (__ldcg(a.out_cu + mid) <= t) below = mid;
+                    if (offset(mid) <= t) below = mid;
                     else above = mid;
                 }
                 request = below;
-                first = __ldcg(a.out_cu + below);
+                first = offset(below);
             }
             if (t < total) {
-                const int64_t at = max(a.lens[request], 0) + (t - first);
-                position = static_cast<int32_t>(min(at, static_cast<int64_t>(INT_MAX)));
-                const int64_t col = quotient(at, a.block);
-                if (col < __ldcg(a.out_held + request))
-                    slot = static_cast<int64_t>(__ldcg(a.table + request * a.table_stride + col)) * a.block +
-                           (at - col * a.block);
-            } else {
-                request = -1;
+                const int32_t len = a.lens[request], now = kSame ? __ldcg(a.out_held + request) : a.out_held[request];
+                map_token(a, t, request, first, len, now, a.table + request * a.table_stride);
             }
-            b = max(__shfl_sync(0xffffffffu, request, 31), b);
+            b = __shfl_sync(0xffffffffu, request, 31);  // past the last token: not used again
             start = __shfl_sync(0xffffffffu, first, 31);
         }
-        if (t < a.capacity) {
-            a.out_request[t] = request;
-            a.out_position[t] = position;
-            a.out_slot[t] = slot;
-        }
+        if (t >= total && t < a.capacity) pad_token(a, t);
     }
 }
+
+constexpr int kStage = 1024;  // requests whose offsets fit a CTA's shared memory
 
 template <bool kTokens> __global__ void __launch_bounds__(kSlotThreads) slots_kernel(const SlotParams a) {
     __shared__ Sums s_warp[kSlotWarps];
@@ -175,6 +194,7 @@ template <bool kTokens> __global__ void __launch_bounds__(kSlotThreads) slots_ke
     __shared__ unsigned long long s_taken, s_lacking;
     __shared__ LongMove s_move[kSlotThreads];
     __shared__ int s_moves;
+    __shared__ int32_t s_cu[kTokens ? kStage + 1 : 1], s_len[kTokens ? kStage : 1], s_now[kTokens ? kStage : 1];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int csize = a.cluster, rank = csize > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -239,8 +259,7 @@ template <bool kTokens> __global__ void __launch_bounds__(kSlotThreads) slots_ke
     // 2. the requests' outputs and the moves of blocks: a few by the
     // request's thread, longer ones by all warps (a request that ends gives
     // hundreds of blocks back).
-    const int64_t head_at = static_cast<int64_t>(static_cast<uint64_t>(head) % static_cast<uint64_t>(a.ring_size));
-    const int64_t tail_at = static_cast<int64_t>(static_cast<uint64_t>(tail) % static_cast<uint64_t>(a.ring_size));
+    const int64_t head_at = ring_start(head, a.ring_size), tail_at = ring_start(tail, a.ring_size);
     int64_t taken = 0, lacking = 0;
     for (int k = 0; k < run; ++k) {
         const int b = b0 + k;
@@ -255,8 +274,10 @@ template <bool kTokens> __global__ void __launch_bounds__(kSlotThreads) slots_ke
             now = served ? r.need : min(r.need, r.held);
             if (served) taken += s.take;
             lacking += r.want - now;
-            a.out_cu[b] = static_cast<int32_t>(min(at.tokens, a.capacity));
+            const int32_t cu = static_cast<int32_t>(min(at.tokens, a.capacity));
+            a.out_cu[b] = cu;
             a.out_held[b] = now;
+            if (kTokens && csize == 1 && a.requests <= kStage) s_cu[b] = cu, s_len[b] = static_cast<int32_t>(r.len), s_now[b] = now;
         }
         // blocks taken: ring -> columns [held, now); given: columns [need, held) -> ring
         const bool takes = now > r.held;
@@ -318,7 +339,34 @@ template <bool kTokens> __global__ void __launch_bounds__(kSlotThreads) slots_ke
         a.out_state[1] = tail + all.give;
         *a.out_lacking = static_cast<int32_t>(min(sum[1], static_cast<int64_t>(INT_MAX)));
     }
-    if constexpr (kTokens) map_tokens(a, rank * kSlotWarps + warp, csize * kSlotWarps, lane);
+    if constexpr (kTokens) {
+        if (a.requests > kStage) {
+            map_tokens<true>(a, rank * kSlotWarps + warp, csize * kSlotWarps, lane);
+            return;
+        }
+        const int32_t total = static_cast<int32_t>(min(all.tokens, a.capacity));
+        if (csize > 1) {
+            for (int b = tid; b < a.requests; b += kSlotThreads) {
+                s_cu[b] = __ldcg(a.out_cu + b);
+                s_len[b] = a.lens[b];
+                s_now[b] = __ldcg(a.out_held + b);
+            }
+            __syncthreads();
+        }
+        for (int64_t t = rank * kSlotThreads + tid; t < a.capacity; t += csize * kSlotThreads) {
+            if (t >= total) {
+                pad_token(a, t);
+                continue;
+            }
+            int below = 0, above = a.requests;  // s_cu[below] <= t < s_cu[above]
+            while (above - below > 1) {
+                const int mid = (below + above) / 2;
+                if (s_cu[mid] <= t) below = mid;
+                else above = mid;
+            }
+            map_token(a, t, below, s_cu[below], s_len[below], s_now[below], a.table + below * a.table_stride);
+        }
+    }
 }
 
 constexpr int kTokenThreads = 256;
@@ -326,7 +374,7 @@ constexpr int kTokenWarps = kTokenThreads / 32;
 
 __global__ void __launch_bounds__(kTokenThreads) slot_tokens_kernel(const SlotParams a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    map_tokens(a, blockIdx.x * kTokenWarps + (threadIdx.x >> 5), gridDim.x * kTokenWarps, threadIdx.x & 31);
+    map_tokens<false>(a, blockIdx.x * kTokenWarps + (threadIdx.x >> 5), gridDim.x * kTokenWarps, threadIdx.x & 31);
 }
 
 }  // namespace
@@ -380,8 +428,9 @@ extern "C" drs_status drs_map_slots(const int32_t* lens, const int32_t* new_lens
     // Many: the cluster for the requests, then a launch for the tokens.
     const bool apart = capacity > kSlotCluster * kSlotThreads;
     const int64_t work = !apart && capacity > requests ? capacity : requests;
+    const int64_t share = apart ? kSlotThreads / 2 : kSlotThreads;
     int cluster = 1;
-    while (cluster < kSlotCluster && work > static_cast<int64_t>(cluster) * kSlotThreads) cluster *= 2;
+    while (cluster < kSlotCluster && work > cluster * share) cluster *= 2;
     a.cluster = cluster;
     const auto kernel = apart ? slots_kernel<false> : slots_kernel<true>;
     if (cluster > 8 && cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
