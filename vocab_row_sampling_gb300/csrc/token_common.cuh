@@ -131,6 +131,46 @@ __device__ __forceinline__ Pair shfl(Pair v, int lane) {
     return Pair{__shfl_sync(0xffffffffu, v.s, lane), __shfl_sync(0xffffffffu, v.c, lane)};
 }
 
+// Two fp32 at once: one instruction per operation on both.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Two running sums of fp32 values: the errors of the additions add up in c.
+struct PairSum2 {
+    uint64_t s = 0, c = 0;
+    __device__ __forceinline__ void add(uint64_t w) {
+        const uint64_t t = add2(s, w);
+        const uint64_t z = sub2(t, s);
+        c = add2(c, add2(sub2(s, sub2(t, z)), sub2(w, z)));
+        s = t;
+    }
+    __device__ __forceinline__ Pair value() const {
+        float s0, s1, c0, c1;
+        unpack2(s, s0, s1);
+        unpack2(c, c0, c1);
+        return normalized(s0, c0) + normalized(s1, c1);
+    }
+};
+
 // Inclusive scan over the first n lanes (n a power of two).
 __device__ __forceinline__ Pair warp_scan_pair(Pair v, int lane, int n = 32) {
 #pragma unroll

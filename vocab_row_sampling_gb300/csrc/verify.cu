@@ -38,6 +38,11 @@ constexpr int kStep = 256;  // elements a warp takes at once: 8 per lane
 
 struct NoDraft {};
 
+// CTAs per SM that registers are held to: 5 (51 registers) measured 49.5 us
+// for 256 requests of 262144 columns, 4 with twice the loads in flight 49.6, 3
+// 53.7, 6 50.4 and 8 53.7; two fp32 rows spill at 5.
+template <typename P, typename Q> constexpr int kResident = sizeof(P) + sizeof(Q) >= 6 ? 4 : 5;
+
 struct VerifyParams {
     const void* target;
     const void* draft;
@@ -49,17 +54,6 @@ struct VerifyParams {
     int32_t* out_accepted;
     int64_t target_rows, target_stride, draft_rows, draft_stride;
     int32_t vocab, max_drafts, cluster;
-};
-
-// A running sum of fp32 values: the errors of the additions add up in c.
-struct PairSum {
-    float s = 0.0f, c = 0.0f;
-    __device__ __forceinline__ void add(float w) {
-        const Pair t = two_sum(s, w);
-        s = t.s;
-        c += t.c;
-    }
-    __device__ __forceinline__ Pair value() const { return normalized(s, c); }
 };
 
 // The row (or pair of rows) a request draws from. q is null where nothing
@@ -82,8 +76,12 @@ template <typename P, typename Q> struct Weights {
     template <bool kSub> __device__ __forceinline__ void finish(const Raw8<P>& rp, const float (&qv)[8], int i,
                                                                 float (&w)[8]) const {
         rp.unpack(w);
+        if constexpr (kSub) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = fmaxf(kSub ? w[e] - qv[e] : w[e], 0.0f);
+            for (int e = 0; e < 8; e += 2) unpack2(sub2(pack2(w[e], w[e + 1]), pack2(qv[e], qv[e + 1])), w[e], w[e + 1]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = fmaxf(w[e], 0.0f);
         if (!kSub && static_cast<uint32_t>(without - i) < 8u) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -132,9 +130,9 @@ __device__ __forceinline__ int pick(const Pair* share, int n, int lane, Pair t, 
 // by one warp; every lane gets its own part.
 template <bool kSub, typename P, typename Q>
 __device__ __forceinline__ Pair lane_sum(const Weights<P, Q>& wt, int begin, int end, int lane) {
-    PairSum sum;
+    PairSum2 sum;
     if (wt.vec) {
-        constexpr int kUnroll = 4;
+        constexpr int kUnroll = 2;
         int i = begin + 8 * lane;
         for (; i + (kUnroll - 1) * kStep + 8 <= end; i += kUnroll * kStep) {
             Raw8<P> rp[kUnroll];
@@ -150,7 +148,7 @@ __device__ __forceinline__ Pair lane_sum(const Weights<P, Q>& wt, int begin, int
                 if constexpr (kSub) rq[k].unpack(qv);
                 wt.template finish<kSub>(rp[k], qv, i + k * kStep, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum.add(w[e]);
+                for (int e = 0; e < 8; e += 2) sum.add(pack2(w[e], w[e + 1]));
             }
         }
         for (; i < end; i += kStep) {
@@ -165,9 +163,9 @@ __device__ __forceinline__ Pair lane_sum(const Weights<P, Q>& wt, int begin, int
                 }
                 wt.template finish<kSub>(rp, qv, i, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum.add(w[e]);
+                for (int e = 0; e < 8; e += 2) sum.add(pack2(w[e], w[e + 1]));
             } else {
-                for (int e = i; e < end; ++e) sum.add(wt.one(e));
+                for (int e = i; e < end; ++e) sum.add(pack2(wt.one(e), 0.0f));
             }
         }
     } else {
@@ -178,15 +176,15 @@ __device__ __forceinline__ Pair lane_sum(const Weights<P, Q>& wt, int begin, int
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = wt.one(i + 32 * e);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum.add(w[e]);
+            for (int e = 0; e < 8; e += 2) sum.add(pack2(w[e], w[e + 1]));
         }
-        for (; i < end; i += 32) sum.add(wt.one(i));
+        for (; i < end; i += 32) sum.add(pack2(wt.one(i), 0.0f));
     }
     return sum.value();
 }
 
 template <typename P, typename Q>
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyParams a) {
+__global__ void __launch_bounds__(kVerifyThreads, kResident<P, Q>) verify_kernel(const VerifyParams a) {
     constexpr bool kDraft = !std::is_same<Q, NoDraft>::value;
     __shared__ __align__(8) Pair s_cta[2][kMaxCluster];  // the CTAs' totals, by attempt
     __shared__ Pair s_warp[kVerifyWarps];                // this CTA's warps' totals
@@ -318,10 +316,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyPara
         const int64_t i = at + 8 * tid;
         float v[8];
         wt.load(i, end, v);
-        PairSum own;
+        PairSum2 own;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            own.add(v[e]);
+            if (e % 2) own.add(pack2(v[e - 1], v[e]));
             if (v[e] > 0.0f) last = static_cast<int>(i) + e;
         }
         const Pair sum = own.value(), scan = warp_scan_pair(sum, lane);
