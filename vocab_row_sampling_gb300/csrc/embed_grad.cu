@@ -221,8 +221,10 @@ template <int kItems> __global__ void __launch_bounds__(kSortThreads) sort_clust
             for (int k = 0; k < 2; ++k) {
                 if (k >= per) break;
 #pragma unroll
-                for (int c = 0; c < kSortCluster; ++c) {
-                    if (c >= csize) break;
+                for (int i = 0; i < kSortCluster; ++i) {
+                    if (i >= csize) break;
+                    // each CTA begins with itself: a CTA answers one at a time
+                    const int c = (rank + i) & (csize - 1);
                     const uint32_t n = csize > 1 ? load_remote(s_total + tid * per + k, c) : s_total[tid * per + k];
                     all[k] += n;
                     if (c < rank) earlier[k] += n;
@@ -448,19 +450,15 @@ __global__ void __launch_bounds__(kSumThreads) grad_join_kernel(const GradParams
     const int across = static_cast<int>(ceil_div(a.width, a.columns * kVec));
     const int64_t piece = blockIdx.x / across * (kSumThreads / a.columns) + ty;
     const int col = static_cast<int>((blockIdx.x % across) * a.columns + tx) * kVec;
-    if (piece >= a.pieces || col >= a.width) return;
+    if (piece >= a.pieces) return;
     const int64_t p0 = piece * a.piece, p1 = p0 + a.piece;
     if (p1 >= a.n) return;
     const uint32_t key = a.keys[p1 - 1];
     if (key == static_cast<uint32_t>(a.vocab) || a.keys[p1] != key) return;
     if (p0 > 0 && a.keys[p0 - 1] == key) return;  // began earlier
-    int64_t lo = p1, hi = a.n;  // the end of the id's tokens
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (a.keys[mid] <= key) lo = mid + 1;
-        else hi = mid;
-    }
-    const int64_t last = (lo - 1) / a.piece;
+    // a warp has one piece (columns >= 32)
+    const int64_t last = (count_below(a, key + 1, threadIdx.x & 31) - 1) / a.piece;
+    if (col >= a.width) return;
     float acc[kVec];
     Row<float, kVec> first;
     first.load(a.partial + (piece * 2 + 1) * a.width + col);
@@ -613,7 +611,7 @@ drs_status sort_tokens(const SortPlan& s, const Workspace& w, const void* ids, i
 template <typename G, typename T, int kVec> drs_status launch_sums(GradParams a, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms <= 0) return DRS_ERR_CUDA;
-    int x = 8;  // at least, so that a CTA's lists stay within 32 KB
+    int x = 32;  // a warp has one piece
     while (x < kSumThreads && x * kVec < a.width) x *= 2;
     a.columns = x;
     const int64_t across = ceil_div(a.width, static_cast<int64_t>(x) * kVec);
