@@ -1,7 +1,9 @@
 // capi.cu -- status strings, the device error flag and launch bookkeeping of
 // libdrs.
 #include <atomic>
+#include <map>
 #include <mutex>
+#include <utility>
 
 #include "drs_internal.h"
 
@@ -81,6 +83,31 @@ int sm_count() {
         g_sms[dev] = n;
     }
     return g_sms[dev];
+}
+
+namespace {
+struct Prepared {
+    size_t smem = 0;
+    bool wide = false;
+};
+std::map<std::pair<const void*, int>, Prepared> g_prepared;
+}  // namespace
+
+bool prepare_kernel(const void* kernel, size_t smem, bool wide_cluster) {
+    const int dev = current_device();
+    if (dev < 0) return false;
+    std::lock_guard<std::mutex> lock(g_mutex);
+    Prepared& p = g_prepared[{kernel, dev}];
+    if (smem > p.smem) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+            return false;
+        p.smem = smem;
+    }
+    if (wide_cluster && !p.wide) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
+        p.wide = true;
+    }
+    return true;
 }
 
 // ------------------------------------------------------- kernel timing

@@ -27,6 +27,12 @@ int sm_count();
 // caller's stream wait for `join` recorded after the second part.
 bool side_stream(cudaStream_t* stream, cudaEvent_t* fork, cudaEvent_t* join);
 
+// Prepare `kernel` for launches with `smem` bytes of dynamic shared memory
+// and, with wide_cluster, clusters of more than 8 CTAs, on the current device
+// (remembered per kernel and device: setting an attribute takes about a
+// microsecond).
+bool prepare_kernel(const void* kernel, size_t smem, bool wide_cluster);
+
 // Map a CUDA error to a status.
 inline drs_status cuda_status(cudaError_t e) {
     return e == cudaSuccess ? DRS_OK : DRS_ERR_CUDA;

@@ -2,8 +2,8 @@
 // out[t] = scale * table[ids[t]], rounded once.
 //
 // Bound by memory: one row read and one written per token. A block's threads
-// lie along the columns, 16 bytes each, and take four tokens at once, so that
-// each thread has four independent loads behind its four ids. Rows that do
+// lie along the columns, 16 bytes each, and take two or four tokens at once:
+// that many independent loads per thread, behind as many ids. Rows that do
 // not start on 16-byte boundaries (odd widths, strides or offsets) are
 // written in aligned 16-byte words all the same, each put together from the
 // two aligned words of the table that hold it: single elements took 12.1 us
@@ -13,8 +13,9 @@
 namespace drs {
 namespace {
 
-constexpr int kEmbedThreads = 256;
-constexpr int kEmbedRows = 4;  // tokens a thread has in flight
+// Threads per CTA, for rows off 16-byte boundaries and for aligned ones:
+// 65536 x 4096 bf16 takes 117 us with 64 or 128, 120 with 256, 125 with 512.
+constexpr int kThreadsOf[2] = {256, 128};
 
 struct EmbedParams {
     const void* table;
@@ -48,8 +49,8 @@ __device__ __forceinline__ uint4 joined(uint4 lo, uint4 hi, int shift) {
 // kAligned: every row of the table and of the output starts on 16 bytes. A
 // thread has word `c` of its rows, and in rows that do not also an element of
 // their edges.
-template <typename T, typename I, bool kAligned>
-__global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams a) {
+template <typename T, typename I, bool kAligned, int kEmbedRows>
+__global__ void __launch_bounds__(kThreadsOf[kAligned]) embed_kernel(const EmbedParams a) {
     constexpr int kVec = 16 / sizeof(T);
     const T* const table = static_cast<const T*>(a.table);
     const I* const ids = static_cast<const I*>(a.ids);
@@ -120,20 +121,31 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_kernel(const EmbedParams 
     }
 }
 
-template <typename T, typename I, bool kAligned> drs_status launch_embed(EmbedParams a, cudaStream_t stream) {
-    constexpr int kVec = 16 / sizeof(T);
-    // threads along the columns: a word each, and at least one for each of
-    // the (at most 4 kVec - 2) elements of a row's edges
-    int64_t places = a.width / kVec;
-    if (!kAligned && places < 4 * kVec) places = 4 * kVec;
-    a.columns = static_cast<int32_t>(ceil_div(places, kEmbedThreads));
+template <typename T, typename I, bool kAligned, int kRows>
+drs_status launch_embed_rows(EmbedParams a, int64_t places, cudaStream_t stream) {
+    constexpr int kThreads = kThreadsOf[kAligned];
+    a.columns = static_cast<int32_t>(ceil_div(places, kThreads));
     int x = static_cast<int>(ceil_div(places, a.columns));
     if (x > 32) x = (x + 31) / 32 * 32;
-    const dim3 block(x, kEmbedThreads / x);
-    const int64_t blocks = ceil_div(a.tokens, block.y * kEmbedRows) * a.columns;
+    const dim3 block(x, kThreads / x);
+    const int64_t blocks = ceil_div(a.tokens, block.y * kRows) * a.columns;
     if (blocks > INT32_MAX) return DRS_ERR_UNSUPPORTED;
-    embed_kernel<T, I, kAligned><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
+    embed_kernel<T, I, kAligned, kRows><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
     return cuda_status(cudaGetLastError());
+}
+
+template <typename T, typename I> drs_status launch_embed(const EmbedParams& a, bool vec, cudaStream_t stream) {
+    constexpr int kVec = 16 / sizeof(T);
+    // threads along the columns: a word each, and in rows off 16-byte
+    // boundaries at least one for each of the (at most 4 kVec - 2) elements of
+    // a row's edges
+    int64_t places = a.width / kVec;
+    if (!vec) return launch_embed_rows<T, I, false, 2>(a, places < 4 * kVec ? 4 * kVec : places, stream);
+    // Tokens per thread, measured: 65536 x 4096 bf16 takes 164 us with one, 125
+    // with two, 120 with four and 122 with eight; 256 x 2048 takes 1.9 us with
+    // one or two, 2.2 with four, 3.0 with eight.
+    const bool many = a.tokens * places > int64_t{8192} * sm_count();
+    return many ? launch_embed_rows<T, I, true, 4>(a, places, stream) : launch_embed_rows<T, I, true, 2>(a, places, stream);
 }
 
 }  // namespace
@@ -166,7 +178,6 @@ extern "C" drs_status drs_embed_tokens(const void* table, drs_dtype dtype, int64
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return with_dtype(dtype, [&](auto t) -> drs_status {
         using T = decltype(t);
-        if (id_bits == 32) return vec ? launch_embed<T, int32_t, true>(a, st) : launch_embed<T, int32_t, false>(a, st);
-        return vec ? launch_embed<T, int64_t, true>(a, st) : launch_embed<T, int64_t, false>(a, st);
+        return id_bits == 32 ? launch_embed<T, int32_t>(a, vec, st) : launch_embed<T, int64_t>(a, vec, st);
     });
 }

@@ -149,10 +149,15 @@ struct ClusterSortParams {
     int32_t passes, cluster;
 };
 
-__device__ __forceinline__ uint32_t load_remote(const uint32_t* local, uint32_t rank) {
-    uint32_t addr, v;
+// 16 bytes of the same shared-memory variable of CTA `rank`.
+__device__ __forceinline__ uint4 load_remote(const void* local, uint32_t rank) {
+    uint32_t addr;
+    uint4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
@@ -161,9 +166,11 @@ template <int kItems> __global__ void __launch_bounds__(kSortThreads) sort_clust
     __shared__ uint32_t s_scan[kSortWarps];
     const int bins = 1 << a.s.bits, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int csize = a.cluster, rank = csize > 1 ? static_cast<int>(cluster_rank()) : 0;
-    uint32_t* const s_total = reinterpret_cast<uint32_t*>(s_item + a.share);  // [bins] this CTA's counts
-    uint32_t* const s_place = s_total + bins;                                 // [bins] places of its first items
-    uint16_t* const s_warp = reinterpret_cast<uint16_t*>(s_place + bins) + warp * bins;  // [warps][bins]
+    // counts are 16-bit: a CTA has at most 8192 items
+    uint16_t* const s_total = reinterpret_cast<uint16_t*>(s_item + (a.share + 1) / 2 * 2);  // [bins] this CTA's counts
+    uint16_t* const s_counts = s_total + bins;                                             // [warps][bins]
+    uint32_t* const s_place = reinterpret_cast<uint32_t*>(s_counts + kSortWarps * bins);   // [bins] places of its first items
+    uint16_t* const s_warp = s_counts + warp * bins;
     const int64_t base = static_cast<int64_t>(rank) * a.share;
     const int count = static_cast<int>(a.s.n - base < a.share ? (a.s.n > base ? a.s.n - base : 0) : a.share);
     const int mine = warp * 32 * kItems + lane;  // item i of this thread: mine + 32 i
@@ -198,46 +205,56 @@ template <int kItems> __global__ void __launch_bounds__(kSortThreads) sort_clust
             below[i] = before + ahead;
         }
         __syncthreads();
-        // the warps' counts become the counts of the warps before
-        for (int d = tid; d < bins; d += kSortThreads) {
+        // the warps' counts become the counts of the warps before, two digits
+        // per thread
+        for (int d = tid; d < bins / 2; d += kSortThreads) {
+            uint32_t* const c = reinterpret_cast<uint32_t*>(s_counts) + d;
             uint32_t run = 0;
-            uint16_t* const c = s_warp - warp * bins + d;
-#pragma unroll 8
-            for (int w = 0; w < kSortWarps; ++w) {
-                const uint32_t n = c[w * bins];
-                c[w * bins] = static_cast<uint16_t>(run);
-                run += n;
+#pragma unroll 1
+            for (int w0 = 0; w0 < kSortWarps; w0 += 16) {
+                uint32_t n[16];
+#pragma unroll
+                for (int w = 0; w < 16; ++w) n[w] = c[(w0 + w) * (bins / 2)];
+#pragma unroll
+                for (int w = 0; w < 16; ++w) {
+                    c[(w0 + w) * (bins / 2)] = run;
+                    run += n[w];
+                }
             }
-            s_total[d] = run;
+            reinterpret_cast<uint32_t*>(s_total)[d] = run;
         }
         if (csize > 1) cluster_sync_all();
         else __syncthreads();
         // places: items with a lower digit, then those of the CTAs before.
-        // A thread takes `per` consecutive digits.
-        const int per = bins > kSortThreads ? bins / kSortThreads : 1;
-        uint32_t all[2] = {0, 0}, earlier[2] = {0, 0};
-        if (tid * per < bins) {
+        // A thread takes eight digits.
+        uint32_t all[8] = {}, earlier[8] = {}, sum = 0;
+        if (tid < bins / 8) {
+#pragma unroll 4
+            for (int i = 0; i < csize; ++i) {
+                // each CTA begins with itself: a CTA answers one at a time
+                const int c = (rank + i) & (csize - 1);
+                const uint4 v = csize > 1 ? load_remote(s_total + 8 * tid, c) : *reinterpret_cast<const uint4*>(s_total + 8 * tid);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (k >= per) break;
-#pragma unroll
-                for (int i = 0; i < kSortCluster; ++i) {
-                    if (i >= csize) break;
-                    // each CTA begins with itself: a CTA answers one at a time
-                    const int c = (rank + i) & (csize - 1);
-                    const uint32_t n = csize > 1 ? load_remote(s_total + tid * per + k, c) : s_total[tid * per + k];
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t n = k % 2 ? w[k / 2] >> 16 : w[k / 2] & 0xffffu;
                     all[k] += n;
                     if (c < rank) earlier[k] += n;
                 }
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum += all[k];
         }
-        const uint32_t sum = all[0] + all[1], scan = warp_scan_inclusive(sum, lane);
+        const uint32_t scan = warp_scan_inclusive(sum, lane);
         if (lane == 31) s_scan[warp] = scan;
         __syncthreads();
-        const uint32_t lower = warp_sum(lane < warp ? s_scan[lane] : 0u) + scan - sum;
-        if (tid * per < bins) {
-            s_place[tid * per] = lower + earlier[0];
-            if (per > 1) s_place[tid * per + 1] = lower + all[0] + earlier[1];
+        uint32_t lower = warp_sum(lane < warp ? s_scan[lane] : 0u) + scan - sum;
+        if (tid < bins / 8) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                s_place[8 * tid + k] = lower + earlier[k];
+                lower += all[k];
+            }
         }
         __syncthreads();
 #pragma unroll
@@ -276,7 +293,8 @@ struct GradParams {
     float* partial;  // [pieces][2][width]
     int64_t n, pieces, grad_stride, table_stride;
     int64_t sum_blocks;  // the CTAs after these zero rows
-    int32_t width, columns, vocab, piece, zero_rows;
+    int32_t width, vocab, piece, zero_rows;
+    uint32_t columns, across;  // threads along the columns, CTAs along a row
     float scale;
     bool accumulate;
 };
@@ -384,10 +402,9 @@ __global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(const GradParams 
         return;
     }
     const int tx = threadIdx.x % a.columns, ty = threadIdx.x / a.columns;
-    const int across = static_cast<int>(ceil_div(a.width, a.columns * kVec));  // CTAs along a row
     const int per_cta = kSumThreads / a.columns;
-    const int64_t piece0 = blockIdx.x / across * per_cta, piece = piece0 + ty;
-    const int col = static_cast<int>((blockIdx.x % across) * a.columns + tx) * kVec;
+    const int64_t piece0 = static_cast<int64_t>(blockIdx.x / a.across) * per_cta, piece = piece0 + ty;
+    const int col = static_cast<int>((blockIdx.x % a.across) * a.columns + tx) * kVec;
     const uint32_t none = static_cast<uint32_t>(a.vocab);
     const int listed = per_cta * a.piece;
     for (int i = threadIdx.x; i < listed; i += kSumThreads) {
@@ -447,9 +464,8 @@ __global__ void __launch_bounds__(kSumThreads) grad_join_kernel(const GradParams
     constexpr int kAhead = 8;
     wait_for_previous();
     const int tx = threadIdx.x % a.columns, ty = threadIdx.x / a.columns;
-    const int across = static_cast<int>(ceil_div(a.width, a.columns * kVec));
-    const int64_t piece = blockIdx.x / across * (kSumThreads / a.columns) + ty;
-    const int col = static_cast<int>((blockIdx.x % across) * a.columns + tx) * kVec;
+    const int64_t piece = static_cast<int64_t>(blockIdx.x / a.across) * (kSumThreads / a.columns) + ty;
+    const int col = static_cast<int>((blockIdx.x % a.across) * a.columns + tx) * kVec;
     if (piece >= a.pieces) return;
     const int64_t p0 = piece * a.piece, p1 = p0 + a.piece;
     if (p1 >= a.n) return;
@@ -457,7 +473,7 @@ __global__ void __launch_bounds__(kSumThreads) grad_join_kernel(const GradParams
     if (key == static_cast<uint32_t>(a.vocab) || a.keys[p1] != key) return;
     if (p0 > 0 && a.keys[p0 - 1] == key) return;  // began earlier
     // a warp has one piece (columns >= 32)
-    const int64_t last = (count_below(a, key + 1, threadIdx.x & 31) - 1) / a.piece;
+    const int64_t last = (count_below(a, key + 1, threadIdx.x & 31) - 1) / static_cast<uint32_t>(a.piece);
     if (col >= a.width) return;
     float acc[kVec];
     Row<float, kVec> first;
@@ -498,6 +514,7 @@ struct SortPlan {
         SortPlan s;
         s.passes = key <= kMaxDigit ? 1 : 2;
         s.bits = (key + s.passes - 1) / s.passes;
+        if (s.bits < 4) s.bits = 4;  // eight digits are one 16-byte word
         s.cluster = 0;
         s.share = 0;
         if (n <= kClusterSort) {
@@ -542,12 +559,9 @@ struct Workspace {
 
 template <int kItems> drs_status launch_cluster_sort(const ClusterSortParams& a, cudaStream_t stream) {
     const size_t bins = size_t{1} << a.s.bits;
-    const size_t smem = static_cast<size_t>(a.share) * 8 + bins * 8 + bins * 2 * kSortWarps;
+    const size_t smem = static_cast<size_t>(a.share + 1) * 8 + bins * (2 + 2 * kSortWarps + 4);
     const auto kernel = sort_cluster_kernel<kItems>;
-    const void* f = reinterpret_cast<const void*>(kernel);
-    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess ||
-        cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return DRS_ERR_CUDA;
+    if (!prepare_kernel(reinterpret_cast<const void*>(kernel), smem, a.cluster > 8)) return DRS_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.cluster));
     cfg.blockDim = dim3(kSortThreads);
@@ -584,9 +598,7 @@ drs_status sort_tokens(const SortPlan& s, const Workspace& w, const void* ids, i
     }
     const size_t bins = size_t{1} << s.bits;
     const size_t count_smem = bins * 4, place_smem = bins * 4 + bins * 2 * kSortWarps;
-    if (cudaFuncSetAttribute(sort_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(place_smem)) != cudaSuccess)
-        return DRS_ERR_CUDA;
+    if (!prepare_kernel(reinterpret_cast<const void*>(sort_place_kernel), place_smem, false)) return DRS_ERR_CUDA;
     for (int pass = 0; pass < s.passes; ++pass) {
         SortParams a{};
         a.ids = ids;
@@ -614,8 +626,8 @@ template <typename G, typename T, int kVec> drs_status launch_sums(GradParams a,
     int x = 32;  // a warp has one piece
     while (x < kSumThreads && x * kVec < a.width) x *= 2;
     a.columns = x;
-    const int64_t across = ceil_div(a.width, static_cast<int64_t>(x) * kVec);
-    a.sum_blocks = ceil_div(a.pieces, kSumThreads / x) * across;
+    a.across = static_cast<uint32_t>(ceil_div(a.width, static_cast<int64_t>(x) * kVec));
+    a.sum_blocks = ceil_div(a.pieces, kSumThreads / x) * a.across;
     int64_t zero_blocks = 0;
     if (!a.accumulate) {
         // Measured for 32768 x 2048 bf16 into 262144 fp32 rows: 335 us with

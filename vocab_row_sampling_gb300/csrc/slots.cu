@@ -433,9 +433,7 @@ extern "C" drs_status drs_map_slots(const int32_t* lens, const int32_t* new_lens
     while (cluster < kSlotCluster && work > cluster * share) cluster *= 2;
     a.cluster = cluster;
     const auto kernel = apart ? slots_kernel<false> : slots_kernel<true>;
-    if (cluster > 8 && cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                            cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return DRS_ERR_CUDA;
+    if (cluster > 8 && !prepare_kernel(reinterpret_cast<const void*>(kernel), 0, true)) return DRS_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(cluster));
     cfg.blockDim = dim3(kSlotThreads);

@@ -53,7 +53,7 @@ struct VerifyParams {
     int64_t* out_tokens;
     int32_t* out_accepted;
     int64_t target_rows, target_stride, draft_rows, draft_stride;
-    int32_t vocab, max_drafts, cluster;
+    int32_t vocab, max_drafts, cluster, part;
 };
 
 // The row (or pair of rows) a request draws from. q is null where nothing
@@ -256,8 +256,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident<P, Q>) verify_kernel
     }
 
     // Each warp of the cluster owns `part` consecutive columns.
-    const int parts = csize * kVerifyWarps;
-    const int part = static_cast<int>(ceil_div(ceil_div(a.vocab, parts), kStep) * kStep);
+    const int part = a.part;
     Pair total{0.0f, 0.0f};
     int used = 0;  // the attempt whose totals count
     for (int attempt = 0; attempt < 2; ++attempt) {
@@ -407,15 +406,13 @@ extern "C" drs_status drs_verify_drafts(const void* target, drs_dtype target_dty
     const int most = requests * 8 < sms ? kMaxCluster : 8;
     while (cluster < most && vocab > 8192 * cluster) cluster *= 2;
     a.cluster = cluster;
+    a.part = static_cast<int32_t>(ceil_div(ceil_div(vocab, cluster * kVerifyWarps), kStep) * kStep);
 
     const bool has_draft = draft != nullptr;
     const VerifyKernel kernel = with_dtype(target_dtype, [&](auto p) -> VerifyKernel {
         return verify_kernel_for<decltype(p)>(has_draft, draft_dtype);
     });
-    if (cluster > 8 &&
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeNonPortableClusterSizeAllowed,
-                             1) != cudaSuccess)
-        return DRS_ERR_CUDA;
+    if (cluster > 8 && !prepare_kernel(reinterpret_cast<const void*>(kernel), 0, true)) return DRS_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(requests * cluster));
     cfg.blockDim = dim3(kVerifyThreads);
