@@ -80,13 +80,18 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
     const int per = bins > kSortThreads ? bins / kSortThreads : 1;
     uint32_t earlier[1 << (kMaxDigit - 10)] = {}, total[1 << (kMaxDigit - 10)] = {}, sum = 0;
     if (tid * per < bins) {
-        for (int t = 0; t < a.tiles; ++t)
-            for (int k = 0; k < per; ++k) {
-                const uint32_t c = a.counts[static_cast<int64_t>(t) * bins + tid * per + k];
-                total[k] += c;
-                if (t < static_cast<int>(blockIdx.x)) earlier[k] += c;
+#pragma unroll
+        for (int k = 0; k < 1 << (kMaxDigit - 10); ++k) {
+            if (k >= per) break;
+            const uint32_t* const c = a.counts + tid * per + k;
+#pragma unroll 16
+            for (int t = 0; t < a.tiles; ++t) {
+                const uint32_t n = c[t * bins];
+                total[k] += n;
+                if (t < static_cast<int>(blockIdx.x)) earlier[k] += n;
             }
-        for (int k = 0; k < per; ++k) sum += total[k];
+            sum += total[k];
+        }
     }
     const uint32_t scan = warp_scan_inclusive(sum, lane);
     if (lane == 31) s_scan[warp] = scan;
@@ -295,6 +300,7 @@ struct GradParams {
     int64_t sum_blocks;  // the CTAs after these zero rows
     int32_t width, vocab, piece, zero_rows;
     uint32_t columns, across;  // threads along the columns, CTAs along a row
+    uint32_t zero_across;      // threads along a row that is zeroed
     float scale;
     bool accumulate;
 };
@@ -351,16 +357,17 @@ __device__ __forceinline__ void write_row(const GradParams& a, uint32_t key, int
     store_row<T, kVec>(p, v);
 }
 
-// n elements from p on, in 16-byte stores between the ragged ends.
-template <typename T> __device__ __forceinline__ void zero_range(T* p, int64_t n) {
+// n elements from p on by `threads` threads (8 at least), in 16-byte stores
+// between the ragged ends.
+template <typename T> __device__ __forceinline__ void zero_range(T* p, int64_t n, int thread, int threads) {
     constexpr int kPer = 16 / sizeof(T);
     int64_t lead = static_cast<int64_t>((-reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
     lead = lead < n ? lead : n;
     const int64_t words = (n - lead) / kPer, done = lead + words * kPer;
-    if (threadIdx.x < lead) p[threadIdx.x] = from_f<T>(0.0f);
-    if (threadIdx.x < n - done) p[done + threadIdx.x] = from_f<T>(0.0f);
+    if (thread < lead) p[thread] = from_f<T>(0.0f);
+    if (thread < n - done) p[done + thread] = from_f<T>(0.0f);
     uint4* const w = reinterpret_cast<uint4*>(p + lead);
-    for (int64_t i = threadIdx.x; i < words; i += kSumThreads) __stcs(w + i, make_uint4(0, 0, 0, 0));
+    for (int64_t i = thread; i < words; i += threads) __stcs(w + i, make_uint4(0, 0, 0, 0));
 }
 
 template <typename T> __device__ __forceinline__ void zero_rows(const GradParams& a, int64_t block) {
@@ -378,6 +385,12 @@ template <typename T> __device__ __forceinline__ void zero_rows(const GradParams
     for (int64_t p = s_range[0] + threadIdx.x; p < s_range[1]; p += kSumThreads) s_touched[a.keys[p] - v0] = true;
     __syncthreads();
     T* const table = static_cast<T*>(a.table) + v0 * a.table_stride;
+    if (a.zero_across < kSumThreads) {  // narrow rows: several at once
+        const int tx = threadIdx.x % a.zero_across, ny = kSumThreads / a.zero_across;
+        for (int r = threadIdx.x / a.zero_across; r < n; r += ny)
+            if (!s_touched[r]) zero_range(table + r * a.table_stride, a.width, tx, a.zero_across);
+        return;
+    }
     const bool dense = a.table_stride == a.width;
     for (int r = 0; r < n;) {
         if (s_touched[r]) {
@@ -386,7 +399,7 @@ template <typename T> __device__ __forceinline__ void zero_rows(const GradParams
         }
         int end = r + 1;  // consecutive rows without padding are one range
         while (dense && end < n && !s_touched[end]) ++end;
-        zero_range(table + r * a.table_stride, dense ? (end - r) * a.table_stride : a.width);
+        zero_range(table + r * a.table_stride, dense ? (end - r) * a.table_stride : a.width, threadIdx.x, kSumThreads);
         r = end;
     }
 }
@@ -623,11 +636,16 @@ drs_status sort_tokens(const SortPlan& s, const Workspace& w, const void* ids, i
 template <typename G, typename T, int kVec> drs_status launch_sums(GradParams a, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms <= 0) return DRS_ERR_CUDA;
-    int x = 32;  // a warp has one piece
-    while (x < kSumThreads && x * kVec < a.width) x *= 2;
-    a.columns = x;
-    a.across = static_cast<uint32_t>(ceil_div(a.width, static_cast<int64_t>(x) * kVec));
-    a.sum_blocks = ceil_div(a.pieces, kSumThreads / x) * a.across;
+    // threads along the columns: 8 at least, which keeps a CTA's lists within
+    // 32 KB, 32 for the last kernel, whose warps search together
+    const auto lay_out = [&](int least) {
+        int x = least;
+        while (x < kSumThreads && x * kVec < a.width) x *= 2;
+        a.columns = x;
+        a.across = static_cast<uint32_t>(ceil_div(a.width, static_cast<int64_t>(x) * kVec));
+        return ceil_div(a.pieces, kSumThreads / x) * a.across;
+    };
+    a.sum_blocks = lay_out(8);
     int64_t zero_blocks = 0;
     if (!a.accumulate) {
         // Measured for 32768 x 2048 bf16 into 262144 fp32 rows: 335 us with
@@ -638,12 +656,14 @@ template <typename G, typename T, int kVec> drs_status launch_sums(GradParams a,
         rows = rows < even ? rows : even;
         a.zero_rows = static_cast<int32_t>(rows < 1 ? 1 : rows > kMaxZeroRows ? kMaxZeroRows : rows);
         zero_blocks = ceil_div(a.vocab, a.zero_rows);
+        a.zero_across = 8;
+        while (a.zero_across < kSumThreads && a.zero_across * 16 < a.width * sizeof(T)) a.zero_across *= 2;
     }
     if (a.sum_blocks + zero_blocks > INT_MAX) return DRS_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.sum_blocks + zero_blocks));
     cfg.blockDim = dim3(kSumThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(kSumThreads / x) * a.piece * 8;
+    cfg.dynamicSmemBytes = static_cast<size_t>(kSumThreads / a.columns) * a.piece * 8;
     cfg.stream = stream;
     cudaLaunchAttribute dependent[1];
     dependent[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -652,7 +672,9 @@ template <typename G, typename T, int kVec> drs_status launch_sums(GradParams a,
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, grad_sum_kernel<G, T, kVec>, a) != cudaSuccess) return DRS_ERR_CUDA;
     if (a.pieces <= 1) return DRS_OK;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.sum_blocks));
+    const int64_t join_blocks = lay_out(32);
+    if (join_blocks > INT_MAX) return DRS_ERR_UNSUPPORTED;
+    cfg.gridDim = dim3(static_cast<unsigned>(join_blocks));
     cfg.dynamicSmemBytes = 0;
     return cuda_status(cudaLaunchKernelEx(&cfg, grad_join_kernel<T, kVec>, a));
 }

@@ -427,10 +427,13 @@ extern "C" drs_status drs_map_slots(const int32_t* lens, const int32_t* new_lens
     // Few tokens: one launch, 32 of them per warp until the cluster is full.
     // Many: the cluster for the requests, then a launch for the tokens.
     const bool apart = capacity > kSlotCluster * kSlotThreads;
-    const int64_t work = !apart && capacity > requests ? capacity : requests;
-    const int64_t share = apart ? kSlotThreads / 2 : kSlotThreads;
+    // The cluster grows with the requests (256 per CTA), with the tokens that
+    // it maps itself and, apart from them, with the blocks that they may take.
+    int64_t work = requests * 2;
+    if (!apart && capacity > work) work = capacity;
+    if (apart && capacity / block_size > work) work = capacity / block_size;
     int cluster = 1;
-    while (cluster < kSlotCluster && work > cluster * share) cluster *= 2;
+    while (cluster < kSlotCluster && work > int64_t{cluster} * kSlotThreads) cluster *= 2;
     a.cluster = cluster;
     const auto kernel = apart ? slots_kernel<false> : slots_kernel<true>;
     if (cluster > 8 && !prepare_kernel(reinterpret_cast<const void*>(kernel), 0, true)) return DRS_ERR_CUDA;

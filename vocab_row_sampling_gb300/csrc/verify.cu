@@ -400,11 +400,22 @@ extern "C" drs_status drs_verify_drafts(const void* target, drs_dtype target_dty
     a.draft_stride = draft_stride;
     a.vocab = static_cast<int32_t>(vocab);
     a.max_drafts = max_drafts;
-    // CTAs per request: 8192 columns (16 per thread) each at least, up to 8,
-    // or 16 where 8 would leave SMs idle.
+    // CTAs per request: as many as are resident at once (about half an SM's
+    // worth is lost to the grouping of clusters, more with 16), 8192 columns
+    // (32 per thread) each at least. us at 262144 columns with 4, 8 and 16
+    // CTAs: 32 requests 21.7, 14.4, 11.8; 64 requests 23.6, 17.6, 20.3;
+    // 88 requests 26.1, 20.6, -; 95 requests 26.7, 26.4, - (a second wave).
+    // Requests that fill several waves anyway: 32768 columns per CTA (256
+    // requests 52.8, 49.0, 63.7 us; 55.0 with 2), or 65536 where that is one
+    // wave (128 requests 29.5, 30.5).
+    const size_t bytes = dtype_bytes(target_dtype) + (draft ? dtype_bytes(draft_dtype) : 1);
+    const int64_t resident = int64_t{sms} * (bytes >= 6 ? 4 : 5);
     int cluster = 1;
-    const int most = requests * 8 < sms ? kMaxCluster : 8;
-    while (cluster < most && vocab > 8192 * cluster) cluster *= 2;
+    while (cluster < kMaxCluster && vocab > 8192 * cluster &&
+           requests * cluster * 2 <= resident - (cluster < 8 ? sms / 2 : sms * 3 / 2))
+        cluster *= 2;
+    if (vocab > 65536 * cluster)
+        while (cluster < 8 && vocab > 32768 * cluster) cluster *= 2;
     a.cluster = cluster;
     a.part = static_cast<int32_t>(ceil_div(ceil_div(vocab, cluster * kVerifyWarps), kStep) * kStep);
 
