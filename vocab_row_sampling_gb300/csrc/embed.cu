@@ -13,9 +13,14 @@
 namespace drs {
 namespace {
 
-// Threads per CTA, for rows off 16-byte boundaries and for aligned ones:
-// 65536 x 4096 bf16 takes 117 us with 64 or 128, 120 with 256, 125 with 512.
-constexpr int kThreadsOf[2] = {256, 128};
+// Threads per CTA: 65536 x 4096 bf16 takes 117 us with 64 or 128, 120 with
+// 256, 125 with 512.
+constexpr int kAlignedThreads = 128;
+// Rows off 16-byte boundaries: threads per CTA and words per thread. us for
+// 30000 x 4095 and 5003 x 1283 16-bit elements: 57.5 and 4.7 with 128 and 4,
+// 62.2 and 4.8 with 256 and 4, 64.9 and 5.4 with 128 and 2.
+constexpr int kOddThreads = 128;
+constexpr int kWords = 4;
 
 struct EmbedParams {
     const void* table;
@@ -36,116 +41,111 @@ template <typename T> __device__ __forceinline__ uint4 scaled(uint4 v, float sca
     return v;
 }
 
-// The 16 bytes that begin `shift` bytes into the 32 bytes of lo and hi.
-__device__ __forceinline__ uint4 joined(uint4 lo, uint4 hi, int shift) {
-    uint32_t w[5] = {lo.x, lo.y, lo.z, lo.w, hi.x};
-    if (shift >= 8) w[0] = lo.z, w[1] = lo.w, w[2] = hi.x, w[3] = hi.y, w[4] = hi.z;
-    if (shift & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = shift >= 8 ? hi.w : hi.y;
-    const int bits = (shift & 3) * 8;
-    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-}
-
-// kAligned: every row of the table and of the output starts on 16 bytes. A
-// thread has word `c` of its rows, and in rows that do not also an element of
-// their edges.
-template <typename T, typename I, bool kAligned, int kEmbedRows>
-__global__ void __launch_bounds__(kThreadsOf[kAligned]) embed_kernel(const EmbedParams a) {
+template <typename T, typename I, int kRows>
+__global__ void __launch_bounds__(kAlignedThreads) embed_kernel(const EmbedParams a) {
     constexpr int kVec = 16 / sizeof(T);
     const T* const table = static_cast<const T*>(a.table);
     const I* const ids = static_cast<const I*>(a.ids);
     T* const out = static_cast<T*>(a.out);
     const int64_t block = blockIdx.x / a.columns;
-    const int c = (blockIdx.x % a.columns) * blockDim.x + threadIdx.x;
-    const int64_t t0 = block * (blockDim.y * kEmbedRows) + threadIdx.y;
-    if (kAligned && c * kVec >= a.width) return;
-    int64_t id[kEmbedRows];
+    const int col = ((blockIdx.x % a.columns) * blockDim.x + threadIdx.x) * kVec;
+    const int64_t t0 = block * (blockDim.y * kRows) + threadIdx.y;
+    if (col >= a.width) return;
+    int64_t id[kRows];
 #pragma unroll
-    for (int r = 0; r < kEmbedRows; ++r) {
+    for (int r = 0; r < kRows; ++r) {
         const int64_t t = t0 + r * blockDim.y;
         const int64_t v = t < a.tokens ? static_cast<int64_t>(ids[t]) : -1;
         id[r] = v >= 0 && v < a.vocab ? v : -1;
     }
-    if constexpr (kAligned) {
-        uint4 v[kEmbedRows];
+    uint4 v[kRows];
 #pragma unroll
-        for (int r = 0; r < kEmbedRows; ++r)
-            v[r] = id[r] >= 0 ? load16(table + id[r] * a.table_stride + c * kVec) : make_uint4(0, 0, 0, 0);
+    for (int r = 0; r < kRows; ++r)
+        v[r] = id[r] >= 0 ? load16(table + id[r] * a.table_stride + col) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int r = 0; r < kEmbedRows; ++r) {
-            const int64_t t = t0 + r * blockDim.y;
-            if (t >= a.tokens) continue;
-            if (id[r] >= 0) v[r] = scaled<T>(v[r], a.scale);
-            __stcs(reinterpret_cast<uint4*>(out + t * a.out_stride + c * kVec), v[r]);
-        }
-    } else {
-        uint4 lo[kEmbedRows], hi[kEmbedRows];
-        T edge[kEmbedRows];
-        int at[kEmbedRows], shift[kEmbedRows], edge_at[kEmbedRows];  // -1: nothing here
-#pragma unroll
-        for (int r = 0; r < kEmbedRows; ++r) {
-            const int64_t t = t0 + r * blockDim.y;
-            at[r] = edge_at[r] = -1;
-            lo[r] = hi[r] = make_uint4(0, 0, 0, 0);
-            edge[r] = from_f<T>(0.0f);
-            if (t >= a.tokens) continue;
-            const T* const src = table + max(id[r], static_cast<int64_t>(0)) * a.table_stride;
-            const int head = min(static_cast<int>((-reinterpret_cast<uintptr_t>(out + t * a.out_stride) & 15) / sizeof(T)), a.width);
-            const int off = static_cast<int>(reinterpret_cast<uintptr_t>(src + head) & 15) / static_cast<int>(sizeof(T));
-            // words [w0, w1) of the row come from words that lie inside the
-            // table's row; the elements before and after (at most 4 kVec) one
-            // by one
-            const int words = (a.width - head) / kVec;
-            const int w0 = head < off ? 1 : 0;
-            const int w1 = off && head - off + (words + 1) * kVec > a.width ? words - 1 : words;
-            const int lead = w0 < w1 ? head + w0 * kVec : a.width, trail = w0 < w1 ? head + w1 * kVec : a.width;
-            if (c >= w0 && c < w1) {
-                at[r] = head + c * kVec;
-                shift[r] = off * static_cast<int>(sizeof(T));
-                if (id[r] >= 0) {
-                    lo[r] = load16(src + at[r] - off);
-                    if (off) hi[r] = load16(src + at[r] - off + kVec);
-                }
-            }
-            if (c < lead + a.width - trail) {
-                edge_at[r] = c < lead ? c : trail + c - lead;
-                if (id[r] >= 0) edge[r] = src[edge_at[r]];
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < kEmbedRows; ++r) {
-            T* const dst = out + (t0 + r * blockDim.y) * a.out_stride;
-            if (at[r] >= 0) __stcs(reinterpret_cast<uint4*>(dst + at[r]), scaled<T>(joined(lo[r], hi[r], shift[r]), a.scale));
-            if (edge_at[r] >= 0) dst[edge_at[r]] = id[r] >= 0 ? from_f<T>(to_f(edge[r]) * a.scale) : edge[r];
-        }
+    for (int r = 0; r < kRows; ++r) {
+        const int64_t t = t0 + r * blockDim.y;
+        if (t >= a.tokens) continue;
+        if (id[r] >= 0) v[r] = scaled<T>(v[r], a.scale);
+        __stcs(reinterpret_cast<uint4*>(out + t * a.out_stride + col), v[r]);
     }
 }
 
-template <typename T, typename I, bool kAligned, int kRows>
-drs_status launch_embed_rows(EmbedParams a, int64_t places, cudaStream_t stream) {
-    constexpr int kThreads = kThreadsOf[kAligned];
-    a.columns = static_cast<int32_t>(ceil_div(places, kThreads));
+// Rows off 16-byte boundaries: a thread has up to kWords aligned words of one
+// output row, and perhaps one element of the row's edges.
+template <typename T, typename I> __global__ void __launch_bounds__(kOddThreads) embed_odd_kernel(const EmbedParams a) {
+    constexpr int kVec = 16 / sizeof(T);
+    const int64_t t = static_cast<int64_t>(blockIdx.x / a.columns) * blockDim.y + threadIdx.y;
+    if (t >= a.tokens) return;
+    const int c = (blockIdx.x % a.columns) * (blockDim.x * kWords) + threadIdx.x;
+    const int64_t id = static_cast<int64_t>(static_cast<const I*>(a.ids)[t]);
+    const bool have = id >= 0 && id < a.vocab;
+    const T* const src = static_cast<const T*>(a.table) + (have ? id : 0) * a.table_stride;
+    T* const dst = static_cast<T*>(a.out) + t * a.out_stride;
+    const int head = min(static_cast<int>((-reinterpret_cast<uintptr_t>(dst) & 15) / sizeof(T)), a.width);
+    const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(src + head) & 15);
+    const int off = shift / static_cast<int>(sizeof(T));
+    // words [w0, w1) of the row come from words that lie inside the table's
+    // row; the elements before and after (at most 4 kVec - 2) one by one
+    const int words = (a.width - head) / kVec;
+    const int w0 = head < off ? 1 : 0;
+    const int w1 = off && head - off + (words + 1) * kVec > a.width ? words - 1 : words;
+    const T* const from = src + (head - off);
+    uint4 lo[kWords], hi[kWords];
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+        const int w = c + k * blockDim.x;
+        lo[k] = hi[k] = make_uint4(0, 0, 0, 0);
+        if (have && w >= w0 && w < w1) {
+            lo[k] = load16(from + w * kVec);
+            if (off) hi[k] = load16(from + (w + 1) * kVec);
+        }
+    }
+    const int lead = w0 < w1 ? head + w0 * kVec : a.width, trail = w0 < w1 ? head + w1 * kVec : a.width;
+    if (c < lead + a.width - trail) {
+        const int i = c < lead ? c : trail + c - lead;
+        dst[i] = from_f<T>(have ? to_f(src[i]) * a.scale : 0.0f);
+    }
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) {
+        const int w = c + k * blockDim.x;
+        if (w < w0 || w >= w1) continue;
+        const uint4 v = joined(lo[k], hi[k], shift);
+        __stcs(reinterpret_cast<uint4*>(dst + head + w * kVec), have ? scaled<T>(v, a.scale) : lo[k]);
+    }
+}
+
+template <typename T, typename I, int kRows> drs_status launch_rows(EmbedParams a, cudaStream_t stream) {
+    const int64_t places = a.width / (16 / sizeof(T));  // a word per thread along the columns
+    a.columns = static_cast<int32_t>(ceil_div(places, kAlignedThreads));
     int x = static_cast<int>(ceil_div(places, a.columns));
     if (x > 32) x = (x + 31) / 32 * 32;
-    const dim3 block(x, kThreads / x);
+    const dim3 block(x, kAlignedThreads / x);
     const int64_t blocks = ceil_div(a.tokens, block.y * kRows) * a.columns;
     if (blocks > INT32_MAX) return DRS_ERR_UNSUPPORTED;
-    embed_kernel<T, I, kAligned, kRows><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
+    embed_kernel<T, I, kRows><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
     return cuda_status(cudaGetLastError());
 }
 
-template <typename T, typename I> drs_status launch_embed(const EmbedParams& a, bool vec, cudaStream_t stream) {
+template <typename T, typename I> drs_status launch_embed(EmbedParams a, bool vec, cudaStream_t stream) {
     constexpr int kVec = 16 / sizeof(T);
-    // threads along the columns: a word each, and in rows off 16-byte
-    // boundaries at least one for each of the (at most 4 kVec - 2) elements of
-    // a row's edges
-    int64_t places = a.width / kVec;
-    if (!vec) return launch_embed_rows<T, I, false, 2>(a, places < 4 * kVec ? 4 * kVec : places, stream);
-    // Tokens per thread, measured: 65536 x 4096 bf16 takes 164 us with one, 125
-    // with two, 120 with four and 122 with eight; 256 x 2048 takes 1.9 us with
-    // one or two, 2.2 with four, 3.0 with eight.
-    const bool many = a.tokens * places > int64_t{8192} * sm_count();
-    return many ? launch_embed_rows<T, I, true, 4>(a, places, stream) : launch_embed_rows<T, I, true, 2>(a, places, stream);
+    const int64_t words = a.width / kVec;
+    if (vec) {
+        // Tokens per thread, measured: 65536 x 4096 bf16 takes 164 us with one,
+        // 125 with two, 120 with four and 122 with eight; 256 x 2048 takes 1.9
+        // us with one or two, 2.2 with four, 3.0 with eight.
+        const bool many = a.tokens * words > int64_t{8192} * sm_count();
+        return many ? launch_rows<T, I, 4>(a, stream) : launch_rows<T, I, 2>(a, stream);
+    }
+    a.columns = static_cast<int32_t>(ceil_div(words, kOddThreads * kWords));
+    if (a.columns < 1) a.columns = 1;
+    int x = static_cast<int>(ceil_div(words, int64_t{a.columns} * kWords));
+    if (x < 32) x = 32;  // one for each of the elements of a row's edges
+    const dim3 block(x, kOddThreads / x);
+    const int64_t blocks = ceil_div(a.tokens, block.y) * a.columns;
+    if (blocks > INT32_MAX) return DRS_ERR_UNSUPPORTED;
+    embed_odd_kernel<T, I><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
+    return cuda_status(cudaGetLastError());
 }
 
 }  // namespace

@@ -73,6 +73,37 @@ template <> __device__ __forceinline__ void Raw8<__half>::unpack(float (&v)[8]) 
     }
 }
 
+// The 16 bytes that begin `shift` bytes into the 32 bytes of lo and hi.
+__device__ __forceinline__ uint4 joined(uint4 lo, uint4 hi, int shift) {
+    uint32_t w[5] = {lo.x, lo.y, lo.z, lo.w, hi.x};
+    if (shift >= 8) w[0] = lo.z, w[1] = lo.w, w[2] = hi.x, w[3] = hi.y, w[4] = hi.z;
+    if (shift & 4) w[0] = w[1], w[1] = w[2], w[2] = w[3], w[3] = w[4], w[4] = shift >= 8 ? hi.w : hi.y;
+    const int bits = (shift & 3) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                      __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// Eight consecutive elements that start anywhere inside a 16-byte word: the
+// words that hold them, and one more where they reach into it.
+template <typename T> struct Raw8Shifted {
+    uint4 w[sizeof(T) / 2 + 1];
+    // first: the start of the word that holds the first element, `shift`
+    // bytes before it
+    __device__ __forceinline__ void load(const T* first, int shift) {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+            w[i] = load16_stream(reinterpret_cast<const char*>(first) + 16 * i);
+        w[sizeof(T) / 2] = make_uint4(0, 0, 0, 0);
+        if (shift) w[sizeof(T) / 2] = load16_stream(reinterpret_cast<const char*>(first) + 8 * sizeof(T));
+    }
+    __device__ __forceinline__ void unpack(int shift, float (&v)[8]) const {
+        Raw8<T> r;
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.w[i] = joined(w[i], w[i + 1], shift);
+        r.unpack(v);
+    }
+};
+
 // ------------------------------------------------------------- scans
 
 template <typename T> __device__ __forceinline__ T warp_scan_inclusive(T v, int lane) {

@@ -40,8 +40,9 @@ struct NoDraft {};
 
 // CTAs per SM that registers are held to: 5 (51 registers) measured 49.5 us
 // for 256 requests of 262144 columns, 4 with twice the loads in flight 49.6, 3
-// 53.7, 6 50.4 and 8 53.7; two fp32 rows spill at 5.
-template <typename P, typename Q> constexpr int kResident = sizeof(P) + sizeof(Q) >= 6 ? 4 : 5;
+// 53.7, 6 50.4 and 8 53.7; fp32 rows spill at 5. bytes: of an element of
+// both rows.
+constexpr int resident_ctas(size_t bytes) { return bytes < 6 ? 5 : 4; }
 
 struct VerifyParams {
     const void* target;
@@ -58,11 +59,11 @@ struct VerifyParams {
 
 // The row (or pair of rows) a request draws from. q is null where nothing
 // is subtracted; `without` is a column whose weight is 0 (-1: none).
-template <typename P, typename Q> struct Weights {
+// kVec: the rows start 16-byte aligned.
+template <typename P, typename Q, bool kVec> struct Weights {
     const P* p;
     const Q* q;
-    int without;
-    bool vec;  // both rows start 16-byte aligned
+    int without, vocab;
 
     __device__ __forceinline__ float one(int i) const {
         float w = to_f(p[i]);
@@ -72,7 +73,7 @@ template <typename P, typename Q> struct Weights {
         return i == without ? 0.0f : fmaxf(w, 0.0f);  // NaN counts as 0
     }
 
-    // Eight columns from i on (i a multiple of 8, i + 8 <= vocab).
+    // Eight columns from i on.
     template <bool kSub> __device__ __forceinline__ void finish(const Raw8<P>& rp, const float (&qv)[8], int i,
                                                                 float (&w)[8]) const {
         rp.unpack(w);
@@ -91,7 +92,7 @@ template <typename P, typename Q> struct Weights {
 
     // Columns i .. i+7 (i a multiple of 8), 0 from `end` on.
     __device__ __forceinline__ void load(int64_t i, int end, float (&w)[8]) const {
-        if (vec && i + 8 <= end) {
+        if (kVec && i + 8 <= end) {
             Raw8<P> rp;
             rp.load(p + i);
             if constexpr (!std::is_same<Q, NoDraft>::value) {
@@ -128,11 +129,11 @@ __device__ __forceinline__ int pick(const Pair* share, int n, int lane, Pair t, 
 
 // The sum of the weights of columns [begin, end), begin a multiple of kStep,
 // by one warp; every lane gets its own part.
-template <bool kSub, typename P, typename Q>
-__device__ __forceinline__ Pair lane_sum(const Weights<P, Q>& wt, int begin, int end, int lane) {
+template <bool kSub, typename P, typename Q, bool kVec>
+__device__ __forceinline__ Pair lane_sum(const Weights<P, Q, kVec>& wt, int begin, int end, int lane) {
     PairSum2 sum;
-    if (wt.vec) {
-        constexpr int kUnroll = 2;
+    if constexpr (kVec) {
+        constexpr int kUnroll = kSub || sizeof(P) == 4 ? 2 : 4;  // 2 KB of a warp's loads in flight
         int i = begin + 8 * lane;
         for (; i + (kUnroll - 1) * kStep + 8 <= end; i += kUnroll * kStep) {
             Raw8<P> rp[kUnroll];
@@ -169,22 +170,56 @@ __device__ __forceinline__ Pair lane_sum(const Weights<P, Q>& wt, int begin, int
             }
         }
     } else {
-        // rows off 16-byte boundaries: single elements, 8 in flight
-        int i = begin + lane;
-        for (; i + 7 * 32 < end; i += kStep) {
-            float w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = wt.one(i + 32 * e);
-#pragma unroll
-            for (int e = 0; e < 8; e += 2) sum.add(pack2(w[e], w[e + 1]));
+        // Rows off 16-byte boundaries: groups of 8 columns from a boundary of p
+        // on, their q put together from the words that hold them; the columns
+        // before and after (and those whose words would leave the row) one by
+        // one. Single elements throughout took 58 us for 256 requests of 200001
+        // columns.
+        using R = typename std::conditional<kSub, Q, P>::type;
+        [[maybe_unused]] constexpr int kWord = 16 / sizeof(R);
+        int i0 = begin + static_cast<int>((-reinterpret_cast<uintptr_t>(wt.p + begin) & 15) / sizeof(P));
+        int shift = 0, off = 0, most = end;
+        if constexpr (kSub) {
+            shift = static_cast<int>(reinterpret_cast<uintptr_t>(wt.q + i0) & 15);
+            off = shift / static_cast<int>(sizeof(R));
+            if (i0 < off) i0 += 8;
+            if (off) most = min(end, wt.vocab - kWord + off);
         }
-        for (; i < end; i += 32) sum.add(pack2(wt.one(i), 0.0f));
+        const int groups = most > i0 ? (most - i0) / 8 : 0, i1 = groups ? i0 + 8 * groups : begin;
+        if (!groups) i0 = begin;
+        if constexpr (kSub) {
+#pragma unroll 1
+            for (int i = i0 + 8 * lane; i < i1; i += kStep) {
+                Raw8<P> rp;
+                Raw8Shifted<R> rq;
+                rp.load(wt.p + i);
+                rq.load(wt.q + i - off, shift);
+                float qv[8], w[8];
+                rq.unpack(shift, qv);
+                wt.template finish<true>(rp, qv, i, w);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) sum.add(pack2(w[e], w[e + 1]));
+            }
+        } else {
+#pragma unroll 2
+            for (int i = i0 + 8 * lane; i < i1; i += kStep) {
+                Raw8<P> rp;
+                float w[8];
+                rp.load(wt.p + i);
+                wt.template finish<false>(rp, w, i, w);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) sum.add(pack2(w[e], w[e + 1]));
+            }
+        }
+        for (int i = begin + lane; i < i0; i += 32) sum.add(pack2(wt.one(i), 0.0f));
+        for (int i = i1 + lane; i < end; i += 32) sum.add(pack2(wt.one(i), 0.0f));
     }
     return sum.value();
 }
 
-template <typename P, typename Q>
-__global__ void __launch_bounds__(kVerifyThreads, kResident<P, Q>) verify_kernel(const VerifyParams a) {
+template <typename P, typename Q, bool kVec>
+__global__ void __launch_bounds__(kVerifyThreads, resident_ctas(sizeof(P) + sizeof(Q)))
+    verify_kernel(const VerifyParams a) {
     constexpr bool kDraft = !std::is_same<Q, NoDraft>::value;
     __shared__ __align__(8) Pair s_cta[2][kMaxCluster];  // the CTAs' totals, by attempt
     __shared__ Pair s_warp[kVerifyWarps];                // this CTA's warps' totals
@@ -240,15 +275,14 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident<P, Q>) verify_kernel
         if (tid == 0) a.out_accepted[b] = accepted;
     }
 
-    Weights<P, Q> wt;
+    Weights<P, Q, kVec> wt;
     wt.p = target + accepted * a.target_stride;
     wt.q = nullptr;
     wt.without = -1;
-    wt.vec = (reinterpret_cast<uintptr_t>(wt.p) & 15) == 0;
+    wt.vocab = a.vocab;
     if (!whole) {
         if constexpr (kDraft) {
             wt.q = static_cast<const Q*>(a.draft) + (first + accepted) * a.draft_stride;
-            wt.vec = wt.vec && (reinterpret_cast<uintptr_t>(wt.q) & 15) == 0;
         } else {
             const int64_t x = a.tokens[first + accepted];
             if (x >= 0 && x < a.vocab) wt.without = static_cast<int>(x);
@@ -293,7 +327,6 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident<P, Q>) verify_kernel
         used = 1;
         wt.q = nullptr;
         wt.without = -1;
-        wt.vec = (reinterpret_cast<uintptr_t>(wt.p) & 15) == 0;
     }
     if (!(total.s > 0.0f)) {  // no mass anywhere
         if (rank == 0 && tid == 0) out[accepted] = -1;
@@ -356,9 +389,13 @@ __global__ void __launch_bounds__(kVerifyThreads, kResident<P, Q>) verify_kernel
 
 using VerifyKernel = void (*)(VerifyParams);
 
-template <typename P> VerifyKernel verify_kernel_for(bool draft, drs_dtype t) {
-    if (!draft) return verify_kernel<P, NoDraft>;
-    return with_dtype(t, [](auto q) -> VerifyKernel { return verify_kernel<P, decltype(q)>; });
+template <typename P, typename Q> VerifyKernel verify_kernel_of(bool vec) {
+    return vec ? verify_kernel<P, Q, true> : verify_kernel<P, Q, false>;
+}
+
+template <typename P> VerifyKernel verify_kernel_for(bool draft, drs_dtype t, bool vec) {
+    if (!draft) return verify_kernel_of<P, NoDraft>(vec);
+    return with_dtype(t, [vec](auto q) -> VerifyKernel { return verify_kernel_of<P, decltype(q)>(vec); });
 }
 
 }  // namespace
@@ -405,23 +442,26 @@ extern "C" drs_status drs_verify_drafts(const void* target, drs_dtype target_dty
     // (32 per thread) each at least. us at 262144 columns with 4, 8 and 16
     // CTAs: 32 requests 21.7, 14.4, 11.8; 64 requests 23.6, 17.6, 20.3;
     // 88 requests 26.1, 20.6, -; 95 requests 26.7, 26.4, - (a second wave).
-    // Requests that fill several waves anyway: 32768 columns per CTA (256
-    // requests 52.8, 49.0, 63.7 us; 55.0 with 2), or 65536 where that is one
-    // wave (128 requests 29.5, 30.5).
+    // Requests that fill several waves anyway: 32768 columns of 4 bytes per CTA
+    // (256 requests 52.8, 49.0, 63.7 us; 55.0 with 2), or 65536 where that is
+    // one wave (128 requests 29.5, 30.5).
     const size_t bytes = dtype_bytes(target_dtype) + (draft ? dtype_bytes(draft_dtype) : 1);
-    const int64_t resident = int64_t{sms} * (bytes >= 6 ? 4 : 5);
+    const bool vec = aligned(target, 16) && target_stride * dtype_bytes(target_dtype) % 16 == 0 &&
+                     (!draft || (aligned(draft, 16) && draft_stride * dtype_bytes(draft_dtype) % 16 == 0));
+    const int64_t resident = int64_t{sms} * resident_ctas(bytes);
     int cluster = 1;
     while (cluster < kMaxCluster && vocab > 8192 * cluster &&
            requests * cluster * 2 <= resident - (cluster < 8 ? sms / 2 : sms * 3 / 2))
         cluster *= 2;
-    if (vocab > 65536 * cluster)
-        while (cluster < 8 && vocab > 32768 * cluster) cluster *= 2;
+    const int64_t row = vocab * static_cast<int64_t>(draft ? bytes : bytes - 1);
+    if (row > (int64_t{1} << 18) * cluster)
+        while (cluster < 8 && row > (int64_t{1} << 17) * cluster) cluster *= 2;
     a.cluster = cluster;
     a.part = static_cast<int32_t>(ceil_div(ceil_div(vocab, cluster * kVerifyWarps), kStep) * kStep);
 
     const bool has_draft = draft != nullptr;
     const VerifyKernel kernel = with_dtype(target_dtype, [&](auto p) -> VerifyKernel {
-        return verify_kernel_for<decltype(p)>(has_draft, draft_dtype);
+        return verify_kernel_for<decltype(p)>(has_draft, draft_dtype, vec);
     });
     if (cluster > 8 && !prepare_kernel(reinterpret_cast<const void*>(kernel), 0, true)) return DRS_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
