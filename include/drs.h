@@ -574,7 +574,8 @@ size_t drs_embed_tokens_grad_workspace_bytes(int64_t tokens, int64_t vocab, int6
  * Returns DRS_ERR_INVALID_ARG for sizes out of range, an unknown type, a
  * stride below width, a null or unaligned pointer or a small workspace;
  * DRS_ERR_UNSUPPORTED for sizes above DRS_MAX_TOKENS, DRS_MAX_VOCAB or
- * DRS_MAX_WIDTH.
+ * DRS_MAX_WIDTH, or too many tokens and columns for one launch (2^31 - 1
+ * blocks).
  */
 drs_status drs_embed_tokens_grad(const void *grad_out, drs_dtype grad_dtype, int64_t tokens,
                                  int64_t width, int64_t grad_stride, const void *ids,

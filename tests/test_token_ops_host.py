@@ -88,6 +88,8 @@ def _grad(lib, grad=FAKE, g=1, tokens=4, width=8, gstride=8, ids=FAKE, bits=64, 
     ({"grad": FAKE + 1}, INV), ({"table": FAKE + 2}, INV), ({"ids": FAKE + 4}, INV),
     ({"vocab": drs.DRS_MAX_VOCAB + 1}, UNS), ({"tokens": drs.DRS_MAX_TOKENS + 1}, UNS),
     ({"width": drs.DRS_MAX_WIDTH + 1, "tstride": 1 << 21, "gstride": 1 << 21}, UNS),
+    # more CTAs than a launch has: refused before the sort is launched
+    ({"tokens": drs.DRS_MAX_TOKENS, "width": drs.DRS_MAX_WIDTH - 1, "tstride": 1 << 20, "gstride": 1 << 20}, UNS),
 ])
 def test_grad_argument_checks(lib, kw, expect):
     assert _grad(lib, **kw) == expect

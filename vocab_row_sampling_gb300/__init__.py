@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 from . import _build
@@ -312,27 +313,30 @@ def _dtype_code(t, name: str) -> int:
     return code
 
 
-def _raw_stream(stream, device) -> int:
+def _raw_stream(stream, gpu: int) -> int:
     """The stream of a call: torch.cuda.current_stream() alone takes 3 us,
     more than a launch."""
     if stream is not None:
         return stream.cuda_stream
     import torch
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return torch._C._cuda_getCurrentRawStream(gpu)
 
 
-def _need(t, name: str, dtype, shape, device):
-    """A contiguous tensor of this type and shape on this device."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous {dtype} {tuple(shape)} on {device} expected, got {t.dtype} "
-                         f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
+def _vector(t, name: str, dtype, n: int, gpu: int) -> int:
+    """The address of a contiguous tensor of n elements of this type on this
+    GPU."""
+    if t.dtype is dtype and t.numel() == n and t.get_device() == gpu and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: contiguous {dtype} with {n} elements on cuda:{gpu} expected, got {t.dtype} "
+                     f"{tuple(t.shape)} on {t.device}, strides {t.stride()}")
 
 
-def _need_rows(t, name: str, device=None):
-    """A 2-D tensor with unit column stride (any row stride) on a GPU;
-    returns the row stride."""
-    if t.dim() != 2 or not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name}: 2-D on {device or 'a CUDA device'} expected, got {t.dim()}-D on {t.device}")
+def _rows(t, name: str, gpu: int = -1) -> int:
+    """The row stride of a 2-D tensor with unit column stride on a GPU (this
+    one when given)."""
+    if t.dim() != 2 or not t.is_cuda or (gpu >= 0 and t.get_device() != gpu):
+        raise ValueError(f"{name}: 2-D on {f'cuda:{gpu}' if gpu >= 0 else 'a CUDA device'} expected, got {t.dim()}-D "
+                         f"on {t.device}")
     rows, columns = t.shape
     step, unit = t.stride()
     if rows == 0 or columns == 0:
@@ -347,32 +351,28 @@ def drs_verify_drafts(target, draft, draft_tokens, cu_drafts, accept_u, sample_u
     """Launch drs_verify_drafts: target [drafts + requests, vocab], draft
     [drafts, vocab] or None, out_tokens int64 [requests, max_drafts + 1]."""
     import torch
-    dev = target.device
-    target_stride = _need_rows(target, "target")
-    target_code = _dtype_code(target, "target")
+    target_stride = _rows(target, "target")
+    gpu = target.get_device()
     target_rows, vocab = target.shape
-    drafts = draft_tokens.numel()
-    draft_code, draft_stride = 0, 0
+    drafts, requests = draft_tokens.numel(), sample_u.numel()
+    draft_ptr, draft_code, draft_stride = None, 0, 0
     if draft is not None:
-        draft_stride = _need_rows(draft, "draft", dev)
+        draft_stride = _rows(draft, "draft", gpu)
         draft_code = _dtype_code(draft, "draft")
         if draft.shape != (drafts, vocab):
             raise ValueError(f"draft: {(drafts, vocab)} expected, got {tuple(draft.shape)}")
-    requests = sample_u.numel()
-    _need(draft_tokens, "draft_tokens", torch.int64, (drafts,), dev)
-    _need(accept_u, "accept_u", torch.float32, (drafts,), dev)
-    _need(cu_drafts, "cu_drafts", torch.int32, (requests + 1,), dev)
-    _need(sample_u, "sample_u", torch.float32, (requests,), dev)
-    if out_tokens.dim() != 2 or out_tokens.shape[1] < 1:
-        raise ValueError(f"out_tokens: [requests, max_drafts + 1] expected, got {tuple(out_tokens.shape)}")
-    _need(out_tokens, "out_tokens", torch.int64, (requests, out_tokens.shape[1]), dev)
-    _need(out_accepted, "out_accepted", torch.int32, (requests,), dev)
-    st = load().drs_verify_drafts(target.data_ptr(), target_code, target_rows, target_stride,
-                                  None if draft is None else draft.data_ptr(), draft_code, drafts,
-                                  draft_stride, vocab, draft_tokens.data_ptr(), cu_drafts.data_ptr(),
-                                  requests, out_tokens.shape[1] - 1, accept_u.data_ptr(),
-                                  sample_u.data_ptr(), out_tokens.data_ptr(), out_accepted.data_ptr(),
-                                  _raw_stream(stream, dev))
+        draft_ptr = draft.data_ptr()
+    if out_tokens.dim() != 2 or out_tokens.shape[0] != requests or out_tokens.shape[1] < 1:
+        raise ValueError(f"out_tokens: [{requests}, max_drafts + 1] expected, got {tuple(out_tokens.shape)}")
+    width = out_tokens.shape[1]
+    st = load().drs_verify_drafts(
+        target.data_ptr(), _dtype_code(target, "target"), target_rows, target_stride, draft_ptr, draft_code, drafts,
+        draft_stride, vocab, _vector(draft_tokens, "draft_tokens", torch.int64, drafts, gpu),
+        _vector(cu_drafts, "cu_drafts", torch.int32, requests + 1, gpu), requests, width - 1,
+        _vector(accept_u, "accept_u", torch.float32, drafts, gpu),
+        _vector(sample_u, "sample_u", torch.float32, requests, gpu),
+        _vector(out_tokens, "out_tokens", torch.int64, requests * width, gpu),
+        _vector(out_accepted, "out_accepted", torch.int32, requests, gpu), _raw_stream(stream, gpu))
     _check(st, "drs_verify_drafts")
 
 
@@ -384,53 +384,51 @@ def drs_map_slots(lens, new_lens, held, block_table, block_size: int, free_ring,
     capacity. block_table and free_ring are updated in place; out_held and
     out_ring_state may be held and ring_state."""
     import torch
-    dev = lens.device
     i32, i64 = torch.int32, torch.int64
-    requests, capacity = lens.numel(), out_request.numel()
-    table_stride = _need_rows(block_table, "block_table", dev)
-    if block_table.dtype != i32 or block_table.shape[0] != requests:
+    requests, capacity, ring = lens.numel(), out_request.numel(), free_ring.numel()
+    table_stride = _rows(block_table, "block_table")
+    gpu = block_table.get_device()
+    if block_table.dtype is not i32 or block_table.shape[0] != requests:
         raise ValueError(f"block_table: int32 [{requests}, max_blocks] expected, got {block_table.dtype} "
                          f"{tuple(block_table.shape)}")
-    for t, name, dtype, n in ((lens, "lens", i32, requests), (new_lens, "new_lens", i32, requests),
-                              (held, "held", i32, requests), (free_ring, "free_ring", i32, free_ring.numel()),
-                              (ring_state, "ring_state", i64, 2), (out_cu, "out_cu", i32, requests + 1),
-                              (out_request, "out_request", i32, capacity),
-                              (out_position, "out_position", i32, capacity),
-                              (out_slot, "out_slot", i64, capacity), (out_held, "out_held", i32, requests),
-                              (out_ring_state, "out_ring_state", i64, 2), (out_lacking, "out_lacking", i32, 1)):
-        _need(t, name, dtype, (n,), dev)
-    st = load().drs_map_slots(lens.data_ptr(), new_lens.data_ptr(), held.data_ptr(), requests, block_size,
-                              block_table.data_ptr(), table_stride, block_table.shape[1],
-                              free_ring.data_ptr(), free_ring.numel(), ring_state.data_ptr(), capacity,
-                              out_cu.data_ptr(), out_request.data_ptr(), out_position.data_ptr(),
-                              out_slot.data_ptr(), out_held.data_ptr(), out_ring_state.data_ptr(),
-                              out_lacking.data_ptr(), _raw_stream(stream, dev))
+    st = load().drs_map_slots(
+        _vector(lens, "lens", i32, requests, gpu), _vector(new_lens, "new_lens", i32, requests, gpu),
+        _vector(held, "held", i32, requests, gpu), requests, block_size, block_table.data_ptr(), table_stride,
+        block_table.shape[1], _vector(free_ring, "free_ring", i32, ring, gpu), ring,
+        _vector(ring_state, "ring_state", i64, 2, gpu), capacity, _vector(out_cu, "out_cu", i32, requests + 1, gpu),
+        _vector(out_request, "out_request", i32, capacity, gpu),
+        _vector(out_position, "out_position", i32, capacity, gpu), _vector(out_slot, "out_slot", i64, capacity, gpu),
+        _vector(out_held, "out_held", i32, requests, gpu),
+        _vector(out_ring_state, "out_ring_state", i64, 2, gpu),
+        _vector(out_lacking, "out_lacking", i32, 1, gpu), _raw_stream(stream, gpu))
     _check(st, "drs_map_slots")
 
 
-def _id_bits(ids, dev) -> int:
+def _id_bits(ids) -> int:
     import torch
-    bits = {torch.int32: 32, torch.int64: 64}.get(ids.dtype)
-    if bits is None or ids.dim() != 1 or ids.device != dev or not ids.is_contiguous():
-        raise ValueError(f"ids: contiguous 1-D int32 or int64 on {dev} expected, got {ids.dtype} "
-                         f"{tuple(ids.shape)} on {ids.device}, strides {ids.stride()}")
-    return bits
+    if ids.dtype is torch.int64:
+        return 64
+    if ids.dtype is torch.int32:
+        return 32
+    raise ValueError(f"ids: int32 or int64 expected, got {ids.dtype}")
 
 
 def drs_embed_tokens(table, ids, scale: float, out, stream=None):
     """Launch drs_embed_tokens: table [vocab, width], ids int32 or int64
     [tokens], out [tokens, width] of the table's type."""
-    table_stride, out_stride = _need_rows(table, "table"), _need_rows(out, "out", table.device)
+    gpu = table.get_device()
+    table_stride, out_stride = _rows(table, "table"), _rows(out, "out", gpu)
     vocab, width = table.shape
-    bits = _id_bits(ids, table.device)
-    if out.dtype != table.dtype or out.shape != (ids.numel(), width):
-        raise ValueError(f"out: {table.dtype} {(ids.numel(), width)} expected, got {out.dtype} {tuple(out.shape)}")
+    tokens = ids.numel()
+    if out.dtype is not table.dtype or out.shape != (tokens, width):
+        raise ValueError(f"out: {table.dtype} {(tokens, width)} expected, got {out.dtype} {tuple(out.shape)}")
     st = load().drs_embed_tokens(table.data_ptr(), _dtype_code(table, "table"), vocab, width, table_stride,
-                                 ids.data_ptr(), bits, ids.numel(), scale, out.data_ptr(), out_stride,
-                                 _raw_stream(stream, table.device))
+                                 _vector(ids, "ids", ids.dtype, tokens, gpu), _id_bits(ids), tokens, scale,
+                                 out.data_ptr(), out_stride, _raw_stream(stream, gpu))
     _check(st, "drs_embed_tokens")
 
 
+@functools.lru_cache(maxsize=256)
 def drs_embed_tokens_grad_workspace_bytes(tokens: int, vocab: int, width: int) -> int:
     return int(load().drs_embed_tokens_grad_workspace_bytes(tokens, vocab, width))
 
@@ -439,18 +437,22 @@ def drs_embed_tokens_grad(grad_out, ids, scale: float, accumulate: bool, grad_ta
                           stream=None):
     """Launch drs_embed_tokens_grad: grad_out [tokens, width], grad_table
     [vocab, width] (each fp32, bf16 or fp16)."""
-    grad_stride = _need_rows(grad_out, "grad_out")
-    table_stride = _need_rows(grad_table, "grad_table", grad_out.device)
+    gpu = grad_out.get_device()
+    grad_stride, table_stride = _rows(grad_out, "grad_out"), _rows(grad_table, "grad_table", gpu)
     vocab, width = grad_table.shape
-    bits = _id_bits(ids, grad_out.device)
-    if grad_out.shape != (ids.numel(), width):
-        raise ValueError(f"grad_out: {(ids.numel(), width)} expected, got {tuple(grad_out.shape)}")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    st = load().drs_embed_tokens_grad(grad_out.data_ptr(), _dtype_code(grad_out, "grad_out"), ids.numel(), width,
-                                      grad_stride, ids.data_ptr(), bits, scale, 1 if accumulate else 0,
-                                      grad_table.data_ptr(), _dtype_code(grad_table, "grad_table"), vocab,
-                                      table_stride, None if workspace is None else workspace.data_ptr(),
-                                      ws_bytes, _raw_stream(stream, grad_out.device))
+    tokens = ids.numel()
+    if grad_out.shape != (tokens, width):
+        raise ValueError(f"grad_out: {(tokens, width)} expected, got {tuple(grad_out.shape)}")
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.get_device() != gpu or not workspace.is_contiguous():
+            raise ValueError(f"workspace: contiguous on cuda:{gpu} expected, got {workspace.device}")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = load().drs_embed_tokens_grad(grad_out.data_ptr(), _dtype_code(grad_out, "grad_out"), tokens, width,
+                                      grad_stride, _vector(ids, "ids", ids.dtype, tokens, gpu), _id_bits(ids), scale,
+                                      1 if accumulate else 0, grad_table.data_ptr(),
+                                      _dtype_code(grad_table, "grad_table"), vocab, table_stride, ws, ws_bytes,
+                                      _raw_stream(stream, gpu))
     _check(st, "drs_embed_tokens_grad")
 
 
@@ -660,11 +662,12 @@ def verify_drafts(target_probs, draft_tokens, cu_drafts, accept_u, sample_u, max
     requests = sample_u.numel()
     if max_drafts < 0 or (out_tokens is not None and out_tokens.shape != (requests, max_drafts + 1)):
         raise ValueError(f"out_tokens: [{requests}, max_drafts + 1] with max_drafts {max_drafts} expected")
-    with _allocate_on(stream):
-        if out_tokens is None:
-            out_tokens = torch.empty(requests, max_drafts + 1, dtype=torch.int64, device=target_probs.device)
-        if out_accepted is None:
-            out_accepted = torch.empty(requests, dtype=torch.int32, device=target_probs.device)
+    if out_tokens is None or out_accepted is None:
+        with _allocate_on(stream):
+            if out_tokens is None:
+                out_tokens = torch.empty(requests, max_drafts + 1, dtype=torch.int64, device=target_probs.device)
+            if out_accepted is None:
+                out_accepted = torch.empty(requests, dtype=torch.int32, device=target_probs.device)
     drs_verify_drafts(target_probs, draft_probs, draft_tokens, cu_drafts, accept_u, sample_u, out_tokens,
                       out_accepted, stream)
     return out_tokens, out_accepted
@@ -706,9 +709,13 @@ def embed_tokens_grad(grad_out, ids, scale: float, grad_table, accumulate: bool 
     added) into grad_table [vocab, width], which is returned (see
     drs_embed_tokens_grad)."""
     import torch
-    vocab, width = grad_table.shape
-    with _allocate_on(stream):
-        ws = torch.empty(drs_embed_tokens_grad_workspace_bytes(ids.numel(), vocab, width), dtype=torch.uint8,
-                         device=grad_out.device)
+    if grad_table.dim() != 2:
+        raise ValueError(f"grad_table: [vocab, width] expected, got {tuple(grad_table.shape)}")
+    size = drs_embed_tokens_grad_workspace_bytes(ids.numel(), *grad_table.shape)
+    if stream is None:
+        ws = torch.empty(size, dtype=torch.uint8, device=grad_out.device)
+    else:
+        with _allocate_on(stream):
+            ws = torch.empty(size, dtype=torch.uint8, device=grad_out.device)
     drs_embed_tokens_grad(grad_out, ids, scale, accumulate, grad_table, ws, stream)
     return grad_table

@@ -1,9 +1,7 @@
 // capi.cu -- status strings, the device error flag and launch bookkeeping of
 // libdrs.
 #include <atomic>
-#include <map>
 #include <mutex>
-#include <utility>
 
 #include "drs_internal.h"
 
@@ -87,25 +85,36 @@ int sm_count() {
 
 namespace {
 struct Prepared {
+    const void* kernel = nullptr;
+    int device = 0;
     size_t smem = 0;
     bool wide = false;
 };
-std::map<std::pair<const void*, int>, Prepared> g_prepared;
+constexpr int kPrepared = 128;
+Prepared g_prepared[kPrepared];
 }  // namespace
 
 bool prepare_kernel(const void* kernel, size_t smem, bool wide_cluster) {
     const int dev = current_device();
     if (dev < 0) return false;
     std::lock_guard<std::mutex> lock(g_mutex);
-    Prepared& p = g_prepared[{kernel, dev}];
-    if (smem > p.smem) {
+    Prepared unknown;  // a kernel past the table's end is prepared every time
+    Prepared* p = &unknown;
+    for (Prepared& q : g_prepared) {
+        if (q.kernel && (q.kernel != kernel || q.device != dev)) continue;
+        p = &q;
+        break;
+    }
+    p->kernel = kernel;
+    p->device = dev;
+    if (smem > p->smem) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
             return false;
-        p.smem = smem;
+        p->smem = smem;
     }
-    if (wide_cluster && !p.wide) {
+    if (wide_cluster && !p->wide) {
         if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
-        p.wide = true;
+        p->wide = true;
     }
     return true;
 }

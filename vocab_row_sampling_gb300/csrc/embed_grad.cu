@@ -633,19 +633,41 @@ drs_status sort_tokens(const SortPlan& s, const Workspace& w, const void* ids, i
     return cuda_status(cudaGetLastError());
 }
 
+// Threads of a CTA along the columns (`least` at least), and the CTAs of all
+// pieces.
+struct SumLayout {
+    uint32_t columns, across;
+    int64_t blocks;
+    static SumLayout of(const GradParams& a, int vec, int least) {
+        SumLayout l;
+        int x = least;
+        while (x < kSumThreads && int64_t{x} * vec < a.width) x *= 2;
+        l.columns = x;
+        l.across = static_cast<uint32_t>(ceil_div(a.width, int64_t{x} * vec));
+        l.blocks = ceil_div(a.pieces, kSumThreads / x) * l.across;
+        return l;
+    }
+};
+// 8 columns keep a CTA's lists within 32 KB; the last kernel's warps search
+// together.
+constexpr int kSumColumns = 8, kJoinColumns = 32;
+
+// Whether every launch's grid is in range.
+bool grids_ok(const GradParams& a, int vec) {
+    return SumLayout::of(a, vec, kSumColumns).blocks + a.vocab <= INT_MAX &&
+           SumLayout::of(a, vec, kJoinColumns).blocks <= INT_MAX;
+}
+
 template <typename G, typename T, int kVec> drs_status launch_sums(GradParams a, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms <= 0) return DRS_ERR_CUDA;
-    // threads along the columns: 8 at least, which keeps a CTA's lists within
-    // 32 KB, 32 for the last kernel, whose warps search together
     const auto lay_out = [&](int least) {
-        int x = least;
-        while (x < kSumThreads && x * kVec < a.width) x *= 2;
-        a.columns = x;
-        a.across = static_cast<uint32_t>(ceil_div(a.width, static_cast<int64_t>(x) * kVec));
-        return ceil_div(a.pieces, kSumThreads / x) * a.across;
+        const SumLayout l = SumLayout::of(a, kVec, least);
+        a.columns = l.columns;
+        a.across = l.across;
+        return l.blocks;
     };
-    a.sum_blocks = lay_out(8);
+    a.sum_blocks = lay_out(kSumColumns);
     int64_t zero_blocks = 0;
     if (!a.accumulate) {
         // Measured for 32768 x 2048 bf16 into 262144 fp32 rows: 335 us with
@@ -659,7 +681,6 @@ template <typename G, typename T, int kVec> drs_status launch_sums(GradParams a,
         a.zero_across = 8;
         while (a.zero_across < kSumThreads && a.zero_across * 16 < a.width * sizeof(T)) a.zero_across *= 2;
     }
-    if (a.sum_blocks + zero_blocks > INT_MAX) return DRS_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.sum_blocks + zero_blocks));
     cfg.blockDim = dim3(kSumThreads);
@@ -672,9 +693,7 @@ template <typename G, typename T, int kVec> drs_status launch_sums(GradParams a,
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, grad_sum_kernel<G, T, kVec>, a) != cudaSuccess) return DRS_ERR_CUDA;
     if (a.pieces <= 1) return DRS_OK;
-    const int64_t join_blocks = lay_out(32);
-    if (join_blocks > INT_MAX) return DRS_ERR_UNSUPPORTED;
-    cfg.gridDim = dim3(static_cast<unsigned>(join_blocks));
+    cfg.gridDim = dim3(static_cast<unsigned>(lay_out(kJoinColumns)));
     cfg.dynamicSmemBytes = 0;
     return cuda_status(cudaLaunchKernelEx(&cfg, grad_join_kernel<T, kVec>, a));
 }
@@ -715,15 +734,6 @@ extern "C" drs_status drs_embed_tokens_grad(const void* grad_out, drs_dtype grad
     if (tokens == 0 && accumulate) return DRS_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     GradParams a{};
-    if (tokens > 0) {
-        const SortPlan s = SortPlan::of(tokens, vocab);
-        const Workspace w = Workspace::of(workspace, tokens, vocab, width);
-        const drs_status status = sort_tokens(s, w, ids, id_bits, tokens, vocab, st);
-        if (status != DRS_OK) return status;
-        a.keys = w.sorted_keys;
-        a.tokens = w.sorted_tokens;
-        a.partial = w.partial;
-    }
     a.grad = grad_out;
     a.table = grad_table;
     a.n = tokens;
@@ -738,6 +748,16 @@ extern "C" drs_status drs_embed_tokens_grad(const void* grad_out, drs_dtype grad
     const bool vec = width % 8 == 0 && aligned(grad_out, 16) && aligned(grad_table, 16) &&
                      grad_stride * dtype_bytes(grad_dtype) % 16 == 0 &&
                      table_stride * dtype_bytes(table_dtype) % 16 == 0;
+    if (!grids_ok(a, vec ? 8 : 1)) return DRS_ERR_UNSUPPORTED;
+    if (tokens > 0) {
+        const SortPlan s = SortPlan::of(tokens, vocab);
+        const Workspace w = Workspace::of(workspace, tokens, vocab, width);
+        const drs_status status = sort_tokens(s, w, ids, id_bits, tokens, vocab, st);
+        if (status != DRS_OK) return status;
+        a.keys = w.sorted_keys;
+        a.tokens = w.sorted_tokens;
+        a.partial = w.partial;
+    }
     return with_dtype(grad_dtype, [&](auto g) -> drs_status {
         return with_dtype(table_dtype, [&](auto t) -> drs_status {
             return vec ? launch_sums<decltype(g), decltype(t), 8>(a, st)
