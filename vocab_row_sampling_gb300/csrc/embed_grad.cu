@@ -7,9 +7,9 @@
 // the ids are: the work is even however often an id occurs. A piece's threads
 // lie along the columns and add its tokens' rows in fp32 registers; an id
 // that lies inside a piece is written at once, one that crosses a border
-// leaves fp32 partial sums that a last kernel adds in order. No atomics
-// touch a sum, so equal calls give equal bits. Rows without tokens are zeroed
-// in the same launch (unless the call accumulates).
+// leaves fp32 partial sums that the last of its pieces to finish adds in
+// order. No atomics touch a sum, so equal calls give equal bits. Rows without
+// tokens are zeroed in the same launch (unless the call accumulates).
 //
 // Bound by memory: the gradients of the tokens are read once and the table's
 // rows written once; the partial sums are at most 2 / piece of the former.
@@ -20,8 +20,8 @@
 namespace drs {
 namespace {
 
-// The sums follow the sort, and the last kernel the sums, as programmatic
-// dependent launches: their CTAs are in place when the work before ends.
+// The sums follow the sort as a programmatic dependent launch: their CTAs are
+// in place when the sort ends.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
@@ -30,7 +30,7 @@ __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.lau
 // Least significant digit first, one or two digits. A pass counts the digits
 // of every tile and then places the tile's tokens: a CTA adds up the counts
 // of the tiles before its own, and inside a tile a token's rank among equal
-// digits comes from the warps' match masks, in order.
+// digits comes from the warps' masks, in order.
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
@@ -44,7 +44,8 @@ struct SortParams {
     uint32_t* keys_out;
     uint32_t* tokens_out;
     uint32_t* counts;  // [tiles][bins]
-    int64_t n;
+    unsigned long long* clear;  // counters that the first kernel sets to 0
+    int64_t n, clear_n;
     int32_t tile, tiles, bits, shift, vocab, id_bits;
 };
 
@@ -56,6 +57,20 @@ __device__ __forceinline__ uint32_t sort_key(const SortParams& a, int64_t i) {
     return static_cast<uint32_t>(id >= 0 && id < a.vocab ? id : a.vocab);
 }
 
+// The lanes of the warp with the same digit, for lanes that have one: a
+// ballot per bit. __match_any_sync takes a turn per distinct digit, up to 32
+// (2048 tokens: 18.3 us for the whole call with it, 17.2 so; 131072: 75, 72).
+__device__ __forceinline__ uint32_t lanes_with(uint32_t digit, int bits, bool have) {
+    uint32_t same = __ballot_sync(0xffffffffu, have);
+#pragma unroll
+    for (int b = 0; b < kMaxDigit; ++b) {
+        if (b >= bits) break;
+        const uint32_t set = __ballot_sync(0xffffffffu, digit >> b & 1);
+        same &= digit >> b & 1 ? set : ~set;
+    }
+    return same;
+}
+
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortParams a) {
     extern __shared__ uint32_t s_count[];
     const int bins = 1 << a.bits;
@@ -63,6 +78,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortPara
     __syncthreads();
     const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.tile;
     const int64_t hi = lo + a.tile < a.n ? lo + a.tile : a.n;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kSortThreads + threadIdx.x; i < a.clear_n;
+         i += static_cast<int64_t>(gridDim.x) * kSortThreads)
+        a.clear[i] = 0;
     for (int64_t i = lo + threadIdx.x; i < hi; i += kSortThreads)
         atomicAdd(&s_count[(sort_key(a, i) >> a.shift) & (bins - 1)], 1u);
     __syncthreads();
@@ -114,7 +132,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
         const uint32_t key = have ? sort_key(a, i) : 0;
         const uint32_t token = !have ? 0 : a.tokens_in ? a.tokens_in[i] : static_cast<uint32_t>(i);
         const uint32_t digit = (key >> a.shift) & (bins - 1);
-        const uint32_t same = __match_any_sync(0xffffffffu, have ? digit : 0xffffffffu);
+        const uint32_t same = lanes_with(digit, a.bits, have);
         const int below = __popc(same & ((1u << lane) - 1));
         if (have && below == 0) s_warp[warp * bins + digit] = static_cast<uint16_t>(__popc(same));
         __syncthreads();
@@ -139,18 +157,18 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
     }
 }
 
-// Up to kClusterSort tokens are sorted by one thread-block cluster in its
-// shared memory (one launch; the tiles take two per digit). A warp owns 32 kItems
-// consecutive items and ranks them 32 at a time with match masks and counts
-// of its own; the CTAs read each other's totals through distributed shared
-// memory and send every item to the CTA that holds its place.
+// Up to kClusterSort tokens are sorted by one thread-block cluster (one
+// launch; the tiles take two per digit). A warp owns 32 kItems consecutive
+// items and ranks them 32 at a time with masks and counts of its own;
+// the CTAs read each other's totals through distributed shared memory.
+// and send every item to the CTA that holds its place.
 constexpr int kSortCluster = 16;
 constexpr int kMaxItems = 8;  // per thread
 constexpr int64_t kClusterSort = int64_t{kSortCluster} * kSortThreads * kMaxItems;
 
 struct ClusterSortParams {
     SortParams s;  // ids, keys_out, tokens_out, n, bits, vocab, id_bits
-    int32_t share;   // items per CTA
+    int32_t share;  // items per CTA
     int32_t passes, cluster;
 };
 
@@ -181,7 +199,9 @@ template <int kItems> __global__ void __launch_bounds__(kSortThreads) sort_clust
     const int mine = warp * 32 * kItems + lane;  // item i of this thread: mine + 32 i
 
     launch_next();
-    uint64_t item[kItems];
+    for (int64_t i = static_cast<int64_t>(rank) * kSortThreads + tid; i < a.s.clear_n; i += csize * kSortThreads)
+        a.s.clear[i] = 0;
+    uint64_t item[kItems];  // key << 32 | token
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
         const int at = mine + 32 * i;
@@ -202,7 +222,7 @@ template <int kItems> __global__ void __launch_bounds__(kSortThreads) sort_clust
         for (int i = 0; i < kItems; ++i) {
             const bool have = mine + 32 * i < count;
             const uint32_t digit = static_cast<uint32_t>(item[i] >> (32 + shift)) & (bins - 1);
-            const uint32_t same = __match_any_sync(0xffffffffu, have ? digit : 0xffffffffu);
+            const uint32_t same = lanes_with(digit, a.s.bits, have);
             const uint32_t before = have ? s_warp[digit] : 0, ahead = __popc(same & ((1u << lane) - 1));
             __syncwarp();
             if (have && ahead == 0) s_warp[digit] = static_cast<uint16_t>(before + __popc(same));
@@ -234,7 +254,7 @@ template <int kItems> __global__ void __launch_bounds__(kSortThreads) sort_clust
         // A thread takes eight digits.
         uint32_t all[8] = {}, earlier[8] = {}, sum = 0;
         if (tid < bins / 8) {
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < csize; ++i) {
                 // each CTA begins with itself: a CTA answers one at a time
                 const int c = (rank + i) & (csize - 1);
@@ -286,7 +306,7 @@ template <int kItems> __global__ void __launch_bounds__(kSortThreads) sort_clust
 // ------------------------------------------------------------- the sums
 
 constexpr int kSumThreads = 256;
-constexpr int kMaxPiece = 128;  // sorted tokens per piece, at most
+constexpr int kMinColumns = 32;  // threads of a piece, at least: a warp has one piece
 constexpr int64_t kZeroBytes = 65536;  // of the table per zeroing CTA, about
 constexpr int kMaxZeroRows = 1024;
 
@@ -295,10 +315,11 @@ struct GradParams {
     void* table;
     const uint32_t* keys;  // sorted
     const uint32_t* tokens;
-    float* partial;  // [pieces][2][width]
+    float* partial;               // [pieces][2][width]
+    unsigned long long* arrived;  // [pieces][across], 0 at the start
     int64_t n, pieces, grad_stride, table_stride;
     int64_t sum_blocks;  // the CTAs after these zero rows
-    int32_t width, vocab, piece, zero_rows;
+    int32_t width, vocab, piece_bits, zero_rows;
     uint32_t columns, across;  // threads along the columns, CTAs along a row
     uint32_t zero_across;      // threads along a row that is zeroed
     float scale;
@@ -343,6 +364,25 @@ template <typename T, int kVec> __device__ __forceinline__ void store_row(T* p, 
 #pragma unroll
         for (int i = 0; i < static_cast<int>(kVec * sizeof(T) / 16); ++i)
             __stcs(reinterpret_cast<uint4*>(p) + i, reinterpret_cast<const uint4*>(e)[i]);
+    }
+}
+
+// Partial sums, handed on between CTAs of one launch through L2.
+template <int kVec> __device__ __forceinline__ void store_partial(float* p, const float (&v)[kVec]) {
+    if constexpr (kVec == 8) {
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *p = v[0];
+    }
+}
+
+template <int kVec> __device__ __forceinline__ void load_partial(const float* p, float (&v)[kVec]) {
+    if constexpr (kVec == 8) {
+        const float4 lo = __ldcg(reinterpret_cast<const float4*>(p)), hi = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+        v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+    } else {
+        v[0] = __ldcg(p);
     }
 }
 
@@ -404,39 +444,17 @@ template <typename T> __device__ __forceinline__ void zero_rows(const GradParams
     }
 }
 
+// One piece's tokens, summed by its threads. head: its first id began in an
+// earlier piece; on: its last id goes on in the next one.
 template <typename G, typename T, int kVec>
-__global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(const GradParams a) {
+__device__ __forceinline__ void sum_piece(const GradParams& a, const uint32_t* keys, const uint32_t* tokens, int len,
+                                          int64_t piece, int col, bool head, bool on) {
     constexpr int kAhead = kVec == 8 && sizeof(G) == 4 ? 4 : 8;  // rows a thread has in flight
-    extern __shared__ uint32_t s_list[];  // keys, then tokens of the CTA's pieces
-    launch_next();
-    wait_for_previous();
-    if (blockIdx.x >= a.sum_blocks) {
-        zero_rows<T>(a, blockIdx.x - a.sum_blocks);
-        return;
-    }
-    const int tx = threadIdx.x % a.columns, ty = threadIdx.x / a.columns;
-    const int per_cta = kSumThreads / a.columns;
-    const int64_t piece0 = static_cast<int64_t>(blockIdx.x / a.across) * per_cta, piece = piece0 + ty;
-    const int col = static_cast<int>((blockIdx.x % a.across) * a.columns + tx) * kVec;
     const uint32_t none = static_cast<uint32_t>(a.vocab);
-    const int listed = per_cta * a.piece;
-    for (int i = threadIdx.x; i < listed; i += kSumThreads) {
-        const int64_t p = piece0 * a.piece + i;
-        s_list[i] = p < a.n ? a.keys[p] : none;
-        s_list[listed + i] = p < a.n ? a.tokens[p] : 0;
-    }
-    __syncthreads();
-    if (piece >= a.pieces || col >= a.width) return;
-    const int64_t p0 = piece * a.piece;
-    const int len = static_cast<int>(a.n - p0 < a.piece ? a.n - p0 : a.piece);
-    const uint32_t* const keys = s_list + ty * a.piece;
-    const uint32_t* const tokens = keys + listed;
     const G* const grad = static_cast<const G*>(a.grad) + col;
     float* const partial = a.partial + piece * 2 * a.width + col;
-
     float acc[kVec] = {};
     uint32_t cur = keys[0];
-    bool head = p0 > 0 && a.keys[p0 - 1] == cur;  // began in an earlier piece
     for (int p = 0; p < len; p += kAhead) {
         Row<G, kVec> row[kAhead];
 #pragma unroll
@@ -448,7 +466,7 @@ __global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(const GradParams 
             if (p + k >= len) break;
             const uint32_t key = keys[p + k];
             if (key != cur) {
-                if (head) store_row<float, kVec>(partial, acc);
+                if (head) store_partial<kVec>(partial, acc);
                 else write_row<T, kVec>(a, cur, col, acc);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) acc[i] = 0.0f;
@@ -464,58 +482,110 @@ __global__ void __launch_bounds__(kSumThreads) grad_sum_kernel(const GradParams 
         }
     }
     if (cur == none) return;
-    const bool goes_on = p0 + len < a.n && a.keys[p0 + len] == cur;
-    if (head) store_row<float, kVec>(partial, acc);
-    else if (goes_on) store_row<float, kVec>(partial + a.width, acc);
+    if (head) store_partial<kVec>(partial, acc);
+    else if (on) store_partial<kVec>(partial + a.width, acc);
     else write_row<T, kVec>(a, cur, col, acc);
 }
 
-// The ids that cross borders: the CTA of the piece in which such an id begins
-// adds its partial sums in order.
+// An id that crosses borders: the partial sums of the pieces start ..
+// start + n - 1, added in order.
 template <typename T, int kVec>
-__global__ void __launch_bounds__(kSumThreads) grad_join_kernel(const GradParams a) {
-    constexpr int kAhead = 8;
-    wait_for_previous();
-    const int tx = threadIdx.x % a.columns, ty = threadIdx.x / a.columns;
-    const int64_t piece = static_cast<int64_t>(blockIdx.x / a.across) * (kSumThreads / a.columns) + ty;
-    const int col = static_cast<int>((blockIdx.x % a.across) * a.columns + tx) * kVec;
-    if (piece >= a.pieces) return;
-    const int64_t p0 = piece * a.piece, p1 = p0 + a.piece;
-    if (p1 >= a.n) return;
-    const uint32_t key = a.keys[p1 - 1];
-    if (key == static_cast<uint32_t>(a.vocab) || a.keys[p1] != key) return;
-    if (p0 > 0 && a.keys[p0 - 1] == key) return;  // began earlier
-    // a warp has one piece (columns >= 32)
-    const int64_t last = (count_below(a, key + 1, threadIdx.x & 31) - 1) / static_cast<uint32_t>(a.piece);
-    if (col >= a.width) return;
+__device__ __forceinline__ void join_pieces(const GradParams& a, uint32_t key, int64_t start, int n, int col) {
+    constexpr int kAhead = kVec == 8 ? 4 : 8;
+    const float* p = a.partial + start * 2 * a.width + a.width + col;  // the piece where it begins
     float acc[kVec];
-    Row<float, kVec> first;
-    first.load(a.partial + (piece * 2 + 1) * a.width + col);
-    first.unpack(acc);
-    for (int64_t q = piece + 1; q <= last; q += kAhead) {
-        Row<float, kVec> row[kAhead];
+    load_partial<kVec>(p, acc);
+    p += a.width;  // the others' first ids
+    for (int q = 1; q < n; q += kAhead) {
+        float v[kAhead][kVec];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (q + k <= last) row[k].load(a.partial + (q + k) * 2 * a.width + col);
+            if (q + k < n) load_partial<kVec>(p + static_cast<int64_t>(k) * 2 * a.width, v[k]);
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-            if (q + k > last) break;
-            float v[kVec];
-            row[k].unpack(v);
+            if (q + k >= n) break;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) acc[i] += v[i];
+            for (int i = 0; i < kVec; ++i) acc[i] += v[k][i];
         }
+        p += static_cast<int64_t>(kAhead) * 2 * a.width;
     }
     write_row<T, kVec>(a, key, col, acc);
+}
+
+template <typename G, typename T, int kVec>
+// CTAs per SM that registers are held to: with one element per access 8
+// measured 83 us for 10007 x 1283, 6 85 and 5 88; with eight 4 measured 320
+// us for 32768 x 2048, 3 324, 5 339 (spills) and 2 387.
+__global__ void __launch_bounds__(kSumThreads, kVec == 1 ? 8 : 4) grad_sum_kernel(const GradParams a) {
+    extern __shared__ uint32_t s_list[];  // keys, then tokens of the CTA's pieces
+    __shared__ int64_t s_start[kSumThreads / kMinColumns][2];
+    __shared__ int s_parts[kSumThreads / kMinColumns][2];
+    wait_for_previous();
+    if (blockIdx.x >= a.sum_blocks) {
+        zero_rows<T>(a, blockIdx.x - a.sum_blocks);
+        return;
+    }
+    const int tx = threadIdx.x % a.columns, ty = threadIdx.x / a.columns;
+    const int per_cta = kSumThreads / a.columns;
+    const uint32_t slab = blockIdx.x % a.across;
+    const int64_t piece0 = static_cast<int64_t>(blockIdx.x / a.across) * per_cta, piece = piece0 + ty;
+    const int col = static_cast<int>(slab * a.columns + tx) * kVec;
+    const uint32_t none = static_cast<uint32_t>(a.vocab);
+    const int listed = per_cta << a.piece_bits;
+    for (int i = threadIdx.x; i < listed; i += kSumThreads) {
+        const int64_t p = (piece0 << a.piece_bits) + i;
+        s_list[i] = p < a.n ? a.keys[p] : none;
+        s_list[listed + i] = p < a.n ? a.tokens[p] : 0;
+    }
+    __syncthreads();
+    const bool have = piece < a.pieces;
+    const int64_t p0 = piece << a.piece_bits;
+    const int len = !have ? 0 : a.n - p0 < 1 << a.piece_bits ? static_cast<int>(a.n - p0) : 1 << a.piece_bits;
+    const uint32_t* const keys = s_list + (ty << a.piece_bits);
+    const uint32_t first = have ? keys[0] : none, last = have ? keys[len - 1] : none;
+    const bool head = first != none && p0 > 0 && a.keys[p0 - 1] == first;
+    const bool on = last != none && p0 + len < a.n && a.keys[p0 + len] == last;
+    if (have && col < a.width) sum_piece<G, T, kVec>(a, keys, keys + listed, len, piece, col, head, on);
+
+    // Ids that cross borders. Every piece with a part of such an id counts
+    // itself in at the piece where the id begins, and the one where it ends
+    // says how many there are: whoever makes the count whole adds the parts
+    // up, in their order. Nobody waits.
+    if (!__syncthreads_or(head || on)) return;
+    const bool through = head && on && first == last;
+    if (tx < 32) {  // the piece's first warp
+        const int lane = threadIdx.x & 31;
+        const int64_t start = head ? count_below(a, first, lane) >> a.piece_bits : 0;
+        if (lane < 2) {
+            const bool mine = lane == 0 ? head : on && !through;
+            const int64_t at = lane == 0 ? start : piece;
+            int parts = 0;
+            if (mine) {
+                unsigned long long add = 1;
+                if (lane == 0 && !through) add |= static_cast<unsigned long long>(piece - start + 1) << 32;
+                __threadfence();
+                const unsigned long long now = atomicAdd(a.arrived + at * a.across + slab, add) + add;
+                if (now >> 32 == (now & 0xffffffffu)) parts = static_cast<int>(now >> 32);
+                __threadfence();
+            }
+            s_start[ty][lane] = at;
+            s_parts[ty][lane] = parts;
+        }
+    }
+    __syncthreads();
+    if (col >= a.width) return;
+    for (int side = 0; side < 2; ++side)
+        if (s_parts[ty][side]) join_pieces<T, kVec>(a, side ? last : first, s_start[ty][side], s_parts[ty][side], col);
 }
 
 // ------------------------------------------------------------- the call
 
 size_t rounded(size_t bytes) { return (bytes + kWorkspaceAlign - 1) / kWorkspaceAlign * kWorkspaceAlign; }
 
-// Sorted tokens per piece: short pieces spread few tokens over the GPU, long
-// ones leave fewer partial sums of a frequent id to the last kernel.
-int32_t piece_of(int64_t n) { return n <= 4096 ? 8 : n <= 16384 ? 16 : n <= 65536 ? 32 : n <= 262144 ? 64 : kMaxPiece; }
+// Sorted tokens per piece, a power of two: short pieces spread few tokens over
+// the GPU, long ones leave fewer partial sums of a frequent id.
+int32_t piece_bits_of(int64_t n) { return n <= 4096 ? 3 : n <= 16384 ? 4 : n <= 65536 ? 5 : n <= 262144 ? 6 : 7; }
+int64_t pieces_of(int64_t n) { return ceil_div(n, int64_t{1} << piece_bits_of(n)); }
 
 struct SortPlan {
     int passes, bits;
@@ -546,6 +616,7 @@ struct SortPlan {
 struct Workspace {
     uint32_t *keys[2], *tokens[2], *counts, *sorted_keys, *sorted_tokens;
     float* partial;
+    unsigned long long* arrived;
     size_t bytes;
     static Workspace of(void* base, int64_t n, int64_t vocab, int64_t width) {
         Workspace w{};
@@ -564,7 +635,10 @@ struct Workspace {
         w.sorted_keys = w.keys[copies - 1];
         w.sorted_tokens = w.tokens[copies - 1];
         if (!s.cluster) w.counts = reinterpret_cast<uint32_t*>(take((static_cast<size_t>(s.tiles) << s.bits) * 4));
-        w.partial = reinterpret_cast<float*>(take(static_cast<size_t>(ceil_div(n, piece_of(n))) * 2 * width * 4));
+        const size_t pieces = static_cast<size_t>(pieces_of(n));
+        w.partial = reinterpret_cast<float*>(take(pieces * 2 * width * 4));
+        // a CTA has 256 columns of a piece at least, or all of them
+        w.arrived = reinterpret_cast<unsigned long long*>(take(pieces * ceil_div(width, kSumThreads) * 8));
         w.bytes = at;
         return w;
     }
@@ -591,13 +665,15 @@ template <int kItems> drs_status launch_cluster_sort(const ClusterSortParams& a,
 }
 
 drs_status sort_tokens(const SortPlan& s, const Workspace& w, const void* ids, int id_bits, int64_t n, int64_t vocab,
-                       cudaStream_t stream) {
+                       int64_t counters, cudaStream_t stream) {
     if (s.cluster) {
         ClusterSortParams a{};
         a.s.ids = ids;
         a.s.keys_out = w.sorted_keys;
         a.s.tokens_out = w.sorted_tokens;
         a.s.n = n;
+        a.s.clear = w.arrived;
+        a.s.clear_n = counters;
         a.s.bits = s.bits;
         a.s.vocab = static_cast<int32_t>(vocab);
         a.s.id_bits = id_bits;
@@ -621,6 +697,8 @@ drs_status sort_tokens(const SortPlan& s, const Workspace& w, const void* ids, i
         a.tokens_out = w.tokens[pass];
         a.counts = w.counts;
         a.n = n;
+        a.clear = w.arrived;
+        a.clear_n = pass == 0 ? counters : 0;
         a.tile = s.tile;
         a.tiles = s.tiles;
         a.bits = s.bits;
@@ -633,41 +711,18 @@ drs_status sort_tokens(const SortPlan& s, const Workspace& w, const void* ids, i
     return cuda_status(cudaGetLastError());
 }
 
-// Threads of a CTA along the columns (`least` at least), and the CTAs of all
-// pieces.
-struct SumLayout {
-    uint32_t columns, across;
-    int64_t blocks;
-    static SumLayout of(const GradParams& a, int vec, int least) {
-        SumLayout l;
-        int x = least;
-        while (x < kSumThreads && int64_t{x} * vec < a.width) x *= 2;
-        l.columns = x;
-        l.across = static_cast<uint32_t>(ceil_div(a.width, int64_t{x} * vec));
-        l.blocks = ceil_div(a.pieces, kSumThreads / x) * l.across;
-        return l;
-    }
-};
-// 8 columns keep a CTA's lists within 32 KB; the last kernel's warps search
-// together.
-constexpr int kSumColumns = 8, kJoinColumns = 32;
-
-// Whether every launch's grid is in range.
-bool grids_ok(const GradParams& a, int vec) {
-    return SumLayout::of(a, vec, kSumColumns).blocks + a.vocab <= INT_MAX &&
-           SumLayout::of(a, vec, kJoinColumns).blocks <= INT_MAX;
+// Threads of a CTA along the columns, CTAs along a row, and of all pieces.
+void lay_out(GradParams& a, int vec) {
+    int x = kMinColumns;
+    while (x < kSumThreads && int64_t{x} * vec < a.width) x *= 2;
+    a.columns = x;
+    a.across = static_cast<uint32_t>(ceil_div(a.width, int64_t{x} * vec));
+    a.sum_blocks = ceil_div(a.pieces, kSumThreads / x) * a.across;
 }
 
 template <typename G, typename T, int kVec> drs_status launch_sums(GradParams a, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms <= 0) return DRS_ERR_CUDA;
-    const auto lay_out = [&](int least) {
-        const SumLayout l = SumLayout::of(a, kVec, least);
-        a.columns = l.columns;
-        a.across = l.across;
-        return l.blocks;
-    };
-    a.sum_blocks = lay_out(kSumColumns);
     int64_t zero_blocks = 0;
     if (!a.accumulate) {
         // Measured for 32768 x 2048 bf16 into 262144 fp32 rows: 335 us with
@@ -684,18 +739,14 @@ template <typename G, typename T, int kVec> drs_status launch_sums(GradParams a,
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.sum_blocks + zero_blocks));
     cfg.blockDim = dim3(kSumThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(kSumThreads / a.columns) * a.piece * 8;
+    cfg.dynamicSmemBytes = (static_cast<size_t>(kSumThreads / a.columns) << a.piece_bits) * 8;
     cfg.stream = stream;
     cudaLaunchAttribute dependent[1];
     dependent[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     dependent[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = dependent;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, grad_sum_kernel<G, T, kVec>, a) != cudaSuccess) return DRS_ERR_CUDA;
-    if (a.pieces <= 1) return DRS_OK;
-    cfg.gridDim = dim3(static_cast<unsigned>(lay_out(kJoinColumns)));
-    cfg.dynamicSmemBytes = 0;
-    return cuda_status(cudaLaunchKernelEx(&cfg, grad_join_kernel<T, kVec>, a));
+    return cuda_status(cudaLaunchKernelEx(&cfg, grad_sum_kernel<G, T, kVec>, a));
 }
 
 bool grad_sizes_ok(int64_t tokens, int64_t vocab, int64_t width) {
@@ -737,8 +788,8 @@ extern "C" drs_status drs_embed_tokens_grad(const void* grad_out, drs_dtype grad
     a.grad = grad_out;
     a.table = grad_table;
     a.n = tokens;
-    a.piece = piece_of(tokens);
-    a.pieces = ceil_div(tokens, a.piece);
+    a.piece_bits = piece_bits_of(tokens);
+    a.pieces = pieces_of(tokens);
     a.grad_stride = grad_stride;
     a.table_stride = table_stride;
     a.width = static_cast<int32_t>(width);
@@ -748,15 +799,17 @@ extern "C" drs_status drs_embed_tokens_grad(const void* grad_out, drs_dtype grad
     const bool vec = width % 8 == 0 && aligned(grad_out, 16) && aligned(grad_table, 16) &&
                      grad_stride * dtype_bytes(grad_dtype) % 16 == 0 &&
                      table_stride * dtype_bytes(table_dtype) % 16 == 0;
-    if (!grids_ok(a, vec ? 8 : 1)) return DRS_ERR_UNSUPPORTED;
+    lay_out(a, vec ? 8 : 1);
+    if (a.sum_blocks + vocab > INT_MAX) return DRS_ERR_UNSUPPORTED;
     if (tokens > 0) {
         const SortPlan s = SortPlan::of(tokens, vocab);
         const Workspace w = Workspace::of(workspace, tokens, vocab, width);
-        const drs_status status = sort_tokens(s, w, ids, id_bits, tokens, vocab, st);
+        const drs_status status = sort_tokens(s, w, ids, id_bits, tokens, vocab, a.pieces * a.across, st);
         if (status != DRS_OK) return status;
         a.keys = w.sorted_keys;
         a.tokens = w.sorted_tokens;
         a.partial = w.partial;
+        a.arrived = w.arrived;
     }
     return with_dtype(grad_dtype, [&](auto g) -> drs_status {
         return with_dtype(table_dtype, [&](auto t) -> drs_status {
