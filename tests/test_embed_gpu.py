@@ -214,6 +214,24 @@ def test_grad_many_tokens_and_equal_bits():
         assert torch.equal(t.view(torch.int32), first.view(torch.int32))
 
 
+@pytest.mark.parametrize("width", [64, 4096, 4100])
+def test_grad_equal_bits_over_many_calls(width):
+    """Ids that cross many pieces, whose parts different CTAs may add up: the
+    order of the sums does not change with who does."""
+    lib = drs()
+    ids = some_ids(5000, 600, 2)
+    ids[::4] = 5
+    ids[1::4] = 599
+    g = rows(5000, width, torch.bfloat16, 4)
+    t = torch.zeros(600, width, device="cuda")
+    check_grad(g, ids, 1.0, t)
+    ids = torch.as_tensor(ids).cuda()
+    first = t.clone()
+    for _ in range(30):
+        lib.embed_tokens_grad(g, ids, 1.0, t)
+        assert torch.equal(t, first)
+
+
 def test_grad_of_no_tokens():
     t = torch.ones(100, 33, device="cuda")
     none = torch.zeros(0, dtype=torch.int64, device="cuda")
