@@ -447,7 +447,7 @@ drs_status drs_stash_converged_logprobs(const float *logits, int64_t logits_rows
  *     weights are all 0, from p. After the last draft: from p of the next
  *     position. NaN and negative weights are 0; infinite ones are not supported.
  *     The token is the lowest column whose running sum of weights exceeds
- *     sample_u[b] times their total (the sums are good to about 1e-14);
+ *     sample_u[b] times their total (the sums are good to about 1e-13);
  *     -1 where there is no weight at all.
  *
  *   target      target_dtype [target_rows, vocab], row stride target_stride.

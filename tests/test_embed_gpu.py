@@ -171,8 +171,9 @@ def test_grad_lengths_and_repetition(n, kind):
 
 @pytest.mark.parametrize("vocab", [1, 2, 5, 1023, 1024, 2047, 2048, 65536, 262144, 1 << 21])
 def test_grad_vocabularies(vocab):
-    """One and two digits of the sort, and their borders."""
-    for n in (500, 20000):
+    """One and two digits of the sort, and their borders; the sort by one
+    cluster and, above 131072 tokens, by tiles."""
+    for n in (500, 20000, 131072, 131073):
         g = rows(n, 16, torch.float32, n)
         t = torch.empty(vocab, 16, device="cuda")
         check_grad(g, some_ids(n, vocab, n, "mixed"), 1.0, t)
@@ -239,6 +240,21 @@ def test_grad_of_no_tokens():
     assert (t == 1).all()
     drs().embed_tokens_grad(torch.zeros(0, 33, device="cuda"), none, 1.0, t)
     assert (t == 0).all()
+
+
+@pytest.mark.parametrize("width", [2064, 2051])
+def test_grad_offsets_past_32_bits(width):
+    """A table of over 2^32 elements: its last rows receive sums, its others zeros."""
+    vocab = 1 << 21
+    t = torch.full((vocab, width), 7.0, dtype=torch.bfloat16, device="cuda")
+    ids = torch.tensor([vocab - 1, 0, vocab - 3, vocab - 1]).cuda()
+    g = rows(4, width, torch.float32, 1)
+    drs().embed_tokens_grad(g, ids, 1.0, t)
+    want = torch.stack([g[2], torch.zeros_like(g[0]), g[0] + g[3]]).bfloat16()
+    assert torch.equal(t[-3:], want) and torch.equal(t[0], g[1].bfloat16())
+    assert int(t.count_nonzero()) == int(t[-3:].count_nonzero()) + int(t[0].count_nonzero())
+    drs().embed_tokens_grad(g, ids, 1.0, t, accumulate=True)
+    assert torch.equal(t[-1], (want[2].float() + (g[0] + g[3])).bfloat16())
 
 
 def test_grad_against_differences():

@@ -181,9 +181,54 @@ def test_block_ids_past_32_bit_slots():
     assert ref[3].max() > 2**36
 
 
+def test_table_offsets_past_32_bits():
+    """Rows of the table 2^22 entries apart, the last ones past 2^32 entries."""
+    case = list(state_of(6, 1100, 60, 9, 16, widest=8))
+    far = torch.empty(1100 * 2**22, dtype=torch.int32, device="cuda").view(1100, 2**22)[:, :8]
+    far.copy_(torch.as_tensor(case[3]))
+    dev = lambda a: torch.as_tensor(np.ascontiguousarray(a)).cuda()
+    ring, capacity = dev(case[6]), int(case[1].sum())
+    out = drs().map_slots(dev(case[0]), dev(case[1]), dev(case[2]), far, 16, ring, dev(case[7]), capacity)
+    ref = reference(case[0], case[1], case[2], case[3], 16, case[6], case[7], capacity)
+    for got, want in zip(list(out) + [far, ring], ref):
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
 def test_many_requests():
     case = state_of(9, 70001, 40, 3, 16)
     check(case, int(case[1].sum()) + 1)
+
+
+def test_large_steps_on_another_stream_and_in_a_graph():
+    """The two launches of a large step, in place: on a stream of its own,
+    then captured and replayed on other lengths."""
+    lib = drs()
+    case = state_of(21, 900, 300, 40, 16)
+    lens, new, held, table, widest, block, ring, state = case
+    capacity = int(new.sum()) + 100
+    assert capacity > 8192
+    dev = lambda a: torch.as_tensor(np.ascontiguousarray(a)).cuda()
+    g = [dev(a) for a in (lens, new, held, table, ring, state)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = lib.map_slots(*g[:4], block, g[4], g[5], capacity, stream=side)
+    side.synchronize()
+    ref = reference(lens, new, held, table, block, ring, state, capacity)
+    for got, want in zip(list(out) + [g[3], g[4]], ref):
+        assert np.array_equal(got.cpu().numpy(), want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = lib.map_slots(*g[:4], block, g[4], g[5], capacity)
+    for seed in (22, 23):
+        other = state_of(seed, 900, 300, 40, 16, widest=widest)
+        size = min(len(ring), len(other[6]))
+        fresh = list(other[:4]) + [np.resize(other[6], len(ring)), np.array([3, 3 + size // 2])]
+        for t, a in zip(g, fresh):
+            t.copy_(torch.as_tensor(np.ascontiguousarray(a)))
+        graph.replay()
+        ref = reference(fresh[0], fresh[1], fresh[2], fresh[3], block, fresh[4], fresh[5], capacity)
+        for got, want in zip(list(out) + [g[3], g[4]], ref):
+            assert np.array_equal(got.cpu().numpy(), want)
 
 
 def test_steps_of_a_cache_on_a_captured_graph():

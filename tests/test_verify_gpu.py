@@ -2,9 +2,9 @@
 
 The weights are the fp32 differences that the call defines; everything
 after them (products, sums, comparisons) is fp64 on the CPU. Accepted
-counts and tokens are exact: sums on both sides are good to about 1e-14,
+counts and tokens are exact: sums on both sides are good to about 1e-13,
 and a sampled number that close to a border has a probability of about
-1e-14 times the number of columns. Inputs with sums that are exact in
+1e-13 times the number of columns. Inputs with sums that are exact in
 fp32 (multiples of 1/64) put the sampled numbers on the borders themselves."""
 import numpy as np
 import pytest
@@ -132,6 +132,14 @@ def test_counts_of_requests_and_drafts(requests, most):
         assert np.array_equal(acc, np.diff(a[3]))
 
 
+@pytest.mark.parametrize("requests,vocab,target,draft,pad", [
+    (200, 40000, "bf16", "fp16", 0), (200, 40001, "bf16", "fp16", 0), (48, 140000, "fp16", None, 0),
+    (40, 66003, "fp32", "fp32", 2), (100, 131072, "bf16", "bf16", 0), (24, 262144, "bf16", None, 8)])
+def test_batches_of_every_cluster_size(requests, vocab, target, draft, pad):
+    """Batches that fill the GPU once or several times, with 1 to 16 CTAs per request."""
+    check(*batch(requests + vocab, requests, 2, vocab, target, draft, pad), where=(requests, vocab))
+
+
 def test_sampled_numbers_on_the_borders():
     """Weights that are multiples of 1/64: every sum is exact, so numbers at,
     just below and just above each border have one right column. Zero
@@ -196,6 +204,22 @@ def test_rows_without_weight_and_odd_values(vocab):
             out, acc = check(torch.as_tensor(target).cuda(), None if d is None else torch.as_tensor(d).cuda(), tokens,
                              cu, au, su, 1, where=(u, d is None))
             assert out[1, 0] == -1 and out[2, 0] == -1
+
+
+def test_offsets_past_32_bits():
+    """Rows 2^31 + 8 elements apart: the last ones lie past 2^32 elements."""
+    a = list(batch(12, 2, 1, 3000, "bf16", "bf16"))
+    a[3], a[2] = np.array([0, 1, 2], np.int32), np.array([7, 2999])
+    g = torch.Generator().manual_seed(1)
+    far = []
+    for n in (4, 2):
+        buffer = torch.empty(n * (2**31 + 8), dtype=torch.bfloat16, device="cuda")
+        rows_far = buffer.view(n, 2**31 + 8)[:, :3000]
+        rows_far.copy_(torch.softmax(3 * torch.randn(n, 3000, generator=g), 1))
+        far.append(rows_far)
+    for u in (0.0, 0.99):
+        check(far[0], far[1], a[2], a[3], np.full(2, u, np.float32), np.array([0.2, 0.9], np.float32), 1, where=u)
+        check(far[0], None, a[2], a[3], np.full(2, u, np.float32), np.array([0.2, 0.9], np.float32), 1, where=u)
 
 
 def test_requests_outside_the_arrays_are_marked():

@@ -7,7 +7,8 @@
 // not start on 16-byte boundaries (odd widths, strides or offsets) are
 // written in aligned 16-byte words all the same, each put together from the
 // two aligned words of the table that hold it: single elements took 12.1 us
-// for 5003 x 1283 fp16.
+// for 5003 x 1283 fp16, this 4.6. Measured: 65536 x 4096 bf16 117 us, 6.2 TB/s
+// of the distinct rows and the output; 256 x 2048 2.1 us, the launch.
 #include "token_common.cuh"
 
 namespace drs {
@@ -131,8 +132,8 @@ template <typename T, typename I> drs_status launch_embed(EmbedParams a, bool ve
     constexpr int kVec = 16 / sizeof(T);
     const int64_t words = a.width / kVec;
     if (vec) {
-        // Tokens per thread, measured: 65536 x 4096 bf16 takes 164 us with one,
-        // 125 with two, 120 with four and 122 with eight; 256 x 2048 takes 1.9
+        // Tokens per thread, measured (with 256 threads): 65536 x 4096 bf16 takes
+        // 164 us with one, 125 with two, 120 with four and 122 with eight; 256 x 2048 takes 1.9
         // us with one or two, 2.2 with four, 3.0 with eight.
         const bool many = a.tokens * words > int64_t{8192} * sm_count();
         return many ? launch_rows<T, I, 4>(a, stream) : launch_rows<T, I, 2>(a, stream);

@@ -13,6 +13,9 @@
 //
 // Bound by memory: the gradients of the tokens are read once and the table's
 // rows written once; the partial sums are at most 2 / piece of the former.
+// Measured: 32768 x 2048 bf16 into 262144 fp32 rows 318 us, 7.2 TB/s (17 for the
+// sort, the rest mostly stores, which alone reach 7.6 TB/s); 2048 x 1024 into
+// 8192 rows 17.5 us, half of it the sort's latency.
 #include <climits>
 
 #include "token_common.cuh"
@@ -725,9 +728,9 @@ template <typename G, typename T, int kVec> drs_status launch_sums(GradParams a,
     if (sms <= 0) return DRS_ERR_CUDA;
     int64_t zero_blocks = 0;
     if (!a.accumulate) {
-        // Measured for 32768 x 2048 bf16 into 262144 fp32 rows: 335 us with
-        // 64 KB per CTA, 343 with 256 KB, 361 with 1 MB. Fewer rows where
-        // that would leave SMs idle.
+        // Measured for 32768 x 2048 bf16 into 262144 fp32 rows, when the whole
+        // call took 335 us: 64 KB per CTA 335, 256 KB 343, 1 MB 361. Fewer rows
+        // where that would leave SMs idle.
         int64_t rows = kZeroBytes / (static_cast<int64_t>(a.width) * sizeof(T));
         const int64_t even = ceil_div(a.vocab, sms * 8);
         rows = rows < even ? rows : even;

@@ -14,10 +14,13 @@
 // draw needs, exchange their totals through distributed shared memory, and
 // the CTA whose share holds the drawn column reads one warp's part of it
 // again (from L2) to find the column. Bound by memory for large batches: each
-// needed row is read once.
+// needed row is read once. Measured: 256 requests of 262144 bf16 and fp16
+// columns 47.5 us, 4.9 TB/s of those rows (the same reads without the
+// cluster's barrier and the draw 41 us); one request of 131072 columns 6.2 us,
+// the latency of four dependent loads, a cluster's barrier and a second look.
 //
 // Sums. A drawn column moves when the running sums are off by more than the
-// distance of u * total to a border, so they are held to about 2^-46: all
+// distance of u * total to a border, so they are held to about 2^-44: all
 // sums are pairs of fp32 (the sum and the errors of the additions). fp64 sums
 // took most of the kernel's time (165 us for 256 requests of 262144 columns):
 // this GPU issues one fp64 instruction per SM in 16 cycles. The weight
@@ -90,7 +93,7 @@ template <typename P, typename Q, bool kVec> struct Weights {
         }
     }
 
-    // Columns i .. i+7 (i a multiple of 8), 0 from `end` on.
+    // Columns i .. i+7, 0 from `end` on (with kVec i is a multiple of 8).
     __device__ __forceinline__ void load(int64_t i, int end, float (&w)[8]) const {
         if (kVec && i + 8 <= end) {
             Raw8<P> rp;
