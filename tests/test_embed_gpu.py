@@ -275,6 +275,34 @@ def test_grad_against_differences():
         assert up - down == float((grad.double() * d.double()).sum())
 
 
+def test_workspaces_of_streams():
+    """Calls of growing and shrinking sizes, in turn on three streams that run
+    at the same time, and inside a graph whose workspace is its own."""
+    lib = drs()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    sizes = [(40, 64), (3000, 512), (200, 1024), (9000, 256), (10, 8)]
+    cases = []
+    for k, (n, width) in enumerate(sizes):
+        g, ids = rows(n, width, torch.bfloat16, k), torch.as_tensor(some_ids(n, 700, k)).cuda()
+        cases.append((g, ids, lib.embed_tokens_grad(g, ids, 1.0, torch.empty(700, width, device="cuda"))))
+    outs = [[torch.empty_like(want) for _, _, want in cases] for _ in streams]
+    graph = torch.cuda.CUDAGraph()
+    captured = torch.empty_like(cases[1][2])
+    with torch.cuda.graph(graph):
+        lib.embed_tokens_grad(cases[1][0], cases[1][1], 1.0, captured)
+    torch.cuda.synchronize()
+    for repeat in range(4):
+        graph.replay()
+        for k, (g, ids, _) in enumerate(cases):
+            for st, out in zip(streams, outs):
+                lib.embed_tokens_grad(g, ids, 1.0, out[k], stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(captured, cases[1][2])
+    for out in outs:
+        for got, (_, _, want) in zip(out, cases):
+            assert torch.equal(got, want)
+
+
 def test_streams_and_graphs():
     """Both calls on another stream than the tensors' own, and a training step
     of both captured into a graph and replayed on new ids."""

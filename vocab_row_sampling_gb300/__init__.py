@@ -653,6 +653,30 @@ def _allocate_on(stream):
     return torch.cuda.stream(stream)
 
 
+_stream_workspaces = {}
+
+
+def _stream_workspace(nbytes: int, gpu: int, stream=None):
+    """A workspace of at least nbytes for calls on this stream, kept from
+    call to call (an allocation between two calls takes 5 us) and replaced by
+    a larger one when needed: both belong to the stream, so what still runs on
+    it is done with the old one before its memory is used again. A call that
+    is captured into a graph gets one of the graph's own."""
+    import torch
+    if gpu < 0 or nbytes == 0:
+        return None
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _stream_workspace(nbytes, gpu, None)
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{gpu}")
+    key = (gpu, _raw_stream(None, gpu))
+    ws = _stream_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _stream_workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=f"cuda:{gpu}")
+    return ws
+
+
 def verify_drafts(target_probs, draft_tokens, cu_drafts, accept_u, sample_u, max_drafts: int,
                   draft_probs=None, out_tokens=None, out_accepted=None, stream=None):
     """Verify drafted tokens against the target's probabilities (see
@@ -708,14 +732,9 @@ def embed_tokens_grad(grad_out, ids, scale: float, grad_table, accumulate: bool 
     """The gradient of embed_tokens with respect to its table, written (or
     added) into grad_table [vocab, width], which is returned (see
     drs_embed_tokens_grad)."""
-    import torch
     if grad_table.dim() != 2:
         raise ValueError(f"grad_table: [vocab, width] expected, got {tuple(grad_table.shape)}")
     size = drs_embed_tokens_grad_workspace_bytes(ids.numel(), *grad_table.shape)
-    if stream is None:
-        ws = torch.empty(size, dtype=torch.uint8, device=grad_out.device)
-    else:
-        with _allocate_on(stream):
-            ws = torch.empty(size, dtype=torch.uint8, device=grad_out.device)
+    ws = _stream_workspace(size, grad_out.get_device(), stream)
     drs_embed_tokens_grad(grad_out, ids, scale, accumulate, grad_table, ws, stream)
     return grad_table

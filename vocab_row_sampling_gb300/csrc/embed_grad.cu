@@ -15,7 +15,7 @@
 // rows written once; the partial sums are at most 2 / piece of the former.
 // Measured: 32768 x 2048 bf16 into 262144 fp32 rows 318 us, 7.2 TB/s (17 for the
 // sort, the rest mostly stores, which alone reach 7.6 TB/s); 2048 x 1024 into
-// 8192 rows 17.5 us, half of it the sort's latency.
+// 8192 rows 13.8 us, most of it latency.
 #include <climits>
 
 #include "token_common.cuh"
@@ -30,8 +30,9 @@ __device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.lau
 
 // ------------------------------------------------------------- the sort
 //
-// Least significant digit first, one or two digits. A pass counts the digits
-// of every tile and then places the tile's tokens: a CTA adds up the counts
+// By ranks, by one cluster or by tiles, as the number of tokens grows. The
+// latter two go by digits, the least significant first, one or two of them. A
+// pass of the tiles counts the digits of every tile and then places the tile's tokens: a CTA adds up the counts
 // of the tiles before its own, and inside a tile a token's rank among equal
 // digits comes from the warps' masks, in order.
 
@@ -160,7 +161,44 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
     }
 }
 
-// Up to kClusterSort tokens are sorted by one thread-block cluster (one
+// Up to kRankSort tokens: a token's place is the number of keys below its own,
+// and of equal ones before it, counted by kPerKey threads per token over all
+// keys in shared memory. No passes and no barriers between CTAs.
+// us for the whole call of 2048 tokens (1024 columns), 4096, 6000 and 8192 (512
+// columns) so: 13.8, 28.0, 38.8, 44.3; sorted by a cluster: 17.6, 30.4, 30.6,
+// 31.8 (the comparisons grow with the square).
+constexpr int kRankThreads = 512;
+constexpr int64_t kRankSort = 4096;
+
+template <int kPerKey> __global__ void __launch_bounds__(kRankThreads) sort_rank_kernel(const SortParams a) {
+    extern __shared__ uint4 s_keys4[];
+    uint32_t* const s_keys = reinterpret_cast<uint32_t*>(s_keys4);
+    const int tid = threadIdx.x, n = static_cast<int>(a.n), groups = (n + 3) / 4;
+    launch_next();
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kRankThreads + tid; i < a.clear_n;
+         i += static_cast<int64_t>(gridDim.x) * kRankThreads)
+        a.clear[i] = 0;
+#pragma unroll 8
+    for (int i = tid; i < 4 * groups; i += kRankThreads) s_keys[i] = i < n ? sort_key(a, i) : 0xffffffffu;
+    __syncthreads();
+    const int i = blockIdx.x * (kRankThreads / kPerKey) + tid / kPerKey;
+    const uint32_t key = i < n ? s_keys[i] : 0;
+    int below = 0;
+#pragma unroll 4
+    for (int g = tid % kPerKey; g < groups; g += kPerKey) {
+        const uint4 k = s_keys4[g];
+        const int j = 4 * g;
+        below += (k.x < key + (j < i)) + (k.y < key + (j + 1 < i)) + (k.z < key + (j + 2 < i)) + (k.w < key + (j + 3 < i));
+    }
+#pragma unroll
+    for (int o = kPerKey / 2; o > 0; o >>= 1) below += __shfl_xor_sync(0xffffffffu, below, o);
+    if (i < n && tid % kPerKey == 0) {
+        a.keys_out[below] = key;
+        a.tokens_out[below] = static_cast<uint32_t>(i);
+    }
+}
+
+// More, up to kClusterSort, are sorted by one thread-block cluster (one
 // launch; the tiles take two per digit). A warp owns 32 kItems consecutive
 // items and ranks them 32 at a time with masks and counts of its own;
 // the CTAs read each other's totals through distributed shared memory.
@@ -594,6 +632,7 @@ struct SortPlan {
     int passes, bits;
     int32_t tile, tiles;    // where the tiles sort
     int32_t cluster, share; // where a cluster does (cluster > 0)
+    bool ranks;             // where every token is ranked by itself
     static SortPlan of(int64_t n, int64_t vocab) {
         int key = 1;
         while ((int64_t{1} << key) <= vocab) ++key;  // keys are 0 .. vocab
@@ -603,7 +642,8 @@ struct SortPlan {
         if (s.bits < 4) s.bits = 4;  // eight digits are one 16-byte word
         s.cluster = 0;
         s.share = 0;
-        if (n <= kClusterSort) {
+        s.ranks = n <= kRankSort;
+        if (!s.ranks && n <= kClusterSort) {
             // two items per thread until the cluster is full
             s.cluster = 1;
             while (s.cluster < kSortCluster && n > int64_t{2} * kSortThreads * s.cluster) s.cluster *= 2;
@@ -630,14 +670,14 @@ struct Workspace {
             return p;
         };
         const SortPlan s = SortPlan::of(n, vocab);
-        const int copies = s.cluster ? 1 : s.passes;
+        const int copies = s.ranks || s.cluster ? 1 : s.passes;
         for (int i = 0; i < copies; ++i) {
             w.keys[i] = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(n) * 4));
             w.tokens[i] = reinterpret_cast<uint32_t*>(take(static_cast<size_t>(n) * 4));
         }
         w.sorted_keys = w.keys[copies - 1];
         w.sorted_tokens = w.tokens[copies - 1];
-        if (!s.cluster) w.counts = reinterpret_cast<uint32_t*>(take((static_cast<size_t>(s.tiles) << s.bits) * 4));
+        if (!s.ranks && !s.cluster) w.counts = reinterpret_cast<uint32_t*>(take((static_cast<size_t>(s.tiles) << s.bits) * 4));
         const size_t pieces = static_cast<size_t>(pieces_of(n));
         w.partial = reinterpret_cast<float*>(take(pieces * 2 * width * 4));
         // a CTA has 256 columns of a piece at least, or all of them
@@ -669,6 +709,24 @@ template <int kItems> drs_status launch_cluster_sort(const ClusterSortParams& a,
 
 drs_status sort_tokens(const SortPlan& s, const Workspace& w, const void* ids, int id_bits, int64_t n, int64_t vocab,
                        int64_t counters, cudaStream_t stream) {
+    if (s.ranks) {
+        SortParams a{};
+        a.ids = ids;
+        a.keys_out = w.sorted_keys;
+        a.tokens_out = w.sorted_tokens;
+        a.clear = w.arrived;
+        a.n = n;
+        a.clear_n = counters;
+        a.vocab = static_cast<int32_t>(vocab);
+        a.id_bits = id_bits;
+        const size_t smem = static_cast<size_t>(ceil_div(n, 4)) * 16;
+        // at most 128 CTAs
+        if (n <= 2048)
+            sort_rank_kernel<32><<<static_cast<unsigned>(ceil_div(n, kRankThreads / 32)), kRankThreads, smem, stream>>>(a);
+        else
+            sort_rank_kernel<16><<<static_cast<unsigned>(ceil_div(n, kRankThreads / 16)), kRankThreads, smem, stream>>>(a);
+        return cuda_status(cudaGetLastError());
+    }
     if (s.cluster) {
         ClusterSortParams a{};
         a.s.ids = ids;
