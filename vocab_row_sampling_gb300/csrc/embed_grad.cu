@@ -466,23 +466,43 @@ template <typename T> __device__ __forceinline__ void zero_rows(const GradParams
     for (int64_t p = s_range[0] + threadIdx.x; p < s_range[1]; p += kSumThreads) s_touched[a.keys[p] - v0] = true;
     __syncthreads();
     T* const table = static_cast<T*>(a.table) + v0 * a.table_stride;
-    if (a.zero_across < kSumThreads) {  // narrow rows: several at once
+    constexpr int kPer = 16 / sizeof(T);
+    const uint4 zeros = make_uint4(0, 0, 0, 0);
+    if (a.table_stride != a.width || a.width < kPer) {
+        // rows apart from each other (or very short): some threads for each
         const int tx = threadIdx.x % a.zero_across, ny = kSumThreads / a.zero_across;
         for (int r = threadIdx.x / a.zero_across; r < n; r += ny)
             if (!s_touched[r]) zero_range(table + r * a.table_stride, a.width, tx, a.zero_across);
         return;
     }
-    const bool dense = a.table_stride == a.width;
-    for (int r = 0; r < n;) {
-        if (s_touched[r]) {
-            ++r;
-            continue;
-        }
-        int end = r + 1;  // consecutive rows without padding are one range
-        while (dense && end < n && !s_touched[end]) ++end;
-        zero_range(table + r * a.table_stride, dense ? (end - r) * a.table_stride : a.width, threadIdx.x, kSumThreads);
-        r = end;
+    // Rows that follow each other: the 16-byte words of all of them in one loop.
+    // A word belongs to the row(s) of its first and last element; the quotients
+    // are exact below 2^21 elements.
+    const float inv = 1.0f / static_cast<float>(a.width);
+    const auto row_of = [&](int element) { return static_cast<int>((static_cast<float>(element) + 0.5f) * inv); };
+    const int total = n * a.width;
+    if (a.width % kPer == 0 && (reinterpret_cast<uintptr_t>(table) & 15) == 0) {
+#pragma unroll 4
+        for (int e = threadIdx.x * kPer; e < total; e += kSumThreads * kPer)
+            if (!s_touched[row_of(e)]) __stcs(reinterpret_cast<uint4*>(table + e), zeros);
+        return;
     }
+    const int lead = static_cast<int>((-reinterpret_cast<uintptr_t>(table) & 15) / sizeof(T));
+    const int done = lead + (total - lead) / kPer * kPer;
+#pragma unroll 4
+    for (int e = lead + threadIdx.x * kPer; e < done; e += kSumThreads * kPer) {
+        const int last = row_of(e + kPer - 1), first = row_of(e);
+        const bool head = !s_touched[first], tail = !s_touched[last];
+        if (head && tail) {
+            __stcs(reinterpret_cast<uint4*>(table + e), zeros);
+        } else if (head || tail) {
+            const int border = last * a.width;  // the last row's first element
+            for (int i = head ? e : border; i < (head ? border : e + kPer); ++i) table[i] = from_f<T>(0.0f);
+        }
+    }
+    // the elements before the first word, and after the last one
+    const int edge = threadIdx.x < lead ? threadIdx.x : done + threadIdx.x - lead;
+    if (edge < total && !s_touched[row_of(edge)]) table[edge] = from_f<T>(0.0f);
 }
 
 // One piece's tokens, summed by its threads. head: its first id began in an
