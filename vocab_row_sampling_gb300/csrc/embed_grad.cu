@@ -200,12 +200,15 @@ template <int kPerKey> __global__ void __launch_bounds__(kRankThreads) sort_rank
 
 // More, up to kClusterSort, are sorted by one thread-block cluster (one
 // launch; the tiles take two per digit). A warp owns 32 kItems consecutive
-// items and ranks them 32 at a time with masks and counts of its own;
-// the CTAs read each other's totals through distributed shared memory.
-// and send every item to the CTA that holds its place.
+// items and ranks them 32 at a time with masks and counts of its own; the
+// CTAs read each other's totals through distributed shared memory and send
+// every item to the CTA that holds its place.
 constexpr int kSortCluster = 16;
-constexpr int kMaxItems = 8;  // per thread
-constexpr int64_t kClusterSort = int64_t{kSortCluster} * kSortThreads * kMaxItems;
+constexpr int kClusterThreads = 512;
+constexpr int kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterShare = 2048;  // items per CTA until the cluster is full
+constexpr int kMaxShare = 8192;      // 16-bit counts, and room in shared memory
+constexpr int64_t kClusterSort = int64_t{kSortCluster} * kMaxShare;
 
 struct ClusterSortParams {
     SortParams s;  // ids, keys_out, tokens_out, n, bits, vocab, id_bits
@@ -225,22 +228,22 @@ __device__ __forceinline__ uint4 load_remote(const void* local, uint32_t rank) {
     return v;
 }
 
-template <int kItems> __global__ void __launch_bounds__(kSortThreads) sort_cluster_kernel(const ClusterSortParams a) {
+template <int kItems> __global__ void __launch_bounds__(kClusterThreads) sort_cluster_kernel(const ClusterSortParams a) {
     extern __shared__ uint64_t s_item[];  // [share] key << 32 | token, then the counts
-    __shared__ uint32_t s_scan[kSortWarps];
+    __shared__ uint32_t s_scan[kClusterWarps];
     const int bins = 1 << a.s.bits, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int csize = a.cluster, rank = csize > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int csize = a.cluster, rank = static_cast<int>(cluster_rank());
     // counts are 16-bit: a CTA has at most 8192 items
     uint16_t* const s_total = reinterpret_cast<uint16_t*>(s_item + (a.share + 1) / 2 * 2);  // [bins] this CTA's counts
     uint16_t* const s_counts = s_total + bins;                                             // [warps][bins]
-    uint32_t* const s_place = reinterpret_cast<uint32_t*>(s_counts + kSortWarps * bins);   // [bins] places of its first items
+    uint32_t* const s_place = reinterpret_cast<uint32_t*>(s_counts + kClusterWarps * bins);   // [bins] places of its first items
     uint16_t* const s_warp = s_counts + warp * bins;
     const int64_t base = static_cast<int64_t>(rank) * a.share;
     const int count = static_cast<int>(a.s.n - base < a.share ? (a.s.n > base ? a.s.n - base : 0) : a.share);
     const int mine = warp * 32 * kItems + lane;  // item i of this thread: mine + 32 i
 
     launch_next();
-    for (int64_t i = static_cast<int64_t>(rank) * kSortThreads + tid; i < a.s.clear_n; i += csize * kSortThreads)
+    for (int64_t i = static_cast<int64_t>(rank) * kClusterThreads + tid; i < a.s.clear_n; i += csize * kClusterThreads)
         a.s.clear[i] = 0;
     uint64_t item[kItems];  // key << 32 | token
 #pragma unroll
@@ -273,11 +276,11 @@ template <int kItems> __global__ void __launch_bounds__(kSortThreads) sort_clust
         __syncthreads();
         // the warps' counts become the counts of the warps before, two digits
         // per thread
-        for (int d = tid; d < bins / 2; d += kSortThreads) {
+        for (int d = tid; d < bins / 2; d += kClusterThreads) {
             uint32_t* const c = reinterpret_cast<uint32_t*>(s_counts) + d;
             uint32_t run = 0;
 #pragma unroll 1
-            for (int w0 = 0; w0 < kSortWarps; w0 += 16) {
+            for (int w0 = 0; w0 < kClusterWarps; w0 += 16) {
                 uint32_t n[16];
 #pragma unroll
                 for (int w = 0; w < 16; ++w) n[w] = c[(w0 + w) * (bins / 2)];
@@ -289,8 +292,7 @@ template <int kItems> __global__ void __launch_bounds__(kSortThreads) sort_clust
             }
             reinterpret_cast<uint32_t*>(s_total)[d] = run;
         }
-        if (csize > 1) cluster_sync_all();
-        else __syncthreads();
+        cluster_sync_all();
         // places: items with a lower digit, then those of the CTAs before.
         // A thread takes eight digits.
         uint32_t all[8] = {}, earlier[8] = {}, sum = 0;
@@ -299,7 +301,7 @@ template <int kItems> __global__ void __launch_bounds__(kSortThreads) sort_clust
             for (int i = 0; i < csize; ++i) {
                 // each CTA begins with itself: a CTA answers one at a time
                 const int c = (rank + i) & (csize - 1);
-                const uint4 v = csize > 1 ? load_remote(s_total + 8 * tid, c) : *reinterpret_cast<const uint4*>(s_total + 8 * tid);
+                const uint4 v = load_remote(s_total + 8 * tid, c);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -331,16 +333,13 @@ template <int kItems> __global__ void __launch_bounds__(kSortThreads) sort_clust
             if (pass + 1 == a.passes) {
                 a.s.keys_out[to] = static_cast<uint32_t>(item[i] >> 32);
                 a.s.tokens_out[to] = static_cast<uint32_t>(item[i]);
-            } else if (csize > 1) {
-                store_remote(&s_item[to % a.share], to / a.share, item[i]);
             } else {
-                s_item[to] = item[i];
+                store_remote(&s_item[to % a.share], to / a.share, item[i]);
             }
         }
         // all items sent and all totals read (the last pass reads totals too:
         // no CTA may leave while another reads its shared memory)
-        if (csize > 1) cluster_sync_all();
-        else __syncthreads();
+        cluster_sync_all();
     }
 }
 
@@ -681,9 +680,8 @@ struct SortPlan {
         s.share = 0;
         s.ranks = n <= kRankSort;
         if (!s.ranks && n <= kClusterSort) {
-            // two items per thread until the cluster is full
-            s.cluster = 1;
-            while (s.cluster < kSortCluster && n > int64_t{2} * kSortThreads * s.cluster) s.cluster *= 2;
+            s.cluster = 2;
+            while (s.cluster < kSortCluster && n > int64_t{kClusterShare} * s.cluster) s.cluster *= 2;
             s.share = static_cast<int32_t>(ceil_div(n, s.cluster));
         }
         const int64_t tiles = ceil_div(n, kSortThreads) < kSortTiles ? ceil_div(n, kSortThreads) : kSortTiles;
@@ -726,12 +724,12 @@ struct Workspace {
 
 template <int kItems> drs_status launch_cluster_sort(const ClusterSortParams& a, cudaStream_t stream) {
     const size_t bins = size_t{1} << a.s.bits;
-    const size_t smem = static_cast<size_t>(a.share + 1) * 8 + bins * (2 + 2 * kSortWarps + 4);
+    const size_t smem = static_cast<size_t>(a.share + 1) * 8 + bins * (2 + 2 * kClusterWarps + 4);
     const auto kernel = sort_cluster_kernel<kItems>;
     if (!prepare_kernel(reinterpret_cast<const void*>(kernel), smem, a.cluster > 8)) return DRS_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.cluster));
-    cfg.blockDim = dim3(kSortThreads);
+    cfg.blockDim = dim3(kClusterThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -778,10 +776,10 @@ drs_status sort_tokens(const SortPlan& s, const Workspace& w, const void* ids, i
         a.share = s.share;
         a.passes = s.passes;
         a.cluster = s.cluster;
-        if (s.share <= kSortThreads) return launch_cluster_sort<1>(a, stream);
-        if (s.share <= 2 * kSortThreads) return launch_cluster_sort<2>(a, stream);
-        if (s.share <= 4 * kSortThreads) return launch_cluster_sort<4>(a, stream);
-        return launch_cluster_sort<kMaxItems>(a, stream);
+        constexpr int kFew = kClusterShare / kClusterThreads;
+        if (s.share <= kClusterShare) return launch_cluster_sort<kFew>(a, stream);
+        if (s.share <= 2 * kClusterShare) return launch_cluster_sort<2 * kFew>(a, stream);
+        return launch_cluster_sort<4 * kFew>(a, stream);
     }
     const size_t bins = size_t{1} << s.bits;
     const size_t count_smem = bins * 4, place_smem = bins * 4 + bins * 2 * kSortWarps;
@@ -886,8 +884,6 @@ extern "C" drs_status drs_embed_tokens_grad(const void* grad_out, drs_dtype grad
     a.grad = grad_out;
     a.table = grad_table;
     a.n = tokens;
-    a.piece_bits = piece_bits_of(tokens);
-    a.pieces = pieces_of(tokens);
     a.grad_stride = grad_stride;
     a.table_stride = table_stride;
     a.width = static_cast<int32_t>(width);
@@ -897,6 +893,10 @@ extern "C" drs_status drs_embed_tokens_grad(const void* grad_out, drs_dtype grad
     const bool vec = width % 8 == 0 && aligned(grad_out, 16) && aligned(grad_table, 16) &&
                      grad_stride * dtype_bytes(grad_dtype) % 16 == 0 &&
                      table_stride * dtype_bytes(table_dtype) % 16 == 0;
+    // Single elements per access: pieces twice as long (10007 x 1283 fp32 81.1 ->
+    // 75.6 us; 32768 x 64 in eights 29.5 -> 35.8, so not there).
+    a.piece_bits = piece_bits_of(tokens) + (vec || tokens <= 4096 ? 0 : 1);
+    a.pieces = ceil_div(tokens, int64_t{1} << a.piece_bits);
     lay_out(a, vec ? 8 : 1);
     if (a.sum_blocks + vocab > INT_MAX) return DRS_ERR_UNSUPPORTED;
     if (tokens > 0) {
