@@ -13,9 +13,9 @@
 //
 // Bound by memory: the gradients of the tokens are read once and the table's
 // rows written once; the partial sums are at most 2 / piece of the former.
-// Measured: 32768 x 2048 bf16 into 262144 fp32 rows 318 us, 7.2 TB/s (17 for the
+// Measured: 32768 x 2048 bf16 into 262144 fp32 rows 317 us, 7.2 TB/s (15 for the
 // sort, the rest mostly stores, which alone reach 7.6 TB/s); 2048 x 1024 into
-// 8192 rows 13.8 us, most of it latency.
+// 8192 rows 14.3 us, most of it latency.
 #include <climits>
 
 #include "token_common.cuh"
@@ -589,10 +589,10 @@ __device__ __forceinline__ void join_pieces(const GradParams& a, uint32_t key, i
     write_row<T, kVec>(a, key, col, acc);
 }
 
+// CTAs per SM that registers are held to, measured when the best took 83 and
+// 320 us: with one element per access 8 took 83 us for 10007 x 1283, 6 85 and 5 88;
+// with eight 4 took 320 us for 32768 x 2048, 3 324, 5 339 (spills) and 2 387.
 template <typename G, typename T, int kVec>
-// CTAs per SM that registers are held to: with one element per access 8
-// measured 83 us for 10007 x 1283, 6 85 and 5 88; with eight 4 measured 320
-// us for 32768 x 2048, 3 324, 5 339 (spills) and 2 387.
 __global__ void __launch_bounds__(kSumThreads, kVec == 1 ? 8 : 4) grad_sum_kernel(const GradParams a) {
     extern __shared__ uint32_t s_list[];  // keys, then tokens of the CTA's pieces
     __shared__ int64_t s_start[kSumThreads / kMinColumns][2];
