@@ -402,9 +402,13 @@ extern "C" drs_status drs_map_slots(const int32_t* lens, const int32_t* new_lens
                           static_cast<const void*>(out_held), static_cast<const void*>(out_lacking)})
         if (!aligned(p, 4)) return DRS_ERR_INVALID_ARG;
     if (!aligned(ring_state, 8) || !aligned(out_slot, 8) || !aligned(out_ring_state, 8)) return DRS_ERR_INVALID_ARG;
-    // out_held and out_ring_state may be held and ring_state themselves (read
-    // before the cluster's first barrier, written after it)
+    // out_held and out_ring_state may be held and ring_state themselves: a
+    // request's count is read and written by one thread, the counters are read
+    // at the start and written after the last barrier
     if (out_held && (out_held == lens || out_held == new_lens)) return DRS_ERR_INVALID_ARG;
+
+    const int sms = sm_count();
+    if (sms <= 0) return DRS_ERR_CUDA;
 
     SlotParams a{};
     a.lens = lens;
@@ -426,16 +430,20 @@ extern "C" drs_status drs_map_slots(const int32_t* lens, const int32_t* new_lens
     a.requests = static_cast<int32_t>(requests);
     a.max_blocks = max_blocks;
     a.block = block_size;
-    // Few tokens: one launch, 32 of them per warp until the cluster is full.
-    // Many: the cluster for the requests, then a launch for the tokens.
+    // Few tokens: one launch. Many: the cluster for the requests, then a launch
+    // for the tokens. us in one and in two launches: 64 requests, 512 tokens
+    // 6.7, 8.2; 32 requests, 8192 tokens 7.7, 7.9; 64 requests, 16384 tokens 9.4,
+    // 8.6; 128 requests, 32768 tokens 11.2, 8.8.
     const bool apart = capacity > kSlotCluster * kSlotThreads;
-    // The cluster grows with the requests (256 per CTA), with the tokens that
-    // it maps itself and, apart from them, with the blocks that they may take.
+    // One CTA, or a cluster of 16, by the requests (256 per CTA), the tokens
+    // that the cluster maps itself and, apart from them, the blocks that they
+    // may take. us with 1, 4 and 16 CTAs: 64 requests, 512 tokens 6.7, 7.9, 7.7;
+    // 512 requests, 2048 tokens 13.1, 9.6, 9.1; 4096 requests, 262144 tokens 65.2,
+    // 25.6, 16.1; 128 requests, 32768 tokens (512 blocks) 8.7, 9.2, 9.4.
     int64_t work = requests * 2;
     if (!apart && capacity > work) work = capacity;
     if (apart && capacity / block_size > work) work = capacity / block_size;
-    int cluster = 1;
-    while (cluster < kSlotCluster && work > int64_t{cluster} * kSlotThreads) cluster *= 2;
+    const int cluster = work <= kSlotThreads ? 1 : kSlotCluster;
     a.cluster = cluster;
     const auto kernel = apart ? slots_kernel<false> : slots_kernel<true>;
     if (cluster > 8 && !prepare_kernel(reinterpret_cast<const void*>(kernel), 0, true)) return DRS_ERR_CUDA;
@@ -452,8 +460,6 @@ extern "C" drs_status drs_map_slots(const int32_t* lens, const int32_t* new_lens
     cfg.numAttrs = 1;
     if (cudaLaunchKernelEx(&cfg, kernel, a) != cudaSuccess) return DRS_ERR_CUDA;
     if (!apart) return DRS_OK;
-    const int sms = sm_count();
-    if (sms <= 0) return DRS_ERR_CUDA;
     // up to 8 CTAs per SM, a group of 32 tokens per warp at least
     const int64_t blocks = ceil_div(capacity, 32 * kTokenWarps);
     cudaLaunchConfig_t next{};
