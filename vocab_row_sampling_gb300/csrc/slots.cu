@@ -208,6 +208,7 @@ template <bool kTokens> __global__ void __launch_bounds__(kSlotThreads) slots_ke
     const int b0 = min(lo + static_cast<int64_t>(tid) * run, static_cast<int64_t>(hi));
     const int b1 = min(b0 + run, hi);
 
+    if (csize > 1) cluster_arrive();
     if constexpr (!kTokens) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t head = a.state[0], tail = a.state[1];
     int64_t avail = tail - head;
@@ -219,6 +220,7 @@ template <bool kTokens> __global__ void __launch_bounds__(kSlotThreads) slots_ke
     for (int b = b0; b < b1; ++b) mine += Request::of(a, b).sums();
     Sums at{warp_scan_inclusive(mine.tokens, lane), warp_scan_inclusive(mine.take, lane),
             warp_scan_inclusive(mine.give, lane)};
+    if (csize > 1) cluster_wait();  // the others' shared memory is there
     if (lane == 31) s_warp[warp] = at;
     at.tokens -= mine.tokens, at.take -= mine.take, at.give -= mine.give;
     __syncthreads();

@@ -226,6 +226,18 @@ __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The same barrier in two halves, which all threads call: past the wait every
+// CTA of the cluster has started. Only then may a CTA reach into the shared
+// memory of another; the halves stand apart so that work of the CTA's own hides
+// the barrier. Nothing written before the arrival is handed over.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -233,7 +245,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 
 // Store 8 bytes into the same shared-memory variable of CTA `rank` of the
-// cluster.
+// cluster, which has to have started (a cluster barrier before the first call).
 __device__ __forceinline__ void store_remote(void* local, uint32_t rank, uint64_t v) {
     uint32_t addr;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));

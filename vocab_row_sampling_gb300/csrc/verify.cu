@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kVerifyThreads, resident_ctas(sizeof(P) + size
         }
         return;
     }
+    if (csize > 1) cluster_arrive();
     const P* const target = static_cast<const P*>(a.target) + (first + b) * a.target_stride;
 
     // The accepted drafts, by every warp for itself. u q < p is decided
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__(kVerifyThreads, resident_ctas(sizeof(P) + size
             }
         }
         sum = warp_sum_pair(sum);
+        if (csize > 1 && attempt == 0) cluster_wait();  // the others' shared memory is there
         if (lane == 0) s_warp[warp] = sum;
         __syncthreads();
         if (warp == 0) {
