@@ -87,3 +87,28 @@ def test_a_call_from_within_a_call(stub, monkeypatch):
     done.start()
     done.join(timeout=10)
     assert not done.is_alive() and len(stub.calls) == 2 and not stub.shared
+
+
+def test_what_is_kept_is_bounded(stub, monkeypatch):
+    """A large call's workspace goes back to the allocator with the call, and
+    a stream that is not used again does not keep one for good."""
+    stub.wait = 0.0
+    live = set()
+
+    class Counted(FakeTensor):
+        def __init__(self, *a, **k):
+            super().__init__(*a, **k)
+            self.token = object()
+            live.add((id(self.token), self.numel()))
+
+        def __del__(self):
+            live.discard((id(self.token), self.numel()))
+
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: Counted((n,), dtype))
+    grad_call(1000000)
+    assert sum(size for _, size in live) <= 4 << 20
+    handle = [0]
+    monkeypatch.setattr(drs, "_raw_stream", lambda stream, gpu: handle[0])
+    for handle[0] in range(1, 200):
+        grad_call(500)
+    assert sum(size for _, size in live) <= 64 << 20
