@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kVerifyThreads, resident_ctas(sizeof(P) + size
     // rows outside the arrays: nothing is read (the same for the whole cluster)
     if (first < 0 || first + count > a.draft_rows || first + b + count >= a.target_rows) {
         if (rank == 0) {
-            for (int k = tid; k <= a.max_drafts; k += kVerifyThreads) out[k] = -1;
+            for (int64_t k = tid; k <= a.max_drafts; k += kVerifyThreads) out[k] = -1;
             if (tid == 0) a.out_accepted[b] = -1;
         }
         return;
@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(kVerifyThreads, resident_ctas(sizeof(P) + size
     // exactly, from the product and its rounding error; both sides are taken
     // times 2^100, which keeps the error clear of underflow.
     int accepted = 0;
-    for (int base = 0; base < count; base += 32) {
-        const int j = base + lane;
+    for (int64_t base = 0; base < count; base += 32) {
+        const int64_t j = base + lane;
         bool ok = false;
         if (j < count) {
             const int64_t x = a.tokens[first + j];
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kVerifyThreads, resident_ctas(sizeof(P) + size
     }
     const bool whole = accepted == count;
     if (rank == 0) {
-        for (int k = tid; k <= a.max_drafts; k += kVerifyThreads)
+        for (int64_t k = tid; k <= a.max_drafts; k += kVerifyThreads)
             if (k != accepted) out[k] = k < accepted ? a.tokens[first + k] : -1;
         if (tid == 0) a.out_accepted[b] = accepted;
     }
