@@ -315,12 +315,18 @@ def _dtype_code(t, name: str) -> int:
 
 
 def _raw_stream(stream, gpu: int) -> int:
-    """The stream of a call: torch.cuda.current_stream() alone takes 3 us,
-    more than a launch."""
-    if stream is not None:
-        return stream.cuda_stream
+    """The stream of a call on tensors of this GPU, which has to be the current
+    device, where the library launches (torch.cuda.current_stream() alone takes
+    3 us, more than a launch)."""
     import torch
-    return torch._C._cuda_getCurrentRawStream(gpu)
+    current = torch._C._cuda_getDevice()  # 0.1 us; torch.cuda.current_device() 0.2
+    if gpu != current:
+        raise ValueError(f"tensors on cuda:{gpu}, but the current device is cuda:{current}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(gpu)
+    if stream.device_index != gpu:
+        raise ValueError(f"stream: of cuda:{gpu} expected, got one of cuda:{stream.device_index}")
+    return stream.cuda_stream
 
 
 def _vector(t, name: str, dtype, n: int, gpu: int) -> int:
