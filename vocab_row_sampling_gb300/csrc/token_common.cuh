@@ -152,8 +152,6 @@ __device__ __forceinline__ Pair operator*(float u, Pair a) {
     return normalized(h, fmaf(u, a.s, -h) + u * a.c);
 }
 
-__device__ __forceinline__ bool operator>(Pair a, Pair b) { return (a.s - b.s) + (a.c - b.c) > 0.0f; }
-
 __device__ __forceinline__ Pair shfl_up(Pair v, int o) {
     return Pair{__shfl_up_sync(0xffffffffu, v.s, o), __shfl_up_sync(0xffffffffu, v.c, o)};
 }

@@ -116,14 +116,29 @@ template <typename P, typename Q, bool kVec> struct Weights {
     }
 };
 
+// What a running sum is held against: u times the total. Small totals
+// are taken times 2^100 on both sides, which keeps the product's error clear of
+// underflow (three weights of 2^-149 and u = 1/2: 1.5 steps).
+struct Border {
+    Pair t;
+    float up;
+    __device__ __forceinline__ Border(float u, Pair total) {
+        up = total.s < 0x1p-20f ? 0x1p100f : 1.0f;
+        t = u * Pair{total.s * up, total.c * up};
+    }
+    __device__ __forceinline__ bool below(Pair sum) const {
+        return fmaf(sum.s, up, -t.s) + fmaf(sum.c, up, -t.c) > 0.0f;
+    }
+};
+
 // The first of n shares (a power of two, one per lane) whose running sum
-// from `before` on exceeds t, and in `before` the sum before it; the last
+// from `before` on exceeds the border, and in `before` the sum before it; the last
 // share with any mass where none does.
-__device__ __forceinline__ int pick(const Pair* share, int n, int lane, Pair t, Pair& before) {
+__device__ __forceinline__ int pick(const Pair* share, int n, int lane, const Border& border, Pair& before) {
     const Pair mine = lane < n ? share[lane] : Pair{0.0f, 0.0f};
     const Pair upto = before + warp_scan_pair(mine, lane, n);
     const bool some = lane < n && mine.s > 0.0f;
-    const uint32_t over = __ballot_sync(0xffffffffu, some && upto > t), any = __ballot_sync(0xffffffffu, some);
+    const uint32_t over = __ballot_sync(0xffffffffu, some && border.below(upto)), any = __ballot_sync(0xffffffffu, some);
     const int found = over ? __ffs(over) - 1 : 31 - __clz(any);
     const Pair lower = shfl(upto, found > 0 ? found - 1 : 0);
     if (found > 0) before = lower;
@@ -339,13 +354,13 @@ __global__ void __launch_bounds__(kVerifyThreads, resident_ctas(sizeof(P) + size
     }
 
     // The share that holds the drawn column: the first whose running sum
-    // exceeds t; the last one with any mass where rounding (or u >= 1)
+    // exceeds the border; the last one with any mass where rounding (or u >= 1)
     // leaves none.
-    const Pair t = a.sample_u[b] * total;
+    const Border border(a.sample_u[b], total);
     Pair before{0.0f, 0.0f};
-    const int cta = pick(s_cta[used], csize, lane, t, before);
+    const int cta = pick(s_cta[used], csize, lane, border, before);
     if (rank != cta) return;
-    const int w = pick(s_warp, kVerifyWarps, lane, t, before);
+    const int w = pick(s_warp, kVerifyWarps, lane, border, before);
     const int begin = (rank * kVerifyWarps + w) * part;
     const int end = begin + part < a.vocab ? begin + part : a.vocab;
     int last = -1;  // the last column with a weight that this thread saw
@@ -365,7 +380,7 @@ __global__ void __launch_bounds__(kVerifyThreads, resident_ctas(sizeof(P) + size
         __syncthreads();
         Pair lower = before;
         for (int k = 0; k < warp; ++k) lower = lower + s_scan[k];
-        if (sum.s > 0.0f && lower + scan > t) atomicMin(&s_first, tid);
+        if (sum.s > 0.0f && border.below(lower + scan)) atomicMin(&s_first, tid);
         const Pair left = shfl_up(scan, 1);
         __syncthreads();
         if (s_first == tid) {
@@ -373,7 +388,7 @@ __global__ void __launch_bounds__(kVerifyThreads, resident_ctas(sizeof(P) + size
             int col = last;  // in this thread's eight, as its sum is positive
             for (int e = 0; e < 8; ++e) {
                 run = run + Pair{v[e], 0.0f};
-                if (v[e] > 0.0f && run > t) {
+                if (v[e] > 0.0f && border.below(run)) {
                     col = static_cast<int>(i) + e;
                     break;
                 }
@@ -384,7 +399,7 @@ __global__ void __launch_bounds__(kVerifyThreads, resident_ctas(sizeof(P) + size
         for (int k = 0; k < kVerifyWarps; ++k) before = before + s_scan[k];
         __syncthreads();
     }
-    // The share's sum, added in another order, fell just short of t.
+    // The share's sum, added in another order, fell just short of the border.
     if (tid == 0) s_last = -1;
     __syncthreads();
     atomicMax(&s_last, last);
