@@ -420,9 +420,19 @@ def _id_bits(ids) -> int:
     raise ValueError(f"ids: int32 or int64 expected, got {ids.dtype}")
 
 
+def _no_history(a, b, what: str):
+    """The calls leave no autograd history: refused rather than cut off
+    silently (torch's own functions with `out` do the same)."""
+    import torch
+    if (a.requires_grad or b.requires_grad) and torch.is_grad_enabled():
+        raise ValueError(f"{what}: a tensor requires a gradient, and the call leaves no history; detach it or call "
+                         "under torch.no_grad() (the table's gradient is embed_tokens_grad)")
+
+
 def drs_embed_tokens(table, ids, scale: float, out, stream=None):
     """Launch drs_embed_tokens: table [vocab, width], ids int32 or int64
     [tokens], out [tokens, width] of the table's type."""
+    _no_history(table, out, "drs_embed_tokens")
     gpu = table.get_device()
     table_stride, out_stride = _rows(table, "table"), _rows(out, "out", gpu)
     vocab, width = table.shape
@@ -444,6 +454,7 @@ def drs_embed_tokens_grad(grad_out, ids, scale: float, accumulate: bool, grad_ta
                           stream=None):
     """Launch drs_embed_tokens_grad: grad_out [tokens, width], grad_table
     [vocab, width] (each fp32, bf16 or fp16)."""
+    _no_history(grad_out, grad_table, "drs_embed_tokens_grad")
     gpu = grad_out.get_device()
     grad_stride, table_stride = _rows(grad_out, "grad_out"), _rows(grad_table, "grad_table", gpu)
     vocab, width = grad_table.shape
@@ -734,7 +745,8 @@ def map_slots(lens, new_lens, held, block_table, block_size: int, free_ring, rin
 
 def embed_tokens(table, ids, scale: float = 1.0, out=None, stream=None):
     """scale * table[ids] (see drs_embed_tokens); rows of ids outside the
-    vocabulary are 0."""
+    vocabulary are 0. No autograd history: a table that requires a gradient
+    is refused while autograd records, and its gradient is embed_tokens_grad."""
     import torch
     if out is None:
         with _allocate_on(stream):
