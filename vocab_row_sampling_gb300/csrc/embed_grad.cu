@@ -12,10 +12,12 @@
 // tokens are zeroed in the same launch (unless the call accumulates).
 //
 // Bound by memory: the gradients of the tokens are read once and the table's
-// rows written once; the partial sums are at most 2 / piece of the former.
+// rows written once. The partial sums are at most two rows of fp32 per piece,
+// written and read again: 2 / piece of the elements of the gradients, twice that
+// share of their bytes where those have 16 bits.
 // Measured: 32768 x 2048 bf16 into 262144 fp32 rows 317 us, 7.2 TB/s (15 for the
 // sort, the rest mostly stores, which alone reach 7.6 TB/s); 2048 x 1024 into
-// 8192 rows 14.3 us, most of it latency.
+// 8192 rows 14.2 us, most of it latency.
 #include <climits>
 
 #include "token_common.cuh"
@@ -206,7 +208,11 @@ template <int kPerKey> __global__ void __launch_bounds__(kRankThreads) sort_rank
 constexpr int kSortCluster = 16;
 constexpr int kClusterThreads = 512;
 constexpr int kClusterWarps = kClusterThreads / 32;
-constexpr int kClusterShare = 2048;  // items per CTA until the cluster is full
+// Items per CTA until the cluster is full. us for the whole call of 4097, 8192, 10007,
+// 16384 and 32768 tokens of 64 bf16 columns into 32768 fp32 rows, with 512: 18.8, 19.9,
+// 20.8, 24.7, 28.6; 1024: 17.6, 19.2, 20.8, 24.7, 28.6; 2048: 17.6, 19.9, 19.9, 24.4, 28.6;
+// 4096: 21.2, 24.0, 23.9, 28.5, 33.9.
+constexpr int kClusterShare = 2048;
 constexpr int kMaxShare = 8192;      // 16-bit counts, and room in shared memory
 constexpr int64_t kClusterSort = int64_t{kSortCluster} * kMaxShare;
 
@@ -278,17 +284,13 @@ template <int kItems> __global__ void __launch_bounds__(kClusterThreads) sort_cl
         // per thread
         for (int d = tid; d < bins / 2; d += kClusterThreads) {
             uint32_t* const c = reinterpret_cast<uint32_t*>(s_counts) + d;
-            uint32_t run = 0;
-#pragma unroll 1
-            for (int w0 = 0; w0 < kClusterWarps; w0 += 16) {
-                uint32_t n[16];
+            uint32_t n[kClusterWarps], run = 0;
 #pragma unroll
-                for (int w = 0; w < 16; ++w) n[w] = c[(w0 + w) * (bins / 2)];
+            for (int w = 0; w < kClusterWarps; ++w) n[w] = c[w * (bins / 2)];
 #pragma unroll
-                for (int w = 0; w < 16; ++w) {
-                    c[(w0 + w) * (bins / 2)] = run;
-                    run += n[w];
-                }
+            for (int w = 0; w < kClusterWarps; ++w) {
+                c[w * (bins / 2)] = run;
+                run += n[w];
             }
             reinterpret_cast<uint32_t*>(s_total)[d] = run;
         }
@@ -589,9 +591,10 @@ __device__ __forceinline__ void join_pieces(const GradParams& a, uint32_t key, i
     write_row<T, kVec>(a, key, col, acc);
 }
 
-// CTAs per SM that registers are held to, measured when the best took 83 and
-// 320 us: with one element per access 8 took 83 us for 10007 x 1283, 6 85 and 5 88;
-// with eight 4 took 320 us for 32768 x 2048, 3 324, 5 339 (spills) and 2 387.
+// CTAs per SM that registers are held to. With one element per access 8 take 75.8 us
+// for 10007 x 1283, 6 77.8, 5 and 4 80.0: more rows in flight are worth the 60 bytes
+// per thread that 32 registers spill. With eight 4 take 317 us for 32768 x 2048 (82.2
+// accumulating; 12 to 40 bytes spilled), 3 318 (83.8), 5 336 (105.7) and 2 350 (89.1).
 template <typename G, typename T, int kVec>
 __global__ void __launch_bounds__(kSumThreads, kVec == 1 ? 8 : 4) grad_sum_kernel(const GradParams a) {
     extern __shared__ uint32_t s_list[];  // keys, then tokens of the CTA's pieces
@@ -821,9 +824,9 @@ template <typename G, typename T, int kVec> drs_status launch_sums(GradParams a,
     if (sms <= 0) return DRS_ERR_CUDA;
     int64_t zero_blocks = 0;
     if (!a.accumulate) {
-        // Measured for 32768 x 2048 bf16 into 262144 fp32 rows, when the whole
-        // call took 335 us: 64 KB per CTA 335, 256 KB 343, 1 MB 361. Fewer rows
-        // where that would leave SMs idle.
+        // us with 64 KB, 256 KB and 1 MB per CTA: 32768 x 2048 bf16 into 262144
+        // fp32 rows 317, 323, 337; 10007 x 1283 fp32 into 131072 bf16 rows 75.8,
+        // 85.8, 86.3. Fewer rows where that would leave SMs idle.
         int64_t rows = kZeroBytes / (static_cast<int64_t>(a.width) * sizeof(T));
         const int64_t even = ceil_div(a.vocab, sms * 8);
         rows = rows < even ? rows : even;
