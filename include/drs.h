@@ -469,7 +469,8 @@ drs_status drs_stash_converged_logprobs(const float *logits, int64_t logits_rows
  * read faster. requests == 0 is a no-op. Returns DRS_ERR_INVALID_ARG for
  * negative sizes, an unknown type, a stride below vocab, a null or unaligned
  * pointer; DRS_ERR_UNSUPPORTED for vocab > DRS_MAX_VOCAB or more than
- * 2^27 - 1 requests.
+ * 2^27 - 1 requests; DRS_ERR_CUDA on a device (a partition, say) that grants
+ * no clusters of 16 CTAs, like drs_map_slots and drs_embed_tokens_grad.
  */
 drs_status drs_verify_drafts(const void *target, drs_dtype target_dtype, int64_t target_rows,
                              int64_t target_stride, const void *draft, drs_dtype draft_dtype,
@@ -515,8 +516,8 @@ drs_status drs_verify_drafts(const void *target, drs_dtype target_dtype, int64_t
  *               + position % block_size, -1 where the request has no block
  *               for it. Entries past the last token: -1, 0, -1.
  *
- * Arrays do not overlap except as said. One launch, no workspace; the
- * arrays' contents cannot lead outside them. Positions are at most 2^31 - 1.
+ * Arrays do not overlap except as said. One launch, two above 8192 entries;
+ * no workspace; the arrays' contents cannot lead outside them. Positions are at most 2^31 - 1.
  * Returns DRS_ERR_INVALID_ARG for sizes out of range or a null or
  * unaligned pointer; DRS_ERR_UNSUPPORTED for more than DRS_MAX_REQUESTS
  * requests or 2^31 - 1 tokens.

@@ -12,8 +12,10 @@
 // The tokens then find their request in the offsets and look up their block:
 // in the same launch where there are few, in a launch over all SMs (a
 // programmatic dependent one) where there are many.
-// Measured: 64 decoding requests 7.0 us, 32 canvases of 256 tokens 8.0, 4096
-// requests with 262144 tokens 16.0 (11 for the requests, 5 for the tokens).
+// Measured: 64 decoding requests 7.1 us, 32 canvases of 256 tokens 8.2, 4096
+// requests with 262144 tokens 16.1 (11 for the requests, 5 for the tokens).
+// The CTAs arrive at a cluster barrier when they begin and wait for it before
+// they store into each other's shared memory; the first sums hide it.
 // All sums are 64-bit integers in request order, so the blocks that a
 // request gets do not depend on how the work is split.
 #include <climits>
@@ -434,14 +436,14 @@ extern "C" drs_status drs_map_slots(const int32_t* lens, const int32_t* new_lens
     a.block = block_size;
     // Few tokens: one launch. Many: the cluster for the requests, then a launch
     // for the tokens. us in one and in two launches: 64 requests, 512 tokens
-    // 6.7, 8.2; 32 requests, 8192 tokens 7.7, 7.9; 64 requests, 16384 tokens 9.4,
-    // 8.6; 128 requests, 32768 tokens 11.2, 8.8.
+    // 6.7, 8.0; 512 requests, 2048 tokens 9.2, 10.1; 32 requests, 8192 tokens 8.1, 7.9;
+    // 64 requests, 16384 tokens 9.6, 8.4; 128 requests, 32768 tokens 11.3, 8.7.
     const bool apart = capacity > kSlotCluster * kSlotThreads;
     // One CTA, or a cluster of 16, by the requests (256 per CTA), the tokens
     // that the cluster maps itself and, apart from them, the blocks that they
-    // may take. us with 1, 4 and 16 CTAs: 64 requests, 512 tokens 6.7, 7.9, 7.7;
-    // 512 requests, 2048 tokens 13.1, 9.6, 9.1; 4096 requests, 262144 tokens 65.2,
-    // 25.6, 16.1; 128 requests, 32768 tokens (512 blocks) 8.7, 9.2, 9.4.
+    // may take. us with 1, 4 and 16 CTAs: 64 requests, 512 tokens 6.7, 7.9, 7.9;
+    // 512 requests, 2048 tokens 13.1, 9.6, 9.2; 4096 requests, 262144 tokens 63.7,
+    // 25.3, 16.0; 128 requests, 32768 tokens (512 blocks) 8.7, 9.4, 9.6.
     int64_t work = requests * 2;
     if (!apart && capacity > work) work = capacity;
     if (apart && capacity / block_size > work) work = capacity / block_size;

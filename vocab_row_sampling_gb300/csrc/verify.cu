@@ -15,17 +15,20 @@
 // the CTA whose share holds the drawn column reads one warp's part of it
 // again (from L2) to find the column. Bound by memory for large batches: each
 // needed row is read once. Measured: 256 requests of 262144 bf16 and fp16
-// columns 47.5 us, 4.9 TB/s of those rows (the same reads without the
-// cluster's barrier and the draw 41 us); one request of 131072 columns 6.2 us,
+// columns 47.9 us, 4.9 TB/s of those rows (the same reads without the
+// cluster's barrier and the draw 41 us); one request of 131072 columns 6.3 us,
 // the latency of four dependent loads, a cluster's barrier and a second look.
+// The CTAs arrive at a cluster barrier when they begin and wait for it before
+// they store into each other's shared memory; the sums in between hide it.
 //
 // Sums. A drawn column moves when the running sums are off by more than the
-// distance of u * total to a border, so they are held to about 2^-44: all
-// sums are pairs of fp32 (the sum and the errors of the additions). fp64 sums
-// took most of the kernel's time (165 us for 256 requests of 262144 columns):
-// this GPU issues one fp64 instruction per SM in 16 cycles. The weight
-// itself is the fp32 difference p - q, rounded once (relative 2^-24, exact
-// between values of near exponents).
+// distance of u * total to a border, so they are held to about 2^-44 of the
+// total: all sums are pairs of fp32 (the sum and the errors of the additions).
+// Another column than that of 64-bit sums comes out in about one draw in
+// 10^13 per column. fp64 sums took most of the kernel's time (165 us for 256
+// requests of 262144 columns): this GPU issues one fp64 instruction per SM in 16
+// cycles. The weight itself is the fp32 difference p - q, rounded once
+// (relative 2^-24, exact between values of near exponents).
 #include <climits>
 #include <type_traits>
 
@@ -41,10 +44,11 @@ constexpr int kStep = 256;  // elements a warp takes at once: 8 per lane
 
 struct NoDraft {};
 
-// CTAs per SM that registers are held to: 5 (51 registers) measured 49.5 us
-// for 256 requests of 262144 columns, 4 with twice the loads in flight 49.6, 3
-// 53.7, 6 50.4 and 8 53.7; fp32 rows spill at 5. bytes: of an element of
-// both rows.
+// CTAs per SM that registers are held to: us for 256 requests of 262144 columns
+// with 3, 4, 5, 6 and 8 (16-bit rows): 58.4, 50.9, 47.9, 47.5, 49.7. From 6 on
+// (40 registers) every kernel spills, at 5 some do, by up to 24 bytes per thread,
+// and those of fp32 rows with 16-bit ones by up to 16 at 4.
+// bytes: of an element of both rows.
 constexpr int resident_ctas(size_t bytes) { return bytes < 6 ? 5 : 4; }
 
 struct VerifyParams {
@@ -460,11 +464,12 @@ extern "C" drs_status drs_verify_drafts(const void* target, drs_dtype target_dty
     // CTAs per request: as many as are resident at once (about half an SM's
     // worth is lost to the grouping of clusters, more with 16), 8192 columns
     // (32 per thread) each at least. us at 262144 columns with 4, 8 and 16
-    // CTAs: 32 requests 21.7, 14.4, 11.8; 64 requests 23.6, 17.6, 20.3;
-    // 88 requests 26.1, 20.6, -; 95 requests 26.7, 26.4, - (a second wave).
+    // CTAs: 32 requests 21.3, 14.1, 11.9; 64 requests 23.8, 17.7, 20.7;
+    // 88 requests 26.2, 20.7, 26.6; 95 requests 26.9, 24.6, 27.7 (a second wave;
+    // the rule takes 4 from 86 on).
     // Requests that fill several waves anyway: 32768 columns of 4 bytes per CTA
-    // (256 requests 52.8, 49.0, 63.7 us; 55.0 with 2), or 65536 where that is
-    // one wave (128 requests 29.5, 30.5).
+    // (256 requests 51.5, 48.0, 61.9 us; 55.6 with 2), or 65536 where that is
+    // one wave (128 requests 29.4, 30.0).
     const size_t bytes = dtype_bytes(target_dtype) + (draft ? dtype_bytes(draft_dtype) : 1);
     const bool vec = aligned(target, 16) && target_stride * dtype_bytes(target_dtype) % 16 == 0 &&
                      (!draft || (aligned(draft, 16) && draft_stride * dtype_bytes(draft_dtype) % 16 == 0));
