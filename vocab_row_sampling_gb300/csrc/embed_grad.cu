@@ -167,8 +167,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const SortPara
 // and of equal ones before it, counted by kPerKey threads per token over all
 // keys in shared memory. No passes and no barriers between CTAs.
 // us for the whole call of 2048 tokens (1024 columns), 4096, 6000 and 8192 (512
-// columns) so: 13.8, 28.0, 38.8, 44.3; sorted by a cluster: 17.6, 30.4, 30.6,
-// 31.8 (the comparisons grow with the square).
+// columns) into 8192 rows so: 14.4, 18.2, 28.9, 35.2; sorted by a cluster: 18.3, 18.8,
+// 19.5, 21.6 (the comparisons grow with the square).
 constexpr int kRankThreads = 512;
 constexpr int64_t kRankSort = 4096;
 

@@ -25,7 +25,7 @@
 // distance of u * total to a border, so they are held to about 2^-44 of the
 // total: all sums are pairs of fp32 (the sum and the errors of the additions).
 // Another column than that of 64-bit sums comes out in about one draw in
-// 10^13 per column. fp64 sums took most of the kernel's time (165 us for 256
+// 10^13 per column. fp64 sums took most of the kernel's time (162 us for 256
 // requests of 262144 columns): this GPU issues one fp64 instruction per SM in 16
 // cycles. The weight itself is the fp32 difference p - q, rounded once
 // (relative 2^-24, exact between values of near exponents).
