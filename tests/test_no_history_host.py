@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import vocab_row_sampling_gb300 as drs
-from fake_tensors import FakeTensor, fake_empty
+from fake_tensors import FakeTensor
 from test_current_device_host import stub  # noqa: F401
 
 
