@@ -64,6 +64,10 @@ typedef enum drs_dtype {
 #define DRS_MAX_TOKENS 268435456
 #define DRS_MAX_WIDTH 1048576
 
+/* Largest sizes of drs_token_logprobs: alternatives and rows. */
+#define DRS_MAX_ALTERNATIVES 64
+#define DRS_MAX_SCORE_ROWS 134217727
+
 /*
  * Bytes of device workspace drs_row_stats needs (at least 256-byte aligned,
  * contents arbitrary: each call clears the counters it uses with an
@@ -584,6 +588,127 @@ drs_status drs_embed_tokens_grad(const void *grad_out, drs_dtype grad_dtype, int
                                  void *grad_table, drs_dtype table_dtype, int64_t vocab,
                                  int64_t table_stride, void *workspace, size_t workspace_bytes,
                                  void *stream);
+
+/*
+ * Log probabilities of given tokens under softmax(logits / T), with the
+ * distribution's entropy, the token's rank and the k largest alternatives,
+ * from one read of the logits (scoring of prompts and samples, the forward
+ * pass of a loss). With te = max(T, 1e-10), m = the row's largest logit,
+ * S = the sum over the row of e^((x - m) / te):
+ *   out_logprob  fp32 [rows]: (x_id - m) / te - ln S, the log probability of
+ *                the row's token.
+ *   out_entropy  fp32 [rows]: ln S - (1 / S) * the sum of
+ *                e^((x - m) / te) (x - m) / te; -inf columns drop out.
+ *   out_rank     int32 [rows]: 1 + the number of columns whose logit exceeds
+ *                the token's.
+ *   out_norm     fp32 [rows, 2]: (m, ln S), which drs_token_logprobs_grad
+ *                takes in place of a second look for them.
+ *   out_ids, out_logprobs  int32 and fp32 [rows, k]: the columns of the k
+ *                largest logits (equal ones in column order, -0 equal to 0)
+ *                and their log probabilities.
+ * out_entropy, out_rank and out_norm may be NULL; so may out_ids and
+ * out_logprobs when k is 0.
+ *
+ *   logits      dtype [rows, vocab], row stride row_stride.
+ *   ids         int32 or int64 [rows] (id_bits 32 or 64). A row whose id is
+ *               outside [0, vocab) (padding) is passed over: its outputs are 0,
+ *               0, 0, (0, 0), and -1 and -inf for the alternatives.
+ *   temps       fp32 [ceil(rows / canvas_len)]: row r has
+ *               T = temps[r / canvas_len] (finite or NaN, which is taken as
+ *               1e-10). NULL: 1 for every row.
+ *
+ * A row that is -inf everywhere has no distribution: its log probabilities
+ * are NaN, its entropy 0, its norm (-inf, -inf), its alternatives the first
+ * columns. A row with NaN or +inf has NaN for what depends on its sum; NaN
+ * columns rank below all others, with -inf ones in column order.
+ *
+ * One launch, no workspace. rows == 0 is a no-op. Any stride and alignment
+ * that the type allows. Returns DRS_ERR_INVALID_ARG for sizes out of range
+ * (k > vocab among them), an unknown type, a stride below vocab, a null or
+ * unaligned pointer; DRS_ERR_UNSUPPORTED for vocab > DRS_MAX_VOCAB,
+ * k > DRS_MAX_ALTERNATIVES or rows > DRS_MAX_SCORE_ROWS.
+ */
+drs_status drs_token_logprobs(const void *logits, drs_dtype dtype, int64_t rows, int64_t vocab,
+                              int64_t row_stride, const void *ids, int32_t id_bits,
+                              const float *temps, int64_t canvas_len, int32_t k,
+                              float *out_logprob, float *out_entropy, int32_t *out_rank,
+                              float *out_norm, int32_t *out_ids, float *out_logprobs,
+                              void *stream);
+
+/*
+ * The gradient of drs_token_logprobs' out_logprob and out_entropy with
+ * respect to the logits:
+ *   grad[r, j] = (1 / te) (g ([j == id] - p_j) - h p_j (ln p_j + H))
+ * with p_j = e^((x_j - m) / te - ln S) from the forward call's norm, H its
+ * entropy, g = grad_logprob[r] and h = grad_entropy[r]; computed in fp32 and
+ * rounded once. Rows passed over in the forward call and rows that are -inf
+ * everywhere get zeros; every row is written, and nothing behind vocab.
+ *
+ *   logits, ids, id_bits, temps, canvas_len   as drs_token_logprobs.
+ *   norm         fp32 [rows, 2], out_norm of the forward call.
+ *   entropy      fp32 [rows], out_entropy of the forward call; needed with
+ *                grad_entropy only.
+ *   grad_logprob, grad_entropy  fp32 [rows]; NULL counts as zeros, one of
+ *                them is given.
+ *   grad         grad_dtype [rows, vocab], row stride grad_stride. It may be
+ *                logits itself (of the same type and stride), and does not
+ *                overlap it otherwise.
+ *
+ * One launch, no workspace; equal calls give equal bits. Errors as
+ * drs_token_logprobs.
+ */
+drs_status drs_token_logprobs_grad(const void *logits, drs_dtype dtype, int64_t rows,
+                                   int64_t vocab, int64_t row_stride, const void *ids,
+                                   int32_t id_bits, const float *temps, int64_t canvas_len,
+                                   const float *norm, const float *entropy,
+                                   const float *grad_logprob, const float *grad_entropy,
+                                   void *grad, drs_dtype grad_dtype, int64_t grad_stride,
+                                   void *stream);
+
+/*
+ * Dropout from the counter-based generator, its mask never stored:
+ *   out[r, j] = residual[r, j] + (kept ? x[r, j] / (1 - q) : 0)
+ * in fp32, rounded once; without a residual the second term alone. The share
+ * q dropped is p rounded to a multiple of 2^-16 (ties up), and 1 - q that
+ * of the kept ones, so the expectation is exact; q = 1 drops all. What x
+ * holds in a dropped place has no part in the result (NaN, infinities).
+ * The mask is a function of (seed, global row row0 + r, column): element j is
+ * dropped when the 16-bit number u < q 2^16, with u the lower (j even) or
+ * upper (j odd) half of word (j % 8) / 2 of Philox4x32-10 with the key of
+ * drs_row_stats and counter (j / 8, 0x64726F70, lo32(row), hi32(row)). The
+ * counter's second word keeps it apart from the sampler's noise of the same
+ * seed. A batch split over several calls draws what one call draws.
+ *
+ *   x           dtype [rows, width], row stride x_stride.
+ *   residual    NULL, or out_dtype [rows, width], row stride residual_stride.
+ *   seed        the key; device_seed, when not NULL, is read in its place on
+ *               the GPU (one uint64): a captured graph then draws anew at
+ *               each replay from what stands there.
+ *   out         out_dtype [rows, width], row stride out_stride. It may be x
+ *               (of the same type and stride) or residual (of the same
+ *               stride) itself, and does not overlap them otherwise.
+ *
+ * One launch, no workspace. rows == 0 is a no-op. Returns
+ * DRS_ERR_INVALID_ARG for sizes out of range, p outside [0, 1], an unknown
+ * type, a stride below width, a null or unaligned pointer;
+ * DRS_ERR_UNSUPPORTED for width > DRS_MAX_WIDTH or too many rows for one
+ * launch (2^31 - 1 blocks).
+ */
+drs_status drs_dropout(const void *x, drs_dtype dtype, int64_t rows, int64_t width,
+                       int64_t x_stride, const void *residual, int64_t residual_stride, float p,
+                       uint64_t seed, const uint64_t *device_seed, int64_t row0, void *out,
+                       drs_dtype out_dtype, int64_t out_stride, void *stream);
+
+/*
+ * The gradient of drs_dropout with respect to x, from the same p, seed and
+ * row0: grad_x[r, j] = kept ? grad_out[r, j] / (1 - q) : 0 (that with
+ * respect to the residual is grad_out itself). grad_x may be grad_out (of
+ * the same type and stride). Errors as drs_dropout.
+ */
+drs_status drs_dropout_grad(const void *grad_out, drs_dtype grad_dtype, int64_t rows,
+                            int64_t width, int64_t grad_stride, float p, uint64_t seed,
+                            const uint64_t *device_seed, int64_t row0, void *grad_x,
+                            drs_dtype x_dtype, int64_t x_stride, void *stream);
 
 /* Static, human-readable name of a status code. */
 const char *drs_status_string(drs_status s);

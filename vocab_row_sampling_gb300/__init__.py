@@ -13,11 +13,13 @@ Entry points (same names as the C ABI):
   drs_topk_workspace_bytes, drs_philox_gumbel, drs_scaled_logits,
   drs_stash_converged_logprobs, drs_stash_workspace_bytes,
   drs_verify_drafts, drs_map_slots, drs_embed_tokens, drs_embed_tokens_grad,
-  drs_embed_tokens_grad_workspace_bytes,
+  drs_embed_tokens_grad_workspace_bytes, drs_token_logprobs,
+  drs_token_logprobs_grad, drs_dropout, drs_dropout_grad,
   drs_status_string, drs_get_device_error.
 Convenience wrappers that allocate outputs: row_stats, row_stats_topk,
 topk_logprobs, philox_gumbel, stash_converged_logprobs, verify_drafts,
-map_slots, embed_tokens, embed_tokens_grad.
+map_slots, embed_tokens, embed_tokens_grad, token_logprobs,
+token_logprobs_grad, dropout, dropout_grad.
 """
 from __future__ import annotations
 
@@ -41,6 +43,8 @@ DRS_MAX_VOCAB = 2097152
 DRS_MAX_REQUESTS = 1048576
 DRS_MAX_TOKENS = 268435456
 DRS_MAX_WIDTH = 1048576
+DRS_MAX_ALTERNATIVES = 64
+DRS_MAX_SCORE_ROWS = 134217727
 
 EXPORTED = ("drs_row_stats", "drs_row_stats_workspace_bytes", "drs_row_stats_noalloc",
             "drs_row_stats_topk", "drs_row_stats_topk_workspace_bytes", "drs_topk_logprobs",
@@ -50,7 +54,8 @@ EXPORTED = ("drs_row_stats", "drs_row_stats_workspace_bytes", "drs_row_stats_noa
             "drs_row_stats_seeds_workspace_bytes", "drs_stash_converged_logprobs",
             "drs_stash_workspace_bytes", "drs_test_two_pass",
             "drs_row_split_plan", "drs_verify_drafts", "drs_map_slots", "drs_embed_tokens",
-            "drs_embed_tokens_grad", "drs_embed_tokens_grad_workspace_bytes")
+            "drs_embed_tokens_grad", "drs_embed_tokens_grad_workspace_bytes", "drs_token_logprobs",
+            "drs_token_logprobs_grad", "drs_dropout", "drs_dropout_grad")
 
 
 class DrsError(RuntimeError):
@@ -140,6 +145,17 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.drs_embed_tokens_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i32, ctypes.c_float,
                                           ctypes.c_int, vp, ctypes.c_int, i64, i64, vp, sz, vp]
     lib.drs_embed_tokens_grad.restype = ctypes.c_int
+    lib.drs_token_logprobs.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i32, vp, i64, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.drs_token_logprobs.restype = ctypes.c_int
+    lib.drs_token_logprobs_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i32, vp, i64, vp, vp, vp, vp, vp,
+                                            ctypes.c_int, i64, vp]
+    lib.drs_token_logprobs_grad.restype = ctypes.c_int
+    lib.drs_dropout.argtypes = [vp, ctypes.c_int, i64, i64, i64, vp, i64, ctypes.c_float, u64, vp, i64, vp,
+                                ctypes.c_int, i64, vp]
+    lib.drs_dropout.restype = ctypes.c_int
+    lib.drs_dropout_grad.argtypes = [vp, ctypes.c_int, i64, i64, i64, ctypes.c_float, u64, vp, i64, vp, ctypes.c_int,
+                                     i64, vp]
+    lib.drs_dropout_grad.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -420,13 +436,13 @@ def _id_bits(ids) -> int:
     raise ValueError(f"ids: int32 or int64 expected, got {ids.dtype}")
 
 
-def _no_history(a, b, what: str):
+def _no_history(a, b, what: str, gradient: str = "the table's gradient is embed_tokens_grad"):
     """The calls leave no autograd history: refused rather than cut off
     silently (torch's own functions with `out` do the same)."""
     import torch
     if (a.requires_grad or b.requires_grad) and torch.is_grad_enabled():
         raise ValueError(f"{what}: a tensor requires a gradient, and the call leaves no history; detach it or call "
-                         "under torch.no_grad() (the table's gradient is embed_tokens_grad)")
+                         f"under torch.no_grad() ({gradient})")
 
 
 def drs_embed_tokens(table, ids, scale: float, out, stream=None):
@@ -472,6 +488,116 @@ def drs_embed_tokens_grad(grad_out, ids, scale: float, accumulate: bool, grad_ta
                                       _dtype_code(grad_table, "grad_table"), vocab, table_stride, ws, ws_bytes,
                                       _raw_stream(stream, gpu))
     _check(st, "drs_embed_tokens_grad")
+
+
+def _temps(temps, rows: int, canvas_len: int, gpu: int):
+    import torch
+    if canvas_len < 1:
+        raise ValueError(f"canvas_len: at least 1 expected, got {canvas_len}")
+    return None if temps is None else _vector(temps, "temps", torch.float32, -(-rows // canvas_len), gpu)
+
+
+def drs_token_logprobs(logits, ids, temps, canvas_len: int, out_logprob, out_entropy, out_rank, out_norm, out_ids,
+                       out_logprobs, stream=None):
+    """Launch drs_token_logprobs: logits [rows, vocab], ids int32 or int64
+    [rows]; k is the width of out_ids [rows, k]. out_entropy, out_rank and
+    out_norm may be None, out_ids and out_logprobs too (k = 0)."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    _no_history(logits, out_logprob, "drs_token_logprobs", "the logits' gradient is token_logprobs_grad")
+    stride = _rows(logits, "logits")
+    gpu = logits.get_device()
+    rows, vocab = logits.shape
+    k = 0
+    if out_ids is not None:
+        if out_ids.dim() != 2:
+            raise ValueError(f"out_ids: [{rows}, k] expected, got {tuple(out_ids.shape)}")
+        k = out_ids.shape[1]
+    if (out_ids is None) != (out_logprobs is None):
+        raise ValueError("out_ids and out_logprobs: both or neither expected")
+    st = load().drs_token_logprobs(
+        logits.data_ptr(), _dtype_code(logits, "logits"), rows, vocab, stride,
+        _vector(ids, "ids", ids.dtype, rows, gpu), _id_bits(ids), _temps(temps, rows, canvas_len, gpu), canvas_len, k,
+        _vector(out_logprob, "out_logprob", f32, rows, gpu),
+        None if out_entropy is None else _vector(out_entropy, "out_entropy", f32, rows, gpu),
+        None if out_rank is None else _vector(out_rank, "out_rank", i32, rows, gpu),
+        None if out_norm is None else _vector(out_norm, "out_norm", f32, 2 * rows, gpu),
+        None if out_ids is None else _vector(out_ids, "out_ids", i32, rows * k, gpu),
+        None if out_ids is None else _vector(out_logprobs, "out_logprobs", f32, rows * k, gpu), _raw_stream(stream, gpu))
+    _check(st, "drs_token_logprobs")
+
+
+def drs_token_logprobs_grad(logits, ids, temps, canvas_len: int, norm, entropy, grad_logprob, grad_entropy, grad,
+                            stream=None):
+    """Launch drs_token_logprobs_grad: grad [rows, vocab] (fp32, bf16 or fp16,
+    or logits itself); grad_logprob or grad_entropy may be None, entropy
+    without grad_entropy too."""
+    import torch
+    f32 = torch.float32
+    _no_history(logits, grad, "drs_token_logprobs_grad", "there is no second derivative")
+    stride = _rows(logits, "logits")
+    gpu = logits.get_device()
+    grad_stride = _rows(grad, "grad", gpu)
+    rows, vocab = logits.shape
+    if grad.shape != logits.shape:
+        raise ValueError(f"grad: {(rows, vocab)} expected, got {tuple(grad.shape)}")
+    st = load().drs_token_logprobs_grad(
+        logits.data_ptr(), _dtype_code(logits, "logits"), rows, vocab, stride,
+        _vector(ids, "ids", ids.dtype, rows, gpu), _id_bits(ids), _temps(temps, rows, canvas_len, gpu), canvas_len,
+        _vector(norm, "norm", f32, 2 * rows, gpu), None if entropy is None else _vector(entropy, "entropy", f32, rows, gpu),
+        None if grad_logprob is None else _vector(grad_logprob, "grad_logprob", f32, rows, gpu),
+        None if grad_entropy is None else _vector(grad_entropy, "grad_entropy", f32, rows, gpu),
+        grad.data_ptr(), _dtype_code(grad, "grad"), grad_stride, _raw_stream(stream, gpu))
+    _check(st, "drs_token_logprobs_grad")
+
+
+def _seed(seed, gpu: int):
+    """(host seed, address of the device's): an int, or an int64 or uint64 tensor of one element on the GPU."""
+    if isinstance(seed, int):
+        return seed & (2**64 - 1), None
+    import torch
+    if seed.dtype not in (torch.int64, torch.uint64):
+        raise ValueError(f"seed: an int or one int64 on the GPU expected, got {seed.dtype}")
+    return 0, _vector(seed, "seed", seed.dtype, 1, gpu)
+
+
+def drs_dropout(x, residual, p: float, seed, row0: int, out, stream=None):
+    """Launch drs_dropout: x and out [rows, width], residual None or of out's
+    type and shape; seed an int or an int64 tensor of one element on the GPU."""
+    _no_history(x, out, "drs_dropout", "the gradient is dropout_grad")
+    gpu = x.get_device()
+    x_stride, out_stride = _rows(x, "x"), _rows(out, "out", gpu)
+    rows, width = x.shape
+    if out.shape != x.shape:
+        raise ValueError(f"out: {(rows, width)} expected, got {tuple(out.shape)}")
+    residual_ptr, residual_stride = None, 0
+    if residual is not None:
+        _no_history(residual, out, "drs_dropout", "the residual's gradient is the output's")
+        residual_ptr, residual_stride = residual.data_ptr(), _rows(residual, "residual", gpu)
+        if residual.dtype is not out.dtype or residual.shape != out.shape:
+            raise ValueError(f"residual: {out.dtype} {(rows, width)} expected, got {residual.dtype} "
+                             f"{tuple(residual.shape)}")
+    key, device_key = _seed(seed, gpu)
+    st = load().drs_dropout(x.data_ptr(), _dtype_code(x, "x"), rows, width, x_stride, residual_ptr, residual_stride, p,
+                            key, device_key, row0, out.data_ptr(), _dtype_code(out, "out"), out_stride,
+                            _raw_stream(stream, gpu))
+    _check(st, "drs_dropout")
+
+
+def drs_dropout_grad(grad_out, p: float, seed, row0: int, grad_x, stream=None):
+    """Launch drs_dropout_grad: grad_out and grad_x [rows, width] (each fp32,
+    bf16 or fp16); seed as drs_dropout."""
+    _no_history(grad_out, grad_x, "drs_dropout_grad", "the gradient of a gradient is dropout_grad again")
+    gpu = grad_out.get_device()
+    grad_stride, x_stride = _rows(grad_out, "grad_out"), _rows(grad_x, "grad_x", gpu)
+    rows, width = grad_out.shape
+    if grad_x.shape != grad_out.shape:
+        raise ValueError(f"grad_x: {(rows, width)} expected, got {tuple(grad_x.shape)}")
+    key, device_key = _seed(seed, gpu)
+    st = load().drs_dropout_grad(grad_out.data_ptr(), _dtype_code(grad_out, "grad_out"), rows, width, grad_stride, p,
+                                 key, device_key, row0, grad_x.data_ptr(), _dtype_code(grad_x, "grad_x"), x_stride,
+                                 _raw_stream(stream, gpu))
+    _check(st, "drs_dropout_grad")
 
 
 KERNEL_NAMES = ("split_prep", "split_pass1", "split_merge", "split_pass2", "split_cluster",
@@ -783,3 +909,65 @@ def embed_tokens_grad(grad_out, ids, scale: float, grad_table, accumulate: bool 
         with kept.lock:
             drs_embed_tokens_grad(grad_out, ids, scale, accumulate, grad_table, kept.at_least(size, gpu))
     return grad_table
+
+
+def token_logprobs(logits, ids, k: int = 0, temps=None, canvas_len: int = 1, out=None, stream=None):
+    """Log probabilities of the rows' tokens under softmax(logits / T), with
+    entropy, rank and the k largest alternatives (see drs_token_logprobs).
+    Returns `out`: (logprob, entropy, rank, norm [rows, 2], top_ids [rows, k],
+    top_logprobs [rows, k]), allocated when not given. No autograd history:
+    the gradient is token_logprobs_grad, which takes norm and entropy."""
+    import torch
+    if out is None:
+        dev, rows = logits.device, logits.shape[0]
+        f32, i32 = dict(dtype=torch.float32, device=dev), dict(dtype=torch.int32, device=dev)
+        with _allocate_on(stream):
+            out = (torch.empty(rows, **f32), torch.empty(rows, **f32), torch.empty(rows, **i32),
+                   torch.empty(rows, 2, **f32), torch.empty(rows, k, **i32), torch.empty(rows, k, **f32))
+    elif out[4] is None:
+        if k != 0:
+            raise ValueError(f"out: [rows, {k}] alternatives expected, got none")
+    elif out[4].shape != (logits.shape[0], k):
+        raise ValueError(f"out: [{logits.shape[0]}, {k}] alternatives expected, got {tuple(out[4].shape)}")
+    drs_token_logprobs(logits, ids, temps, canvas_len, *out, stream=stream)
+    return out
+
+
+def token_logprobs_grad(logits, ids, norm, grad_logprob, entropy=None, grad_entropy=None, temps=None,
+                        canvas_len: int = 1, out=None, stream=None):
+    """The gradient of token_logprobs' logprob and entropy with respect to the
+    logits, from its norm (and entropy, with grad_entropy), written into out
+    [rows, vocab] (allocated in the logits' type when not given; logits
+    itself is allowed), which is returned (see drs_token_logprobs_grad)."""
+    import torch
+    if out is None:
+        with _allocate_on(stream):
+            out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    drs_token_logprobs_grad(logits, ids, temps, canvas_len, norm, entropy, grad_logprob, grad_entropy, out, stream)
+    return out
+
+
+def dropout(x, p: float, seed, residual=None, row0: int = 0, out=None, stream=None):
+    """Dropout of x [rows, width], added to the residual when one is given
+    (see drs_dropout): the mask follows from seed (an int, or an int64 tensor
+    of one element on the GPU), row0 and the place, and is not stored. out:
+    of the residual's type, or x's, when not given. No autograd history: the
+    gradient is dropout_grad."""
+    import torch
+    if out is None:
+        with _allocate_on(stream):
+            out = torch.empty(x.shape, dtype=x.dtype if residual is None else residual.dtype, device=x.device)
+    drs_dropout(x, residual, p, seed, row0, out, stream)
+    return out
+
+
+def dropout_grad(grad_out, p: float, seed, row0: int = 0, out=None, stream=None):
+    """The gradient of dropout with respect to x, from the p, seed and row0 of
+    the forward call, written into out (allocated in grad_out's type when not
+    given; grad_out itself is allowed), which is returned."""
+    import torch
+    if out is None:
+        with _allocate_on(stream):
+            out = torch.empty(grad_out.shape, dtype=grad_out.dtype, device=grad_out.device)
+    drs_dropout_grad(grad_out, p, seed, row0, out, stream)
+    return out

@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(PKG_DIR, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libdrs.so")
 
 SOURCES = ["capi.cu", "row_stats.cu", "row_split.cu", "row_cluster.cu", "topk.cu", "stash.cu", "philox_gumbel.cu", "scale.cu",
-           "verify.cu", "slots.cu", "embed.cu", "embed_grad.cu"]
+           "verify.cu", "slots.cu", "embed.cu", "embed_grad.cu", "logprobs.cu", "logprobs_grad.cu", "dropout.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 # No fast-math: IEEE division, denormals kept (the probabilities can be
 # fp32 subnormals that are still representable in bf16).
