@@ -1,14 +1,21 @@
 // logprobs.cu -- log probabilities of given tokens with entropy, rank and top
 // alternatives (drs_token_logprobs).
 //
-// s_j = x_j / T, m = max x, S = sum e^((x_j - m) / T):
-//   logprob = (x_id - m) / T - ln S
-//   entropy = ln S - (1 / S) sum e^((x_j - m) / T) (x_j - m) / T
+// With c = log2(e) / T and t_j = (x_j - M) c for any reference M:
+//   S = sum 2^t_j, W = sum 2^t_j t_j
+//   ln of the softmax's denominator relative to M: ln S
+//   entropy = ln 2 (log2 S - W / S)
 //   rank    = 1 + the number of x_j > x_id
-// The alternatives are the k largest x_j, equal ones in column order.
+// M is a warp's running reference, raised when a segment's largest logit
+// passes it by more than 2^8 in the exponent; S and W then move along:
+// S' = 2^d S, W' = 2^d (W + d S) with d = (M - M') c.
 //
-// A CTA takes a row: its largest logit, then the sums, then the alternatives
-// one after the other, each as the largest key below the one before.
+// One read of the row. A CTA (or a cluster of them) takes a row, its warps segments of
+// 256 columns, and keep each segment's largest logit in shared memory. The k
+// largest logits lie in the k segments whose largest logits come first (by
+// value, then by column): any logit of another segment has k before it, one in
+// each of these. So only k segments are looked at again, from L2, and of
+// these only what reaches the k-th segment's largest.
 #include <climits>
 
 #include "token_common.cuh"
@@ -18,9 +25,15 @@ namespace {
 
 constexpr int kThreadsPerRow = 256;
 constexpr int kRowWarps = kThreadsPerRow / 32;
+constexpr int kMaxRowCluster = 16;
+constexpr int kSegment = 256;   // columns a warp takes at once: 8 per lane
+constexpr int kTile = 4;        // segments whose loads a warp has in flight
+constexpr int kMaxSegments = 2048;  // per CTA
+constexpr int kListed = 512;    // candidates of the short way
 // Exponents (base 2) below this give 0; held there so that 0 times an
-// infinite exponent does not arise in the entropy's sum.
+// infinite exponent does not arise in W.
 constexpr float kLeastExponent = -200.0f;
+constexpr float kSlack = 8.0f;  // exponents above the reference before it moves
 
 struct LogprobParams {
     const void* logits;
@@ -33,23 +46,10 @@ struct LogprobParams {
     int32_t* out_ids;
     float* out_logprobs;
     int64_t row_stride, canvas_len;
-    int32_t vocab, k;
+    int32_t vocab, k, id_bits, cluster, segments;  // segments: of a CTA
 };
 
-// Larger keys: larger values, then lower columns. NaN counts as -inf, -0 as 0.
-__device__ __forceinline__ uint64_t key_of(float v, int column) {
-    v = fmaxf(v, -INFINITY) + 0.0f;
-    const uint32_t b = __float_as_uint(v);
-    const uint32_t order = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-    return static_cast<uint64_t>(order) << 32 | static_cast<uint32_t>(~column);
-}
-
-__device__ __forceinline__ float value_of(uint64_t key) {
-    const uint32_t order = static_cast<uint32_t>(key >> 32);
-    return __uint_as_float(order ^ (order >> 31 ? 0x80000000u : 0xFFFFFFFFu));
-}
-
-__device__ __forceinline__ int column_of(uint64_t key) { return static_cast<int>(~static_cast<uint32_t>(key)); }
+// ------------------------------------------------------------- elements
 
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
@@ -57,81 +57,487 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-template <typename V, typename F> __device__ V block_reduce(V v, V* s_part, F f) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-    __syncthreads();
-    if (lane == 0) s_part[warp] = v;
-    __syncthreads();
-    v = s_part[0];
-    for (int w = 1; w < kRowWarps; ++w) v = f(v, s_part[w]);
-    return v;
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
-template <typename T, typename I> __global__ void __launch_bounds__(kThreadsPerRow) logprob_kernel(const LogprobParams a) {
-    __shared__ uint64_t s_key[kRowWarps];
-    __shared__ float s_float[kRowWarps];
-    __shared__ int s_int[kRowWarps];
-    const int64_t row = blockIdx.x;
-    const int64_t id = static_cast<int64_t>(static_cast<const I*>(a.ids)[row]);
-    if (id < 0 || id >= a.vocab) {
-        if (threadIdx.x == 0) {
-            a.out_logprob[row] = 0.0f;
-            if (a.out_entropy) a.out_entropy[row] = 0.0f;
-            if (a.out_rank) a.out_rank[row] = 0;
-            if (a.out_norm) a.out_norm[2 * row] = a.out_norm[2 * row + 1] = 0.0f;
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// The largest of eight elements (NaN left out), and how many exceed a value,
+// counted over a tile: 16-bit elements in pairs of 16-bit sums (whole numbers
+// of at most 4 per segment in each half).
+template <typename T> struct Eight;
+template <> struct Eight<float> {
+    using Count = int;
+    __device__ static float largest(const Raw8<float>& r) {
+        float v[8];
+        r.unpack(v);
+        return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+    }
+    __device__ static Count zero() { return 0; }
+    __device__ static void count(const Raw8<float>& r, float own, Count& n) {
+        float v[8];
+        r.unpack(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) n += v[e] > own;
+    }
+    __device__ static int total(Count n) { return n; }
+};
+template <typename T, typename T2> struct EightHalves {
+    using Count = T2;
+    __device__ static T2 pair(uint32_t w) { return *reinterpret_cast<const T2*>(&w); }
+    __device__ static float largest(const Raw8<T>& r) {
+        const T2 m = __hmax2(__hmax2(pair(r.w[0].x), pair(r.w[0].y)), __hmax2(pair(r.w[0].z), pair(r.w[0].w)));
+        return fmaxf(to_f(m.x), to_f(m.y));
+    }
+    __device__ static Count zero() { return pair(0); }
+    __device__ static void count(const Raw8<T>& r, T own, Count& n) {
+        T2 o;
+        o.x = o.y = own;
+        n = __hadd2(n, __hadd2(__hadd2(__hgt2(pair(r.w[0].x), o), __hgt2(pair(r.w[0].y), o)),
+                               __hadd2(__hgt2(pair(r.w[0].z), o), __hgt2(pair(r.w[0].w), o))));
+    }
+    __device__ static int total(Count n) { return static_cast<int>(to_f(n.x) + to_f(n.y)); }
+};
+template <> struct Eight<__nv_bfloat16> : EightHalves<__nv_bfloat16, __nv_bfloat162> {};
+template <> struct Eight<__half> : EightHalves<__half, __half2> {};
+
+// A row as a line of aligned units of eight elements: column j stands at
+// place j + lead, so that units start on 16-byte boundaries; places outside the
+// row count as -inf and are not read.
+template <typename T> struct Row {
+    const T* first;  // place 0
+    int lead, end;   // places of columns 0 and vocab
+
+    __device__ Row(const T* x, int vocab) {
+        lead = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
+        first = x - lead;
+        end = vocab + lead;
+    }
+    __device__ __forceinline__ bool whole(int place, int n) const { return place >= lead && place + n <= end; }
+    __device__ __forceinline__ Raw8<T> unit(int place) const {
+        Raw8<T> r;
+        if (whole(place, 8)) {
+            r.load(first + place);
+        } else {
+            T* const e = reinterpret_cast<T*>(&r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                e[i] = place + i >= lead && place + i < end ? first[place + i] : from_f<T>(-INFINITY);
         }
-        for (int i = threadIdx.x; i < a.k; i += kThreadsPerRow) {
-            a.out_ids[row * a.k + i] = -1;
-            a.out_logprobs[row * a.k + i] = -INFINITY;
+        return r;
+    }
+};
+
+// ------------------------------------------------------------- keys
+
+// Whole numbers in the order of the values: NaN counts as -inf, -0 as 0.
+__device__ __forceinline__ uint32_t order_of(float v) {
+    const uint32_t b = __float_as_uint(fmaxf(v, -INFINITY) + 0.0f);
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float value_of(uint32_t order) {
+    return __uint_as_float(order ^ (order >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// Larger keys: larger values, then lower places. No key is 0.
+__device__ __forceinline__ uint64_t key_of(uint32_t order, int place) {
+    return static_cast<uint64_t>(order) << 32 | static_cast<uint32_t>(~place);
+}
+
+__device__ __forceinline__ int place_of(uint64_t key) { return static_cast<int>(~static_cast<uint32_t>(key)); }
+
+// ------------------------------------------------------------- selection
+
+struct Selection {
+    uint64_t list[kListed];              // candidates: keys of segments, then of elements
+    uint32_t unit[DRS_MAX_ALTERNATIVES * 32];  // orders of units' largest, then of elements
+    int chosen[2][DRS_MAX_ALTERNATIVES];
+    uint64_t best[DRS_MAX_ALTERNATIVES];  // the CTA's k largest, in order
+    int counts[32];
+    int n, m;
+};
+
+// How many of the n keys exceed this one.
+__device__ __forceinline__ int keys_above(const uint64_t* list, int n, uint64_t key) {
+    int above = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) above += list[i] > key;
+    return above;
+}
+
+// A value that at least k of the n > k values reach, by every warp for itself: the
+// k-th largest of the largest of 32 (k <= 32) or 64 groups of them.
+__device__ __forceinline__ uint32_t reached_by(const uint32_t* value, int n, int k, int lane) {
+    uint32_t a = 0, b = 0;  // below every order
+    int above_a = 0, above_b = 0;
+    if (k <= 32) {
+        for (int i = lane; i < n; i += 32) a = max(a, value[i]);
+#pragma unroll 8
+        for (int i = 0; i < 32; ++i) above_a += __shfl_sync(0xffffffffu, a, i) > a;
+        return __reduce_min_sync(0xffffffffu, above_a < k ? a : 0xffffffffu);  // the smallest that fewer than k exceed
+    }
+    for (int i = lane; i < n; i += 64) {
+        a = max(a, value[i]);
+        if (i + 32 < n) b = max(b, value[i + 32]);
+    }
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+        const uint32_t u = __shfl_sync(0xffffffffu, a, i), v = __shfl_sync(0xffffffffu, b, i);
+        above_a += (u > a) + (v > a);
+        above_b += (u > b) + (v > b);
+    }
+    return __reduce_min_sync(0xffffffffu, min(above_a < k ? a : 0xffffffffu, above_b < k ? b : 0xffffffffu));
+}
+
+// The k largest of n values, equal ones by index, as indices in ascending
+// order (all when n <= k): their number. By all threads; any values.
+__device__ int select_exact(const uint32_t* value, int n, int k, int* chosen, Selection& s) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    if (n <= k) {
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreadsPerRow) chosen[i] = i;
+        __syncthreads();
+        return n;
+    }
+    __syncthreads();
+    if (tid < 32) s.counts[tid] = 0;
+    __syncthreads();
+    uint32_t least = 0;  // the largest number that at least k values reach, bit by bit
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t next = least | 1u << bit;
+        int reach = 0;
+        for (int i = tid; i < n; i += kThreadsPerRow) reach += value[i] >= next;
+        reach = __reduce_add_sync(0xffffffffu, reach);
+        if (lane == 0) atomicAdd(&s.counts[bit], reach);
+        __syncthreads();
+        reach = s.counts[bit];
+        if (reach >= k) least = next;
+        if (reach == k) break;
+    }
+    if (tid < 32) {  // those above, and the first of the equal ones
+        int above = 0;
+        for (int i = lane; i < n; i += 32) above += value[i] > least;
+        int ties = k - __reduce_add_sync(0xffffffffu, above), at = 0;
+        for (int i = lane; i - lane < n && at < k; i += 32) {
+            const uint32_t v = i < n ? value[i] : 0;
+            const uint32_t more = __ballot_sync(0xffffffffu, v > least);
+            const uint32_t same = __ballot_sync(0xffffffffu, i < n && v == least);
+            const uint32_t below = (1u << lane) - 1;
+            const int rank = __popc(same & below);
+            const bool take = (more >> lane & 1) || ((same >> lane & 1) && rank < ties);
+            const uint32_t taken = __ballot_sync(0xffffffffu, take);
+            if (take) chosen[at + __popc(taken & below)] = i;
+            at += __popc(taken);
+            ties -= min(ties, __popc(same));
+        }
+    }
+    __syncthreads();
+    return k;
+}
+
+// The CTA's k largest logits into s.best, in order, then 0 (where it has fewer
+// columns). segment: the orders of its n segments' largest, first: its
+// first segment.
+template <typename T> __device__ void select_top(const Row<T>& row, const uint32_t* segment, int n, int first, int k,
+                                                 Selection& s) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) s.n = s.m = 0;
+    if (tid < k) s.best[tid] = 0;
+    __syncthreads();
+    int found = -1;
+    if (n > k) {
+        // The short way: segments that reach a bound, k of them, and what in
+        // these reaches the k-th one's largest.
+        const uint32_t bound = reached_by(segment, n, k, lane);
+        for (int i = tid; i < n; i += kThreadsPerRow) {
+            if (segment[i] >= bound) {
+                const int at = atomicAdd(&s.n, 1);
+                if (at < kListed) s.list[at] = key_of(segment[i], i);
+            }
+        }
+        __syncthreads();
+        const int listed = s.n;
+        if (listed <= kListed) {
+            for (int i = tid; i < listed; i += kThreadsPerRow) {
+                const uint64_t key = s.list[i];
+                const int above = keys_above(s.list, listed, key);
+                if (above < k) s.chosen[0][above] = place_of(key);
+            }
+            __syncthreads();
+            const uint32_t least = segment[s.chosen[0][k - 1]];
+            for (int c = warp; c < k; c += kRowWarps) {
+                const int place = (first + s.chosen[0][c]) * kSegment + lane * 8;
+                float v[8];
+                row.unit(place).unpack(v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t order = order_of(v[e]);
+                    if (order >= least && place + e >= row.lead && place + e < row.end) {
+                        const int at = atomicAdd(&s.m, 1);
+                        if (at < kListed) s.list[at] = key_of(order, place + e);
+                    }
+                }
+            }
+            __syncthreads();
+            if (s.m <= kListed) found = s.m;
+        }
+    }
+    if (found < 0) {
+        // The long way, for rows with many equal logits, risen or short ones: the k segments, then their k units of
+        // eight, then their k elements.
+        const int segments = select_exact(segment, n, k, s.chosen[0], s);
+        for (int c = warp; c < segments; c += kRowWarps) {
+            float v[8];
+            const int place = (first + s.chosen[0][c]) * kSegment + lane * 8;
+            row.unit(place).unpack(v);
+            uint32_t most = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (place + e >= row.lead && place + e < row.end) most = max(most, order_of(v[e]));
+            s.unit[c * 32 + lane] = most;
+        }
+        const int units = select_exact(s.unit, segments * 32, k, s.chosen[1], s);
+        if (tid < units) s.chosen[1][tid] = (first + s.chosen[0][s.chosen[1][tid] >> 5]) * 32 + (s.chosen[1][tid] & 31);
+        __syncthreads();
+        for (int i = tid; i < units * 8; i += kThreadsPerRow) {
+            const int place = s.chosen[1][i >> 3] * 8 + (i & 7);
+            s.unit[i] = place >= row.lead && place < row.end ? order_of(to_f(row.first[place])) : 0;
+        }
+        found = select_exact(s.unit, units * 8, k, s.chosen[0], s);
+        if (tid < found) {
+            const int i = s.chosen[0][tid];
+            s.list[tid] = s.unit[i] ? key_of(s.unit[i], s.chosen[1][i >> 3] * 8 + (i & 7)) : 0;
+        }
+        __syncthreads();
+    }
+    for (int i = tid; i < found; i += kThreadsPerRow) {
+        const uint64_t key = s.list[i];
+        const int above = keys_above(s.list, found, key);
+        if (above < k && key) s.best[above] = key;
+    }
+    __syncthreads();
+}
+
+// ------------------------------------------------------------- sums
+
+// S and W relative to `top`, and the number of columns above the token.
+struct Sums {
+    float top, sum, weighted;
+    int above;
+};
+
+// The exponent by which sums relative to `from` are moved to `to`.
+__device__ __forceinline__ float shift_of(float from, float to, float c) {
+    return from == -INFINITY ? 0.0f : max_nan((from - to) * c, -1000.0f);
+}
+
+// The first n lanes' sums together, on every lane.
+__device__ __forceinline__ Sums together(Sums s, bool have, float c) {
+    if (!have) s = Sums{-INFINITY, 0.0f, 0.0f, 0};
+    const float top = warp_max(s.top);
+    const float d = shift_of(s.top, top, c), f = ex2_approx(d);
+    return Sums{top, warp_sum(s.sum * f), warp_sum(f * fmaf(d, s.sum, s.weighted)), warp_sum(s.above)};
+}
+
+// The sums of this thread's part of the CTA's segments; top and reference are the
+// warp's. kTop: the segments' largest go to `segment`.
+template <typename T, bool kTop>
+__device__ __forceinline__ Sums row_sums(const Row<T>& row, int first, int n, float c, T own, uint32_t* segment) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float slack = kSlack / c;
+    float top = -INFINITY, reference = -INFINITY;
+    uint64_t sum = 0, weighted = 0;
+    const uint64_t c2 = pack2(c, c);
+    int above = 0;
+    for (int i = warp * kTile; i < n; i += kRowWarps * kTile) {
+        Raw8<T> raw[kTile];
+        const int place = (first + i) * kSegment + lane * 8;
+        if (i + kTile <= n && row.whole((first + i) * kSegment, kTile * kSegment)) {
+#pragma unroll
+            for (int u = 0; u < kTile; ++u) raw[u].load(row.first + place + u * kSegment);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kTile; ++u) raw[u] = row.unit(place + u * kSegment);
+        }
+        typename Eight<T>::Count exceed = Eight<T>::zero();
+#pragma unroll
+        for (int u = 0; u < kTile; ++u) {
+            if (i + u >= n) break;
+            const float most = warp_max(Eight<T>::largest(raw[u]));
+            if (kTop && lane == 0) segment[i + u] = order_of(most);
+            top = fmaxf(top, most);
+            if (most > reference + slack || reference == -INFINITY) {
+                const float d = shift_of(reference, top, c), f = ex2_approx(d);
+                const uint64_t f2 = pack2(f, f);
+                weighted = mul2(f2, fma2(pack2(d, d), sum, weighted));
+                sum = mul2(f2, sum);
+                reference = top;
+            }
+            const float base = reference == -INFINITY ? 0.0f : reference;
+            const uint64_t base2 = pack2(base, base);
+            float v[8];
+            raw[u].unpack(v);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                float t0, t1;
+                unpack2(mul2(sub2(pack2(v[e], v[e + 1]), base2), c2), t0, t1);
+                t0 = max_nan(t0, kLeastExponent);
+                t1 = max_nan(t1, kLeastExponent);
+                const uint64_t p = pack2(ex2_approx(t0), ex2_approx(t1));
+                sum = add2(sum, p);
+                weighted = fma2(p, pack2(t0, t1), weighted);
+            }
+            Eight<T>::count(raw[u], own, exceed);
+        }
+        above += Eight<T>::total(exceed);
+    }
+    float s0, s1, w0, w1;
+    unpack2(sum, s0, s1);
+    unpack2(weighted, w0, w1);
+    const float d = shift_of(reference, top, c), f = ex2_approx(d);
+    return Sums{top, f * (s0 + s1), f * fmaf(d, s0 + s1, w0 + w1), above};
+}
+
+// ------------------------------------------------------------- the kernel
+
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(kThreadsPerRow, 4) logprob_kernel(const LogprobParams a) {
+    extern __shared__ uint32_t s_segment[];
+    __shared__ Selection s_select;
+    __shared__ uint64_t s_best[kTop ? kMaxRowCluster : 1][DRS_MAX_ALTERNATIVES];  // the cluster's CTAs' largest
+    __shared__ uint64_t s_cta[kMaxRowCluster][2];                                 // and their sums
+    __shared__ Sums s_warp[kRowWarps];
+    __shared__ float s_norm[2];
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int csize = a.cluster, k = a.k;
+    const int rank = csize > 1 ? static_cast<int>(cluster_rank()) : 0;
+    const int64_t r = blockIdx.x / csize;
+    const int64_t id = a.id_bits == 64 ? static_cast<const int64_t*>(a.ids)[r] : static_cast<const int32_t*>(a.ids)[r];
+    if (id < 0 || id >= a.vocab) {  // the same for the whole cluster
+        if (rank == 0) {
+            if (tid == 0) {
+                a.out_logprob[r] = 0.0f;
+                if (a.out_entropy) a.out_entropy[r] = 0.0f;
+                if (a.out_rank) a.out_rank[r] = 0;
+                if (a.out_norm) a.out_norm[2 * r] = a.out_norm[2 * r + 1] = 0.0f;
+            }
+            for (int i = tid; i < k; i += kThreadsPerRow) {
+                a.out_ids[r * k + i] = -1;
+                a.out_logprobs[r * k + i] = -INFINITY;
+            }
         }
         return;
     }
-    const T* const x = static_cast<const T*>(a.logits) + row * a.row_stride;
-    const float inverse = a.temps ? 1.0f / fmaxf(a.temps[row / a.canvas_len], kTempFloor) : 1.0f;
-    const float own = to_f(x[id]);
-    float top = -INFINITY;
-    int above = 0;
-    for (int j = threadIdx.x; j < a.vocab; j += kThreadsPerRow) {
-        const float v = to_f(x[j]);
-        top = fmaxf(top, v);
-        above += v > own;
-    }
-    top = block_reduce(top, s_float, [](float p, float q) { return fmaxf(p, q); });
-    above = block_reduce(above, s_int, [](int p, int q) { return p + q; });
-    const float base = top == -INFINITY ? 0.0f : top, scale = inverse * kLog2e;
-    float sum = 0.0f, weighted = 0.0f;
-    for (int j = threadIdx.x; j < a.vocab; j += kThreadsPerRow) {
-        const float t = max_nan((to_f(x[j]) - base) * scale, kLeastExponent);
-        const float e = ex2_approx(t);
-        sum += e;
-        weighted = fmaf(e, t, weighted);
-    }
-    const auto add = [](float p, float q) { return p + q; };
-    sum = block_reduce(sum, s_float, add);
-    weighted = block_reduce(weighted, s_float, add);
-    const float log_sum = top == -INFINITY && sum == 0.0f ? -INFINITY : logf(sum);
-    const auto logprob = [&](float v) { return (v - top) * inverse - log_sum; };
-    if (threadIdx.x == 0) {
-        a.out_logprob[row] = logprob(own);
-        if (a.out_entropy) a.out_entropy[row] = sum == 0.0f ? 0.0f : log_sum - weighted / sum * kLn2;
-        if (a.out_rank) a.out_rank[row] = 1 + above;
-        if (a.out_norm) a.out_norm[2 * row] = top, a.out_norm[2 * row + 1] = log_sum;
-    }
-    uint64_t last = ~0ull;
-    for (int i = 0; i < a.k; ++i) {
-        uint64_t best = 0;
-        for (int j = threadIdx.x; j < a.vocab; j += kThreadsPerRow) {
-            const uint64_t key = key_of(to_f(x[j]), j);
-            if (key < last && key > best) best = key;
+    if (csize > 1) cluster_arrive();
+    const T* const x = static_cast<const T*>(a.logits) + r * a.row_stride;
+    const Row<T> row(x, a.vocab);
+    const T own = x[id];
+    const float inverse = a.temps ? 1.0f / fmaxf(a.temps[r / a.canvas_len], kTempFloor) : 1.0f;
+    const float c = inverse * kLog2e;
+
+    const int first = rank * a.segments;
+    const int n = max(0, min(a.segments, (row.end + kSegment - 1) / kSegment - first));
+    Sums sums = row_sums<T, kTop>(row, first, n, c, own, s_segment);
+    sums.sum = warp_sum(sums.sum);
+    sums.weighted = warp_sum(sums.weighted);
+    sums.above = warp_sum(sums.above);
+    if (lane == 0) s_warp[warp] = sums;
+    __syncthreads();
+    if (kTop) select_top(row, s_segment, n, first, k, s_select);
+    if (csize > 1) {
+        cluster_wait();
+        if (warp == 0) {
+            sums = together(s_warp[lane % kRowWarps], lane < kRowWarps, c);
+            if (lane == 0) {
+                store_remote(&s_cta[rank][0], 0, pack2(sums.top, sums.sum));
+                store_remote(&s_cta[rank][1], 0, pack2(sums.weighted, __int_as_float(sums.above)));
+            }
         }
-        last = block_reduce(best, s_key, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
-        if (threadIdx.x == 0) {
-            a.out_ids[row * a.k + i] = column_of(last);
-            a.out_logprobs[row * a.k + i] = logprob(value_of(last));
+        if (kTop && tid < k) store_remote(&s_best[rank][tid], 0, s_select.best[tid]);
+        cluster_sync_all();
+        if (rank != 0) return;
+    }
+    if (warp == 0) {
+        if (csize > 1) {
+            const int from = lane % kMaxRowCluster;
+            unpack2(s_cta[from][0], sums.top, sums.sum);
+            float above;
+            unpack2(s_cta[from][1], sums.weighted, above);
+            sums.above = __float_as_int(above);
+            sums = together(sums, lane < csize, c);
+        } else {
+            sums = together(s_warp[lane % kRowWarps], lane < kRowWarps, c);
+        }
+        if (lane == 0) {
+            const float log_sum = sums.sum == 0.0f ? -INFINITY : logf(sums.sum);
+            a.out_logprob[r] = (to_f(own) - sums.top) * inverse - log_sum;
+            if (a.out_entropy) a.out_entropy[r] = sums.sum == 0.0f ? 0.0f : log_sum - sums.weighted / sums.sum * kLn2;
+            if (a.out_rank) a.out_rank[r] = 1 + sums.above;
+            if (a.out_norm) a.out_norm[2 * r] = sums.top, a.out_norm[2 * r + 1] = log_sum;
+            s_norm[0] = sums.top;
+            s_norm[1] = log_sum;
         }
     }
+    if (!kTop) return;
+    __syncthreads();
+    for (int i = tid; i < csize * k; i += kThreadsPerRow) {
+        const int list = i / k;
+        int above = i % k;
+        const uint64_t key = csize > 1 ? s_best[list][above] : s_select.best[above];
+        if (key == 0) continue;
+        for (int other = 0; other < csize; ++other) {
+            if (other == list) continue;
+            int low = 0, high = k;  // the keys of a list fall: how many exceed this one
+            while (low < high) {
+                const int mid = (low + high) / 2;
+                if (s_best[other][mid] > key) low = mid + 1;
+                else high = mid;
+            }
+            above += low;
+        }
+        if (above < k) {
+            a.out_ids[r * k + above] = place_of(key) - row.lead;
+            a.out_logprobs[r * k + above] = (value_of(static_cast<uint32_t>(key >> 32)) - s_norm[0]) * inverse - s_norm[1];
+        }
+    }
+}
+
+template <typename T> drs_status launch_logprobs(LogprobParams a, int64_t rows, cudaStream_t stream) {
+    const int sms = sm_count();
+    if (sms <= 0) return DRS_ERR_CUDA;
+    const int64_t segments = ceil_div(a.vocab + 16 / sizeof(T) - 1, kSegment);
+    const int64_t resident = int64_t{sms} * 4;
+    int cluster = 1;
+    while (cluster < kMaxRowCluster &&
+           (segments > int64_t{kMaxSegments} * cluster ||
+            (segments > 32 * cluster && rows * cluster * 2 <= resident - (cluster < 8 ? sms / 2 : sms * 3 / 2))))
+        cluster *= 2;
+    a.cluster = cluster;
+    a.segments = static_cast<int32_t>(ceil_div(segments, cluster));
+    const auto kernel = a.k > 0 ? logprob_kernel<T, true> : logprob_kernel<T, false>;
+    if (cluster > 8 && !prepare_kernel(reinterpret_cast<const void*>(kernel), 0, true)) return DRS_ERR_CUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
+    cfg.blockDim = dim3(kThreadsPerRow);
+    cfg.dynamicSmemBytes = a.segments * sizeof(uint32_t);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, a));
 }
 
 }  // namespace
@@ -166,12 +572,6 @@ extern "C" drs_status drs_token_logprobs(const void* logits, drs_dtype dtype, in
     a.canvas_len = canvas_len;
     a.vocab = static_cast<int32_t>(vocab);
     a.k = k;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return with_dtype(dtype, [&](auto t) -> drs_status {
-        using T = decltype(t);
-        const unsigned grid = static_cast<unsigned>(rows);
-        if (id_bits == 32) logprob_kernel<T, int32_t><<<grid, kThreadsPerRow, 0, st>>>(a);
-        else logprob_kernel<T, int64_t><<<grid, kThreadsPerRow, 0, st>>>(a);
-        return cuda_status(cudaGetLastError());
-    });
+    a.id_bits = id_bits;
+    return with_dtype(dtype, [&](auto t) { return launch_logprobs<decltype(t)>(a, rows, static_cast<cudaStream_t>(stream)); });
 }
