@@ -10,6 +10,8 @@ namespace drs {
 namespace {
 
 constexpr int kGradThreads = 256;
+constexpr int kUnits = 4;  // units of eight columns per thread
+constexpr int kCtaColumns = kGradThreads * kUnits * 8;
 constexpr float kLeastExponent = -200.0f;  // 2^-200 is 0 in fp32
 
 struct LogprobGradParams {
@@ -22,35 +24,139 @@ struct LogprobGradParams {
     const float* grad_entropy;
     void* grad;
     int64_t row_stride, grad_stride, canvas_len;
-    int32_t vocab;
+    int32_t vocab, id_bits, chunks;  // chunks: CTAs along a row
 };
 
-template <typename T, typename G, typename I>
+// What a row's columns have in common. With l = log2 p_j:
+//   dx_j = 2^l (a0 + a1 l), and g (1 - p) / T more in the token's column.
+struct RowTerms {
+    float top, scale, shift, a0, a1;
+    float inverse, log_sum, g, h, entropy;
+    int id;
+    bool none;  // passed over, or without a distribution: zeros
+
+    __device__ RowTerms(const LogprobGradParams& a, int64_t row) {
+        const int64_t token =
+            a.id_bits == 64 ? static_cast<const int64_t*>(a.ids)[row] : static_cast<const int32_t*>(a.ids)[row];
+        top = a.norm[2 * row];
+        log_sum = a.norm[2 * row + 1];
+        none = token < 0 || token >= a.vocab || top == -INFINITY;
+        id = none ? -1 : static_cast<int>(token);
+        inverse = a.temps ? 1.0f / fmaxf(a.temps[row / a.canvas_len], kTempFloor) : 1.0f;
+        g = a.grad_logprob ? a.grad_logprob[row] : 0.0f;
+        h = a.grad_entropy ? a.grad_entropy[row] : 0.0f;
+        entropy = a.grad_entropy ? a.entropy[row] : 0.0f;
+        scale = inverse * kLog2e;
+        shift = log_sum * kLog2e;
+        a0 = -(g + h * entropy) * inverse;
+        a1 = -h * kLn2 * inverse;
+    }
+
+    // The token's column: g (1 - p) without the difference's cancellation.
+    __device__ float own(float v) const {
+        const float lp = (v - top) * inverse - log_sum;
+        const float p = ex2_approx(fmaxf((v - top) * scale - shift, kLeastExponent));
+        return (h == 0.0f ? 0.0f : -h * p * (fmaxf(lp, kLeastExponent) + entropy) * inverse) - g * expm1f(lp) * inverse;
+    }
+
+    __device__ float one(float v, int col) const {
+        if (none) return 0.0f;
+        if (col == id) return own(v);
+        const float l = fmaxf((v - top) * scale - shift, kLeastExponent);
+        return ex2_approx(l) * fmaf(a1, l, a0);
+    }
+
+    // Columns col .. col+7.
+    __device__ __forceinline__ void eight(float (&v)[8], int col) const {
+        if (none) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+            return;
+        }
+        const bool here = static_cast<uint32_t>(id - col) < 8u;
+        float at = 0.0f;
+        if (here) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (col + e == id) at = own(v[e]);
+        }
+        const uint64_t top2 = pack2(top, top), scale2 = pack2(scale, scale), shift2 = pack2(shift, shift);
+        const uint64_t a02 = pack2(a0, a0), a12 = pack2(a1, a1);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            float l0, l1;
+            unpack2(sub2(mul2(sub2(pack2(v[e], v[e + 1]), top2), scale2), shift2), l0, l1);
+            l0 = fmaxf(l0, kLeastExponent);
+            l1 = fmaxf(l1, kLeastExponent);
+            unpack2(mul2(pack2(ex2_approx(l0), ex2_approx(l1)), fma2(a12, pack2(l0, l1), a02)), v[e], v[e + 1]);
+        }
+        if (here) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (col + e == id) v[e] = at;
+        }
+    }
+};
+
+// Rows of both arrays that start on 16-byte boundaries.
+template <typename T, typename G>
 __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const LogprobGradParams a) {
-    const int64_t row = blockIdx.x;
+    const int64_t row = blockIdx.x / a.chunks;
+    const int first = static_cast<int>(blockIdx.x % a.chunks) * kCtaColumns + threadIdx.x * 8;
     const T* const x = static_cast<const T*>(a.logits) + row * a.row_stride;
     G* const out = static_cast<G*>(a.grad) + row * a.grad_stride;
-    const int64_t id = static_cast<int64_t>(static_cast<const I*>(a.ids)[row]);
-    const float top = a.norm[2 * row], log_sum = a.norm[2 * row + 1];
-    if (id < 0 || id >= a.vocab || top == -INFINITY) {
-        for (int j = threadIdx.x; j < a.vocab; j += kGradThreads) out[j] = from_f<G>(0.0f);
-        return;
+    Raw8<T> raw[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        const int col = first + u * kGradThreads * 8;
+        if (col + 8 <= a.vocab) raw[u].load(x + col);
     }
-    const float inverse = a.temps ? 1.0f / fmaxf(a.temps[row / a.canvas_len], kTempFloor) : 1.0f;
-    const float g = a.grad_logprob ? a.grad_logprob[row] : 0.0f, h = a.grad_entropy ? a.grad_entropy[row] : 0.0f;
-    const float entropy = a.grad_entropy ? a.entropy[row] : 0.0f;
-    const float scale = inverse * kLog2e, shift = log_sum * kLog2e;
-    const float a0 = -(g + h * entropy) * inverse, a1 = -h * kLn2 * inverse;
-    for (int j = threadIdx.x; j < a.vocab; j += kGradThreads) {
-        const float v = to_f(x[j]);
-        const float l = fmaxf((v - top) * scale - shift, kLeastExponent);
-        float d = ex2_approx(l) * fmaf(a1, l, a0);
-        if (j == id) {  // g (1 - p) without the difference's cancellation
-            const float lp = (v - top) * inverse - log_sum;
-            d = (h == 0.0f ? 0.0f : -h * ex2_approx(l) * (fmaxf(lp, kLeastExponent) + entropy) * inverse) -
-                g * expm1f(lp) * inverse;
+    const RowTerms terms(a, row);
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        const int col = first + u * kGradThreads * 8;
+        if (col + 8 <= a.vocab) {
+            float v[8];
+            raw[u].unpack(v);
+            terms.eight(v, col);
+            store8_stream(out + col, v);
+        } else {
+            for (int j = col; j < a.vocab; ++j) out[j] = from_f<G>(terms.one(to_f(x[j]), j));
         }
-        out[j] = from_f<G>(d);
+    }
+}
+
+// Other rows: units of eight columns from a boundary of the gradient's row on,
+// the logits of each put together from the words that hold them, and the
+// columns before and after one by one.
+template <typename T, typename G>
+__global__ void __launch_bounds__(kGradThreads) logprob_grad_odd_kernel(const LogprobGradParams a) {
+    const int64_t row = blockIdx.x / a.chunks;
+    const int chunk = static_cast<int>(blockIdx.x % a.chunks);
+    const T* const x = static_cast<const T*>(a.logits) + row * a.row_stride;
+    G* const out = static_cast<G*>(a.grad) + row * a.grad_stride;
+    const int head = min(static_cast<int>((-reinterpret_cast<uintptr_t>(out) & 15) / sizeof(G)), a.vocab);
+    const int tail = head + (a.vocab - head) / 8 * 8;  // the first column behind the units
+    const int first = head + chunk * kCtaColumns + threadIdx.x * 8;
+    Any8<T> raw[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        const int col = first + u * kGradThreads * 8;
+        if (col < tail) raw[u].load(x, col, a.vocab);
+    }
+    const RowTerms terms(a, row);
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+        const int col = first + u * kGradThreads * 8;
+        if (col >= tail) break;
+        float v[8];
+        raw[u].unpack(v);
+        terms.eight(v, col);
+        store8_stream(out + col, v);
+    }
+    if (chunk == 0 && threadIdx.x < head + a.vocab - tail) {
+        const int j = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;
+        out[j] = from_f<G>(terms.one(to_f(x[j]), j));
     }
 }
 
@@ -89,14 +195,17 @@ extern "C" drs_status drs_token_logprobs_grad(const void* logits, drs_dtype dtyp
     a.grad_stride = grad_stride;
     a.canvas_len = canvas_len;
     a.vocab = static_cast<int32_t>(vocab);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    a.id_bits = id_bits;
+    a.chunks = static_cast<int32_t>(ceil_div(vocab, kCtaColumns));
+    if (rows > INT32_MAX / a.chunks) return DRS_ERR_UNSUPPORTED;
+    const bool vec = aligned(logits, 16) && aligned(grad, 16) && row_stride * dtype_bytes(dtype) % 16 == 0 &&
+                     grad_stride * dtype_bytes(grad_dtype) % 16 == 0;
     return with_dtype(dtype, [&](auto t) -> drs_status {
         return with_dtype(grad_dtype, [&](auto o) -> drs_status {
             using T = decltype(t);
             using G = decltype(o);
-            const unsigned grid = static_cast<unsigned>(rows);
-            if (id_bits == 32) logprob_grad_kernel<T, G, int32_t><<<grid, kGradThreads, 0, st>>>(a);
-            else logprob_grad_kernel<T, G, int64_t><<<grid, kGradThreads, 0, st>>>(a);
+            const auto kernel = vec ? logprob_grad_kernel<T, G> : logprob_grad_odd_kernel<T, G>;
+            kernel<<<static_cast<unsigned>(rows * a.chunks), kGradThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
             return cuda_status(cudaGetLastError());
         });
     });

@@ -1,6 +1,6 @@
 // token_common.cuh -- building blocks of the token operators (verify.cu,
-// slots.cu, embed.cu, embed_grad.cu): element types, vector accesses and
-// block-wide scans.
+// slots.cu, embed.cu, embed_grad.cu, logprobs.cu, logprobs_grad.cu,
+// dropout.cu): element types, vector accesses and block-wide scans.
 #pragma once
 
 #include <cstdint>
@@ -104,6 +104,56 @@ template <typename T> struct Raw8Shifted {
     }
 };
 
+// Eight consecutive elements of a row, wherever they start: the aligned words
+// that hold them where these lie inside the row, else one by one. Elements from
+// `width` on are 0.
+template <typename T> struct Any8 {
+    Raw8Shifted<T> raw;
+    int shift;
+    __device__ __forceinline__ void load(const T* row, int col, int width) {
+        constexpr int kVec = 16 / sizeof(T);
+        shift = static_cast<int>(reinterpret_cast<uintptr_t>(row + col) & 15);
+        const int off = shift / static_cast<int>(sizeof(T));
+        if (col >= off && col - off + (off ? kVec : 0) + 8 <= width) {
+            raw.load(row + (col - off), shift);
+        } else {
+            shift = 0;
+            T* const e = reinterpret_cast<T*>(raw.w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = from_f<T>(0.0f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + i < width) e[i] = row[col + i];
+        }
+    }
+    __device__ __forceinline__ void unpack(float (&v)[8]) const {
+        if (shift) {
+            raw.unpack(shift, v);
+        } else {
+            Raw8<T> r;
+#pragma unroll
+            for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.w[i] = raw.w[i];
+            r.unpack(v);
+        }
+    }
+};
+
+// Eight consecutive elements, rounded to their type and written once, from a
+// 16-byte boundary on.
+template <typename T> __device__ __forceinline__ void store8_stream(T* p, const float (&v)[8]) {
+    uint4* const q = reinterpret_cast<uint4*>(p);
+    if constexpr (sizeof(T) == 4) {
+        __stcs(q, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
+        __stcs(q + 1, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
+    } else {
+        uint4 w;
+        T* const e = reinterpret_cast<T*>(&w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = from_f<T>(v[i]);
+        __stcs(q, w);
+    }
+}
+
 // ------------------------------------------------------------- scans
 
 template <typename T> __device__ __forceinline__ T warp_scan_inclusive(T v, int lane) {
@@ -180,6 +230,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 
