@@ -28,7 +28,6 @@ constexpr int kRowWarps = kThreadsPerRow / 32;
 constexpr int kMaxRowCluster = 16;
 constexpr int kSegment = 256;   // columns a warp takes at once: 8 per lane
 constexpr int kTile = 4;        // segments whose loads a warp has in flight
-constexpr int kMaxSegments = 2048;  // per CTA
 constexpr int kListed = 512;    // candidates of the short way
 // Exponents (base 2) below this give 0; held there so that 0 times an
 // infinite exponent does not arise in W.
@@ -46,10 +45,18 @@ struct LogprobParams {
     int32_t* out_ids;
     float* out_logprobs;
     int64_t row_stride, canvas_len;
-    int32_t vocab, k, id_bits, cluster, segments;  // segments: of a CTA
+    int32_t vocab, k, id_bits, cluster, part;  // part: segments of a CTA
 };
 
 // ------------------------------------------------------------- elements
+
+// 2^x, results below the normal range 0: one instruction (ex2_approx takes
+// four), in sums of terms relative to their largest.
+__device__ __forceinline__ float ex2_flushed(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
@@ -145,19 +152,21 @@ __device__ __forceinline__ int place_of(uint64_t key) { return static_cast<int>(
 // ------------------------------------------------------------- selection
 
 struct Selection {
-    uint64_t list[kListed];              // candidates: keys of segments, then of elements
+    __align__(16) uint64_t list[kListed];      // candidates: keys of segments, then of elements
     uint32_t unit[DRS_MAX_ALTERNATIVES * 32];  // orders of units' largest, then of elements
     int chosen[2][DRS_MAX_ALTERNATIVES];
-    uint64_t best[DRS_MAX_ALTERNATIVES];  // the CTA's k largest, in order
     int counts[32];
     int n, m;
 };
 
-// How many of the n keys exceed this one.
+// How many of the n keys exceed this one. The list goes on with three zeros.
 __device__ __forceinline__ int keys_above(const uint64_t* list, int n, uint64_t key) {
     int above = 0;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) above += list[i] > key;
+#pragma unroll 2
+    for (int i = 0; i < n; i += 4) {
+        const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(list + i), q = *reinterpret_cast<const ulonglong2*>(list + i + 2);
+        above += (p.x > key) + (p.y > key) + (q.x > key) + (q.y > key);
+    }
     return above;
 }
 
@@ -231,16 +240,11 @@ __device__ int select_exact(const uint32_t* value, int n, int k, int* chosen, Se
     return k;
 }
 
-// The CTA's k largest logits into s.best, in order, then 0 (where it has fewer
-// columns). segment: the orders of its n segments' largest, first: its
-// first segment.
-template <typename T> __device__ void select_top(const Row<T>& row, const uint32_t* segment, int n, int first, int k,
-                                                 Selection& s) {
+// The row's k largest logits into s.list, in no order: their number, at least k (keys of 0
+// among them are places outside the row). segment: the orders of its n
+// segments' largest.
+template <typename T> __device__ int select_top(const Row<T>& row, const uint32_t* segment, int n, int k, Selection& s) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0) s.n = s.m = 0;
-    if (tid < k) s.best[tid] = 0;
-    __syncthreads();
-    int found = -1;
     if (n > k) {
         // The short way: segments that reach a bound, k of them, and what in
         // these reaches the k-th one's largest.
@@ -253,7 +257,9 @@ template <typename T> __device__ void select_top(const Row<T>& row, const uint32
         }
         __syncthreads();
         const int listed = s.n;
-        if (listed <= kListed) {
+        if (listed <= kListed - 4) {
+            if (tid < 3) s.list[listed + tid] = 0;
+            __syncthreads();
             for (int i = tid; i < listed; i += kThreadsPerRow) {
                 const uint64_t key = s.list[i];
                 const int above = keys_above(s.list, listed, key);
@@ -261,57 +267,68 @@ template <typename T> __device__ void select_top(const Row<T>& row, const uint32
             }
             __syncthreads();
             const uint32_t least = segment[s.chosen[0][k - 1]];
-            for (int c = warp; c < k; c += kRowWarps) {
-                const int place = (first + s.chosen[0][c]) * kSegment + lane * 8;
-                float v[8];
-                row.unit(place).unpack(v);
+            constexpr int kAtOnce = 4;
+            for (int c = warp; c < k; c += kRowWarps * kAtOnce) {
+                Raw8<T> raw[kAtOnce];
+                int place[kAtOnce];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t order = order_of(v[e]);
-                    if (order >= least && place + e >= row.lead && place + e < row.end) {
-                        const int at = atomicAdd(&s.m, 1);
-                        if (at < kListed) s.list[at] = key_of(order, place + e);
+                for (int u = 0; u < kAtOnce; ++u) {
+                    const int at = c + u * kRowWarps;
+                    place[u] = at < k ? s.chosen[0][at] * kSegment + lane * 8 : row.end;  // the row's end: none
+                    raw[u] = row.unit(place[u]);
+                }
+#pragma unroll
+                for (int u = 0; u < kAtOnce; ++u) {
+                    float v[8];
+                    raw[u].unpack(v);
+                    uint32_t reach = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const bool inside = place[u] + e >= row.lead && place[u] + e < row.end;
+                        reach |= (inside && order_of(v[e]) >= least ? 1u : 0u) << e;
+                    }
+                    if (reach) {
+                        int at = atomicAdd(&s.m, __popc(reach));
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (reach >> e & 1) {
+                                if (at < kListed) s.list[at] = key_of(order_of(v[e]), place[u] + e);
+                                ++at;
+                            }
                     }
                 }
             }
             __syncthreads();
-            if (s.m <= kListed) found = s.m;
+            if (s.m <= kListed - 4) return s.m;
         }
     }
-    if (found < 0) {
-        // The long way, for rows with many equal logits, risen or short ones: the k segments, then their k units of
-        // eight, then their k elements.
-        const int segments = select_exact(segment, n, k, s.chosen[0], s);
-        for (int c = warp; c < segments; c += kRowWarps) {
-            float v[8];
-            const int place = (first + s.chosen[0][c]) * kSegment + lane * 8;
-            row.unit(place).unpack(v);
-            uint32_t most = 0;
+    // The long way, for rows with many equal logits and for short ones: the k
+    // segments, then their k units of eight, then their k elements.
+    const int segments = select_exact(segment, n, k, s.chosen[0], s);
+    for (int c = warp; c < segments; c += kRowWarps) {
+        float v[8];
+        const int place = s.chosen[0][c] * kSegment + lane * 8;
+        row.unit(place).unpack(v);
+        uint32_t most = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (place + e >= row.lead && place + e < row.end) most = max(most, order_of(v[e]));
-            s.unit[c * 32 + lane] = most;
-        }
-        const int units = select_exact(s.unit, segments * 32, k, s.chosen[1], s);
-        if (tid < units) s.chosen[1][tid] = (first + s.chosen[0][s.chosen[1][tid] >> 5]) * 32 + (s.chosen[1][tid] & 31);
-        __syncthreads();
-        for (int i = tid; i < units * 8; i += kThreadsPerRow) {
-            const int place = s.chosen[1][i >> 3] * 8 + (i & 7);
-            s.unit[i] = place >= row.lead && place < row.end ? order_of(to_f(row.first[place])) : 0;
-        }
-        found = select_exact(s.unit, units * 8, k, s.chosen[0], s);
-        if (tid < found) {
-            const int i = s.chosen[0][tid];
-            s.list[tid] = s.unit[i] ? key_of(s.unit[i], s.chosen[1][i >> 3] * 8 + (i & 7)) : 0;
-        }
-        __syncthreads();
+        for (int e = 0; e < 8; ++e)
+            if (place + e >= row.lead && place + e < row.end) most = max(most, order_of(v[e]));
+        s.unit[c * 32 + lane] = most;
     }
-    for (int i = tid; i < found; i += kThreadsPerRow) {
-        const uint64_t key = s.list[i];
-        const int above = keys_above(s.list, found, key);
-        if (above < k && key) s.best[above] = key;
+    const int units = select_exact(s.unit, segments * 32, k, s.chosen[1], s);
+    if (tid < units) s.chosen[1][tid] = s.chosen[0][s.chosen[1][tid] >> 5] * 32 + (s.chosen[1][tid] & 31);
+    __syncthreads();
+    for (int i = tid; i < units * 8; i += kThreadsPerRow) {
+        const int place = s.chosen[1][i >> 3] * 8 + (i & 7);
+        s.unit[i] = place >= row.lead && place < row.end ? order_of(to_f(row.first[place])) : 0;
+    }
+    const int found = select_exact(s.unit, units * 8, k, s.chosen[0], s);
+    if (tid < found) {
+        const int i = s.chosen[0][tid];
+        s.list[tid] = s.unit[i] ? key_of(s.unit[i], s.chosen[1][i >> 3] * 8 + (i & 7)) : 0;
     }
     __syncthreads();
+    return found;
 }
 
 // ------------------------------------------------------------- sums
@@ -335,73 +352,92 @@ __device__ __forceinline__ Sums together(Sums s, bool have, float c) {
     return Sums{top, warp_sum(s.sum * f), warp_sum(f * fmaf(d, s.sum, s.weighted)), warp_sum(s.above)};
 }
 
-// The sums of this thread's part of the CTA's segments; top and reference are the
-// warp's. kTop: the segments' largest go to `segment`.
-template <typename T, bool kTop>
-__device__ __forceinline__ Sums row_sums(const Row<T>& row, int first, int n, float c, T own, uint32_t* segment) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const float slack = kSlack / c;
-    float top = -INFINITY, reference = -INFINITY;
+// The sums of a thread's part of a row; top and reference are the warp's.
+struct RunningSums {
+    float top = -INFINITY, reference = -INFINITY, bound = -INFINITY;  // bound: where the reference moves
+    float base = 0.0f;                                                // the reference, 0 before there is one
     uint64_t sum = 0, weighted = 0;
-    const uint64_t c2 = pack2(c, c);
-    int above = 0;
-    for (int i = warp * kTile; i < n; i += kRowWarps * kTile) {
-        Raw8<T> raw[kTile];
-        const int place = (first + i) * kSegment + lane * 8;
-        if (i + kTile <= n && row.whole((first + i) * kSegment, kTile * kSegment)) {
+
+    // The reference moves to the largest so far.
+    __device__ __forceinline__ void move(float c) {
+        const float d = shift_of(reference, top, c), f = ex2_approx(d);
+        const uint64_t f2 = pack2(f, f);
+        weighted = mul2(f2, fma2(pack2(d, d), sum, weighted));
+        sum = mul2(f2, sum);
+        reference = base = top;
+        bound = top + kSlack / c;
+    }
+
+    // Eight columns per lane; most: the warp's largest.
+    template <typename T> __device__ __forceinline__ void add(const Raw8<T>& raw, float most, float c) {
+        top = fmaxf(top, most);
+        if (most > bound) move(c);
+        const uint64_t base2 = pack2(base, base), c2 = pack2(c, c);
+        float v[8];
+        raw.unpack(v);
 #pragma unroll
-            for (int u = 0; u < kTile; ++u) raw[u].load(row.first + place + u * kSegment);
-        } else {
-#pragma unroll
-            for (int u = 0; u < kTile; ++u) raw[u] = row.unit(place + u * kSegment);
+        for (int e = 0; e < 8; e += 2) {
+            float t0, t1;
+            unpack2(mul2(sub2(pack2(v[e], v[e + 1]), base2), c2), t0, t1);
+            t0 = max_nan(t0, kLeastExponent);
+            t1 = max_nan(t1, kLeastExponent);
+            const uint64_t p = pack2(ex2_flushed(t0), ex2_flushed(t1));
+            sum = add2(sum, p);
+            weighted = fma2(p, pack2(t0, t1), weighted);
         }
+    }
+
+    __device__ __forceinline__ Sums value(float c, int above) const {
+        float s0, s1, w0, w1;
+        unpack2(sum, s0, s1);
+        unpack2(weighted, w0, w1);
+        const float d = shift_of(reference, top, c), f = ex2_approx(d);
+        return Sums{top, f * (s0 + s1), f * fmaf(d, s0 + s1, w0 + w1), above};
+    }
+};
+
+// The sums of the row's segments [first, end). kTop: their largest go to `segment`.
+template <typename T, bool kTop>
+__device__ __forceinline__ Sums row_sums(const Row<T>& row, int first, int end, float c, T own, float* segment) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    RunningSums sums;
+    int above = 0;
+    for (int i = first + warp * kTile; i < end; i += kRowWarps * kTile) {
         typename Eight<T>::Count exceed = Eight<T>::zero();
+        if (i + kTile <= end && row.whole(i * kSegment, kTile * kSegment)) {
+            Raw8<T> raw[kTile];
+            const T* const from = row.first + i * kSegment + lane * 8;
 #pragma unroll
-        for (int u = 0; u < kTile; ++u) {
-            if (i + u >= n) break;
-            const float most = warp_max(Eight<T>::largest(raw[u]));
-            if (kTop && lane == 0) segment[i + u] = order_of(most);
-            top = fmaxf(top, most);
-            if (most > reference + slack || reference == -INFINITY) {
-                const float d = shift_of(reference, top, c), f = ex2_approx(d);
-                const uint64_t f2 = pack2(f, f);
-                weighted = mul2(f2, fma2(pack2(d, d), sum, weighted));
-                sum = mul2(f2, sum);
-                reference = top;
-            }
-            const float base = reference == -INFINITY ? 0.0f : reference;
-            const uint64_t base2 = pack2(base, base);
-            float v[8];
-            raw[u].unpack(v);
+            for (int u = 0; u < kTile; ++u) raw[u].load(from + u * kSegment);
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                float t0, t1;
-                unpack2(mul2(sub2(pack2(v[e], v[e + 1]), base2), c2), t0, t1);
-                t0 = max_nan(t0, kLeastExponent);
-                t1 = max_nan(t1, kLeastExponent);
-                const uint64_t p = pack2(ex2_approx(t0), ex2_approx(t1));
-                sum = add2(sum, p);
-                weighted = fma2(p, pack2(t0, t1), weighted);
+            for (int u = 0; u < kTile; ++u) {
+                const float most = warp_max(Eight<T>::largest(raw[u]));
+                if (kTop && lane == 0) segment[i + u] = most;
+                sums.add(raw[u], most, c);
+                Eight<T>::count(raw[u], own, exceed);
             }
-            Eight<T>::count(raw[u], own, exceed);
+        } else {
+#pragma unroll 1
+            for (int u = i; u < min(i + kTile, end); ++u) {
+                const Raw8<T> raw = row.unit(u * kSegment + lane * 8);
+                const float most = warp_max(Eight<T>::largest(raw));
+                if (kTop && lane == 0) segment[u] = most;
+                sums.add(raw, most, c);
+                Eight<T>::count(raw, own, exceed);
+            }
         }
         above += Eight<T>::total(exceed);
     }
-    float s0, s1, w0, w1;
-    unpack2(sum, s0, s1);
-    unpack2(weighted, w0, w1);
-    const float d = shift_of(reference, top, c), f = ex2_approx(d);
-    return Sums{top, f * (s0 + s1), f * fmaf(d, s0 + s1, w0 + w1), above};
+    return sums.value(c, above);
 }
 
 // ------------------------------------------------------------- the kernel
 
 template <typename T, bool kTop>
 __global__ void __launch_bounds__(kThreadsPerRow, 4) logprob_kernel(const LogprobParams a) {
-    extern __shared__ uint32_t s_segment[];
+    extern __shared__ uint32_t s_segment[];  // the row's segments' largest: values, then their orders
     __shared__ Selection s_select;
-    __shared__ uint64_t s_best[kTop ? kMaxRowCluster : 1][DRS_MAX_ALTERNATIVES];  // the cluster's CTAs' largest
-    __shared__ uint64_t s_cta[kMaxRowCluster][2];                                 // and their sums
+    __shared__ uint64_t s_cta[kMaxRowCluster][2];  // the cluster's CTAs' sums
     __shared__ Sums s_warp[kRowWarps];
     __shared__ float s_norm[2];
 
@@ -432,17 +468,24 @@ __global__ void __launch_bounds__(kThreadsPerRow, 4) logprob_kernel(const Logpro
     const float inverse = a.temps ? 1.0f / fmaxf(a.temps[r / a.canvas_len], kTempFloor) : 1.0f;
     const float c = inverse * kLog2e;
 
-    const int first = rank * a.segments;
-    const int n = max(0, min(a.segments, (row.end + kSegment - 1) / kSegment - first));
-    Sums sums = row_sums<T, kTop>(row, first, n, c, own, s_segment);
+    const int segments = (row.end + kSegment - 1) / kSegment;
+    const int first = min(rank * a.part, segments), end = min(first + a.part, segments);
+    Sums sums = row_sums<T, kTop>(row, first, end, c, own, reinterpret_cast<float*>(s_segment));
     sums.sum = warp_sum(sums.sum);
     sums.weighted = warp_sum(sums.weighted);
     sums.above = warp_sum(sums.above);
     if (lane == 0) s_warp[warp] = sums;
+    if (kTop && tid == 0) s_select.n = s_select.m = 0;
     __syncthreads();
-    if (kTop) select_top(row, s_segment, n, first, k, s_select);
-    if (csize > 1) {
+    if (kTop && rank == 0)
+        for (int i = first + tid; i < end; i += kThreadsPerRow) s_segment[i] = order_of(__uint_as_float(s_segment[i]));
+    if (csize > 1) {  // the first CTA takes it from here
         cluster_wait();
+        if (rank != 0) {
+            if (kTop)
+                for (int i = first + tid; i < end; i += kThreadsPerRow)
+                    store_remote32(&s_segment[i], 0, order_of(__uint_as_float(s_segment[i])));
+        }
         if (warp == 0) {
             sums = together(s_warp[lane % kRowWarps], lane < kRowWarps, c);
             if (lane == 0) {
@@ -450,9 +493,10 @@ __global__ void __launch_bounds__(kThreadsPerRow, 4) logprob_kernel(const Logpro
                 store_remote(&s_cta[rank][1], 0, pack2(sums.weighted, __int_as_float(sums.above)));
             }
         }
-        if (kTop && tid < k) store_remote(&s_best[rank][tid], 0, s_select.best[tid]);
         cluster_sync_all();
         if (rank != 0) return;
+    } else if (kTop) {
+        __syncthreads();
     }
     if (warp == 0) {
         if (csize > 1) {
@@ -476,23 +520,13 @@ __global__ void __launch_bounds__(kThreadsPerRow, 4) logprob_kernel(const Logpro
         }
     }
     if (!kTop) return;
+    const int found = select_top(row, s_segment, segments, k, s_select);  // a barrier comes before s_norm's use
+    if (tid < 3) s_select.list[found + tid] = 0;
     __syncthreads();
-    for (int i = tid; i < csize * k; i += kThreadsPerRow) {
-        const int list = i / k;
-        int above = i % k;
-        const uint64_t key = csize > 1 ? s_best[list][above] : s_select.best[above];
-        if (key == 0) continue;
-        for (int other = 0; other < csize; ++other) {
-            if (other == list) continue;
-            int low = 0, high = k;  // the keys of a list fall: how many exceed this one
-            while (low < high) {
-                const int mid = (low + high) / 2;
-                if (s_best[other][mid] > key) low = mid + 1;
-                else high = mid;
-            }
-            above += low;
-        }
-        if (above < k) {
+    for (int i = tid; i < found; i += kThreadsPerRow) {
+        const uint64_t key = s_select.list[i];
+        const int above = keys_above(s_select.list, found, key);
+        if (above < k && key) {
             a.out_ids[r * k + above] = place_of(key) - row.lead;
             a.out_logprobs[r * k + above] = (value_of(static_cast<uint32_t>(key >> 32)) - s_norm[0]) * inverse - s_norm[1];
         }
@@ -506,17 +540,16 @@ template <typename T> drs_status launch_logprobs(LogprobParams a, int64_t rows, 
     const int64_t resident = int64_t{sms} * 4;
     int cluster = 1;
     while (cluster < kMaxRowCluster &&
-           (segments > int64_t{kMaxSegments} * cluster ||
-            (segments > 32 * cluster && rows * cluster * 2 <= resident - (cluster < 8 ? sms / 2 : sms * 3 / 2))))
+           segments > 32 * cluster && rows * cluster * 2 <= resident - (cluster < 8 ? sms / 2 : sms * 3 / 2))
         cluster *= 2;
     a.cluster = cluster;
-    a.segments = static_cast<int32_t>(ceil_div(segments, cluster));
+    a.part = static_cast<int32_t>(ceil_div(segments, cluster));
     const auto kernel = a.k > 0 ? logprob_kernel<T, true> : logprob_kernel<T, false>;
     if (cluster > 8 && !prepare_kernel(reinterpret_cast<const void*>(kernel), 0, true)) return DRS_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
     cfg.blockDim = dim3(kThreadsPerRow);
-    cfg.dynamicSmemBytes = a.segments * sizeof(uint32_t);
+    cfg.dynamicSmemBytes = a.k > 0 ? segments * sizeof(uint32_t) : 0;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -312,6 +312,12 @@ __device__ __forceinline__ void store_remote(void* local, uint32_t rank, uint64_
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
+__device__ __forceinline__ void store_remote32(void* local, uint32_t rank, uint32_t v) {
+    uint32_t addr;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(local)), "r"(rank));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 // ------------------------------------------------------------- host side
 
 inline bool dtype_ok(drs_dtype t) { return t == DRS_DTYPE_FP32 || t == DRS_DTYPE_BF16 || t == DRS_DTYPE_FP16; }
