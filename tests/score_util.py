@@ -4,9 +4,10 @@ Roundings counted (U = 2^-24, half a step of fp32, relative):
   d = (x - m) / T: the difference, 1 / T, its product with log2 e, that constant and the product with the
       difference: at most 6 U |d|.
   e^d: 2^t to 2^-22 (the bound of ex2.approx), and the error of d.
-  S = sum e^d: every term's relative error, and one rounding per addition on the way of a term into the sum. A thread
-      adds up at most vocab / 256 terms one after the other (a row has 256 threads or more), then the
-      threads' sums meet in at most 32 steps: additions() of them.
+  S = sum e^d: every term's relative error, and one rounding per addition on the way of a term into the sum. A warp
+      takes 256 columns or more at once, whose terms (8 or 16 per lane) are added up first, then the lane's sum of
+      them to its sum of the row, at most vocab / 256 times; the lanes' and warps' sums meet in fewer than 20 steps:
+      additions() of them in all.
   With D = the mean of |d| under the softmax (= entropy - ln S): S is off by rel = 6 U D + 2^-22 + additions U.
   ln S: rel, and one step of its own value; the logprob d - ln S: the errors of both and a rounding.
   entropy = ln S + D: rel (1 + D), the errors of the weights e^d |d| (with D2, the mean of d^2: 6 U D2 + D (2^-22 +

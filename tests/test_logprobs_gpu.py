@@ -54,12 +54,14 @@ def test_temperatures(canvas_len):
 
 
 def test_temperatures_at_and_below_zero():
-    """Clamped at 1e-10: the distribution of the largest logit alone."""
+    """Clamped at 1e-10: the distribution of the largest logit alone, exactly. At 1e-3 the exponents are x c - (m c
+    rounded), 2^-24 of their size off at x = m; e^d is 2^t to 2^-22, so that ln S is within the tolerances but not
+    exactly 0."""
     temps = torch.tensor([0.0, -1.0, 1e-12, 1e-10, 1e-3], device="cuda")
     logits, ids = logits_of("peaks", 5, 3001, torch.float32, 1), torch.tensor([0, 1, 2, 3, 4], device="cuda")
     out = drs().token_logprobs(logits, ids, 4, temps)
     check_logprobs(out, logits, ids, 4, temps)
-    assert (out[1] == 0).all() and (out[5][:, 0] == 0).all()
+    assert (out[1][:4] == 0).all() and (out[5][:4, 0] == 0).all()
 
 
 def test_nan_and_infinite_logits():

@@ -10,29 +10,35 @@
 // passes it by more than 2^8 in the exponent; S and W then move along:
 // S' = 2^d S, W' = 2^d (W + d S) with d = (M - M') c.
 //
-// One read of the row. A CTA (or a cluster of them) takes a row, its warps segments of
-// 256 columns, and keep each segment's largest logit in shared memory. The k
-// largest logits lie in the k segments whose largest logits come first (by
-// value, then by column): any logit of another segment has k before it, one in
-// each of these. So only k segments are looked at again, from L2, and of
-// these only what reaches the k-th segment's largest.
+// One read of the row. Warps take segments of 256 or 512 columns and keep each
+// segment's largest logit in shared memory. The k largest logits lie in the k
+// segments whose largest logits come first (by value, then by column): any
+// logit of another segment has k before it, one in each of these. So only k
+// segments are looked at again, from L2, and of these only what reaches the
+// k-th segment's largest.
 #include <climits>
+#include <cstdlib>
 
 #include "token_common.cuh"
 
 namespace drs {
 namespace {
 
-constexpr int kThreadsPerRow = 256;
-constexpr int kRowWarps = kThreadsPerRow / 32;
+constexpr int kResident = 32;  // warps per SM
 constexpr int kMaxRowCluster = 16;
-constexpr int kSegment = 256;   // columns a warp takes at once: 8 per lane
-constexpr int kTile = 4;        // segments whose loads a warp has in flight
-constexpr int kListed = 512;    // candidates of the short way
+constexpr int kListed = 256;  // candidates of the short way
+constexpr int kSegment = 256;         // columns whose largest is kept: eight per lane of a warp
+constexpr int kBlockBytes = 1024;     // what a warp takes at once: two 16-byte words per lane
+constexpr int kDepth = 4;             // blocks on their way to a warp
+constexpr int kStageBytes = 2048;     // what a warp looks at again at once
 // Exponents (base 2) below this give 0; held there so that 0 times an
 // infinite exponent does not arise in W.
 constexpr float kLeastExponent = -200.0f;
 constexpr float kSlack = 8.0f;  // exponents above the reference before it moves
+
+// Segments in a block, and its columns.
+template <typename T> constexpr int kParts = sizeof(T) == 2 ? 2 : 1;
+template <typename T> constexpr int kBlock = kSegment * kParts<T>;
 
 struct LogprobParams {
     const void* logits;
@@ -44,8 +50,9 @@ struct LogprobParams {
     float* out_norm;
     int32_t* out_ids;
     float* out_logprobs;
-    int64_t row_stride, canvas_len;
-    int32_t vocab, k, id_bits, cluster, part;  // part: segments of a CTA
+    int64_t rows, row_stride, canvas_len;
+    int32_t vocab, k, id_bits;
+    int32_t blocks, cluster, part;  // blocks: of a row, at most; part: of them a CTA's
 };
 
 // ------------------------------------------------------------- elements
@@ -103,6 +110,42 @@ template <typename T, typename T2> struct EightHalves {
 template <> struct Eight<__nv_bfloat16> : EightHalves<__nv_bfloat16, __nv_bfloat162> {};
 template <> struct Eight<__half> : EightHalves<__half, __half2> {};
 
+template <typename T> __device__ T rounded_down(float v);
+template <> __device__ __forceinline__ __nv_bfloat16 rounded_down<__nv_bfloat16>(float v) { return __float2bfloat16_rd(v); }
+template <> __device__ __forceinline__ __half rounded_down<__half>(float v) { return __float2half_rd(v); }
+template <typename T> __device__ constexpr float largest_finite();
+template <> __device__ constexpr float largest_finite<__nv_bfloat16>() { return 0x1.FEp127f; }
+template <> __device__ constexpr float largest_finite<__half>() { return 65504.0f; }
+
+// The least logit that is told from smaller ones: it holds exponents at about
+// kLeastExponent or below, finite. 16-bit elements are raised to it in pairs, before
+// they are taken apart, fp32 exponents one by one.
+template <typename T> struct Floor {
+    __device__ bool set(float) { return true; }
+    __device__ __forceinline__ const Raw8<T>& raise(const Raw8<T>& r) const { return r; }
+    __device__ static __forceinline__ float raise(float t) { return max_nan(t, kLeastExponent); }
+};
+template <typename T, typename T2> struct FloorHalves {
+    T2 least;
+    // false: below the type's range
+    __device__ __forceinline__ bool set(float v) {
+        least.x = least.y = rounded_down<T>(v);
+        return v >= -largest_finite<T>();
+    }
+    __device__ __forceinline__ Raw8<T> raise(const Raw8<T>& r) const {
+        Raw8<T> q;
+        q.w[0] = make_uint4(one(r.w[0].x), one(r.w[0].y), one(r.w[0].z), one(r.w[0].w));
+        return q;
+    }
+    __device__ __forceinline__ uint32_t one(uint32_t w) const {
+        const T2 v = __hmax2_nan(*reinterpret_cast<const T2*>(&w), least);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    __device__ static __forceinline__ float raise(float t) { return t; }
+};
+template <> struct Floor<__nv_bfloat16> : FloorHalves<__nv_bfloat16, __nv_bfloat162> {};
+template <> struct Floor<__half> : FloorHalves<__half, __half2> {};
+
 // A row as a line of aligned units of eight elements: column j stands at
 // place j + lead, so that units start on 16-byte boundaries; places outside the
 // row count as -inf and are not read.
@@ -116,16 +159,25 @@ template <typename T> struct Row {
         end = vocab + lead;
     }
     __device__ __forceinline__ bool whole(int place, int n) const { return place >= lead && place + n <= end; }
+    __device__ __forceinline__ int blocks() const { return (end + kBlock<T> - 1) / kBlock<T>; }
+    // Those wholly inside the row.
+    __device__ __forceinline__ int whole_first() const { return lead > 0 ? 1 : 0; }
+    __device__ __forceinline__ int whole_end() const { return end / kBlock<T>; }
+    // The 16-byte word at a place.
+    __device__ __forceinline__ uint4 word(int place) const {
+        constexpr int kVec = 16 / sizeof(T);
+        if (whole(place, kVec)) return load16_stream(first + place);
+        uint4 w;
+        T* const e = reinterpret_cast<T*>(&w);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) e[i] = place + i >= lead && place + i < end ? first[place + i] : from_f<T>(-INFINITY);
+        return w;
+    }
+    // Eight columns from a place on.
     __device__ __forceinline__ Raw8<T> unit(int place) const {
         Raw8<T> r;
-        if (whole(place, 8)) {
-            r.load(first + place);
-        } else {
-            T* const e = reinterpret_cast<T*>(&r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                e[i] = place + i >= lead && place + i < end ? first[place + i] : from_f<T>(-INFINITY);
-        }
+        for (int h = 0; h < static_cast<int>(sizeof(T) / 2); ++h) r.w[h] = word(place + 4 * h);
         return r;
     }
 };
@@ -149,186 +201,374 @@ __device__ __forceinline__ uint64_t key_of(uint32_t order, int place) {
 
 __device__ __forceinline__ int place_of(uint64_t key) { return static_cast<int>(~static_cast<uint32_t>(key)); }
 
-// ------------------------------------------------------------- selection
+// ------------------------------------------------------------- asynchronous copies
 
-struct Selection {
-    __align__(16) uint64_t list[kListed];      // candidates: keys of segments, then of elements
-    uint32_t unit[DRS_MAX_ALTERNATIVES * 32];  // orders of units' largest, then of elements
-    int chosen[2][DRS_MAX_ALTERNATIVES];
-    int counts[32];
-    int n, m;
-};
-
-// How many of the n keys exceed this one. The list goes on with three zeros.
-__device__ __forceinline__ int keys_above(const uint64_t* list, int n, uint64_t key) {
-    int above = 0;
-#pragma unroll 2
-    for (int i = 0; i < n; i += 4) {
-        const ulonglong2 p = *reinterpret_cast<const ulonglong2*>(list + i), q = *reinterpret_cast<const ulonglong2*>(list + i + 2);
-        above += (p.x > key) + (p.y > key) + (q.x > key) + (q.y > key);
-    }
-    return above;
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int n> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
+__device__ __forceinline__ uint4 load_shared16(uint32_t from) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_shared16(uint32_t to, uint4 v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// A value that at least k of the n > k values reach, by every warp for itself: the
-// k-th largest of the largest of 32 (k <= 32) or 64 groups of them.
-__device__ __forceinline__ uint32_t reached_by(const uint32_t* value, int n, int k, int lane) {
-    uint32_t a = 0, b = 0;  // below every order
+// The whole blocks of rows on their way to a warp: those first, first + step, ... of a row, and, when all of
+// them are on their way, those of the next row. Each turn takes one block and fetches the one kDepth
+// further into its slot; a lane reads what it has copied itself.
+template <typename T, int kStep> struct Ring {
+    uint32_t base, slot = 0;    // this lane's first word; the slot of the next block to take
+    const char* from = nullptr;  // this lane's first word of the next block to fetch
+    int left = 0;                // blocks to fetch at `from` and after it
+
+    __device__ __forceinline__ explicit Ring(float* memory)
+        : base(smem_u32(memory) + (threadIdx.x >> 5) * (kDepth * kBlockBytes) + (threadIdx.x & 31) * 16) {}
+
+    __device__ __forceinline__ void point_at(const Row<T>& row, int first, int count) {
+        from = reinterpret_cast<const char*>(row.first) + (first * kBlockBytes + (threadIdx.x & 31) * 16);
+        left = count;
+    }
+    __device__ __forceinline__ void fetch(uint32_t to) {
+        if (left > 0) {
+            copy16(base + to, from);
+            copy16(base + to + kBlockBytes / 2, from + kBlockBytes / 2);
+            from += kStep * kBlockBytes;
+            --left;
+        }
+        copies_commit();
+    }
+    // The first blocks of a row that nothing has been fetched of.
+    __device__ __forceinline__ void fill() {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) fetch((slot + d * kBlockBytes) % (kDepth * kBlockBytes));
+    }
+    __device__ __forceinline__ void take(uint4 (&w)[2]) {
+        copies_wait<kDepth - 1>();
+        w[0] = load_shared16(base + slot);
+        w[1] = load_shared16(base + slot + kBlockBytes / 2);
+    }
+    __device__ __forceinline__ void fetch_next() {
+        fetch(slot);
+        slot = (slot + kBlockBytes) % (kDepth * kBlockBytes);
+    }
+};
+
+// A lane's eight elements of each of a block's segments, and the places of these in the segment.
+template <typename T> __device__ __forceinline__ void segments_of(const uint4 (&w)[2], Raw8<T> (&raw)[kParts<T>]) {
+    if constexpr (sizeof(T) == 2) raw[0].w[0] = w[0], raw[1].w[0] = w[1];
+    else raw[0].w[0] = w[0], raw[0].w[1] = w[1];
+}
+template <typename T> __device__ __forceinline__ int place_in_segment(int lane, int e) {
+    return sizeof(T) == 2 ? lane * 8 + e : lane * 4 + e % 4 + e / 4 * 128;
+}
+
+// ------------------------------------------------------------- selection, by one warp
+
+__device__ __forceinline__ float warp_min(float v) {
+    float r;
+    asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// A team's warps select together: kWarps of them, which are the CTA.
+template <int kWarps> __device__ __forceinline__ void team_sync() {
+    if constexpr (kWarps == 1) __syncwarp();
+    else __syncthreads();
+}
+
+// A selection's memory: candidates' keys, segments chosen (and units), counters, each warp's words that hold
+// candidates, and the segments they look at (or the largest of units).
+struct Selection {
+    uint64_t* list;
+    int* chosen;
+    int* counts;
+    uint8_t* words;
+    uint32_t* stage;
+
+    __host__ __device__ static constexpr size_t bytes(int warps, int k) {
+        const size_t stage = size_t{kStageBytes} * warps, units = size_t{128} * k;
+        return kListed * 8 + 2 * DRS_MAX_ALTERNATIVES * 4 + 16 + 128 * warps + (stage > units ? stage : units);
+    }
+    __device__ Selection(float* memory, int warps) {
+        list = reinterpret_cast<uint64_t*>(memory);
+        chosen = reinterpret_cast<int*>(list + kListed);
+        counts = chosen + 2 * DRS_MAX_ALTERNATIVES;
+        words = reinterpret_cast<uint8_t*>(counts + 4);
+        stage = reinterpret_cast<uint32_t*>(words + 128 * warps);
+    }
+};
+
+// Places for this warp's `mine` entries per lane in a list that the team counts in `count`: the lane's first.
+template <int kWarps> __device__ __forceinline__ int places_for(int mine, int* count, int lane) {
+    const int upto = warp_scan_inclusive(mine, lane);
+    int first = 0;
+    if (lane == 31) {
+        if constexpr (kWarps == 1) first = *count, *count = first + upto;
+        else if (upto) first = atomicAdd(count, upto);
+    }
+    return __shfl_sync(0xffffffffu, first, 31) + upto - mine;
+}
+
+// f(key, how many keys exceed it) for each of the n keys of a list, by the team.
+template <int kWarps, typename F> __device__ __forceinline__ void rank_keys(const uint64_t* list, int n, F f) {
+    const ulonglong2* const pairs = reinterpret_cast<const ulonglong2*>(list);
+    constexpr int kThreads = kWarps * 32;
+    for (int i = threadIdx.x; i < n; i += 2 * kThreads) {  // two of them at a time
+        const uint64_t a = list[i], b = i + kThreads < n ? list[i + kThreads] : ~0ull, last = list[n - 1];
+        int above_a = (n & 1) && last > a, above_b = (n & 1) && last > b;
+#pragma unroll 4
+        for (int j = 0; j < n / 2; ++j) {
+            const ulonglong2 p = pairs[j];
+            above_a += (p.x > a) + (p.y > a);
+            above_b += (p.x > b) + (p.y > b);
+        }
+        f(a, above_a);
+        if (i + kThreads < n) f(b, above_b);
+    }
+}
+
+// A value that at least k of the 128 n values reach, or -inf (which NaN counts
+// as): the k-th largest of the largest of 32 (k <= 32) or 64 groups of them.
+__device__ __forceinline__ float reached_by(const float4* value, int n, int k, int lane) {
+    float a = -INFINITY, b = -INFINITY;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float4 v = value[i * 32 + lane];
+        a = fmaxf(a, fmaxf(v.x, v.y));
+        b = fmaxf(b, fmaxf(v.z, v.w));
+    }
     int above_a = 0, above_b = 0;
     if (k <= 32) {
-        for (int i = lane; i < n; i += 32) a = max(a, value[i]);
-#pragma unroll 8
+        a = fmaxf(a, b);
+#pragma unroll
         for (int i = 0; i < 32; ++i) above_a += __shfl_sync(0xffffffffu, a, i) > a;
-        return __reduce_min_sync(0xffffffffu, above_a < k ? a : 0xffffffffu);  // the smallest that fewer than k exceed
+        return warp_min(above_a < k ? a : INFINITY);  // the smallest that fewer than k exceed
     }
-    for (int i = lane; i < n; i += 64) {
-        a = max(a, value[i]);
-        if (i + 32 < n) b = max(b, value[i + 32]);
-    }
-#pragma unroll 8
+#pragma unroll
     for (int i = 0; i < 32; ++i) {
-        const uint32_t u = __shfl_sync(0xffffffffu, a, i), v = __shfl_sync(0xffffffffu, b, i);
+        const float u = __shfl_sync(0xffffffffu, a, i), v = __shfl_sync(0xffffffffu, b, i);
         above_a += (u > a) + (v > a);
         above_b += (u > b) + (v > b);
     }
-    return __reduce_min_sync(0xffffffffu, min(above_a < k ? a : 0xffffffffu, above_b < k ? b : 0xffffffffu));
+    return warp_min(fminf(above_a < k ? a : INFINITY, above_b < k ? b : INFINITY));
 }
 
-// The k largest of n values, equal ones by index, as indices in ascending
-// order (all when n <= k): their number. By all threads; any values.
-__device__ int select_exact(const uint32_t* value, int n, int k, int* chosen, Selection& s) {
-    const int tid = threadIdx.x, lane = tid & 31;
-    if (n <= k) {
-        __syncthreads();
-        for (int i = tid; i < n; i += kThreadsPerRow) chosen[i] = i;
-        __syncthreads();
-        return n;
-    }
-    __syncthreads();
-    if (tid < 32) s.counts[tid] = 0;
-    __syncthreads();
-    uint32_t least = 0;  // the largest number that at least k values reach, bit by bit
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t next = least | 1u << bit;
-        int reach = 0;
-        for (int i = tid; i < n; i += kThreadsPerRow) reach += value[i] >= next;
-        reach = __reduce_add_sync(0xffffffffu, reach);
-        if (lane == 0) atomicAdd(&s.counts[bit], reach);
-        __syncthreads();
-        reach = s.counts[bit];
-        if (reach >= k) least = next;
-        if (reach == k) break;
-    }
-    if (tid < 32) {  // those above, and the first of the equal ones
-        int above = 0;
-        for (int i = lane; i < n; i += 32) above += value[i] > least;
-        int ties = k - __reduce_add_sync(0xffffffffu, above), at = 0;
-        for (int i = lane; i - lane < n && at < k; i += 32) {
-            const uint32_t v = i < n ? value[i] : 0;
-            const uint32_t more = __ballot_sync(0xffffffffu, v > least);
-            const uint32_t same = __ballot_sync(0xffffffffu, i < n && v == least);
-            const uint32_t below = (1u << lane) - 1;
-            const int rank = __popc(same & below);
-            const bool take = (more >> lane & 1) || ((same >> lane & 1) && rank < ties);
-            const uint32_t taken = __ballot_sync(0xffffffffu, take);
-            if (take) chosen[at + __popc(taken & below)] = i;
-            at += __popc(taken);
-            ties -= min(ties, __popc(same));
-        }
-    }
-    __syncthreads();
-    return k;
-}
-
-// The row's k largest logits into s.list, in no order: their number, at least k (keys of 0
-// among them are places outside the row). segment: the orders of its n
-// segments' largest.
-template <typename T> __device__ int select_top(const Row<T>& row, const uint32_t* segment, int n, int k, Selection& s) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// The k largest of n numbers, equal ones by index, as indices in ascending
+// order (all when n <= k): how many.
+__device__ int select_exact(const uint32_t* value, int n, int k, int* chosen, int lane) {
+    __syncwarp();
+    uint32_t least = 0;  // the largest number that at least k reach, bit by bit
     if (n > k) {
-        // The short way: segments that reach a bound, k of them, and what in
-        // these reaches the k-th one's largest.
-        const uint32_t bound = reached_by(segment, n, k, lane);
-        for (int i = tid; i < n; i += kThreadsPerRow) {
-            if (segment[i] >= bound) {
-                const int at = atomicAdd(&s.n, 1);
-                if (at < kListed) s.list[at] = key_of(segment[i], i);
-            }
-        }
-        __syncthreads();
-        const int listed = s.n;
-        if (listed <= kListed - 4) {
-            if (tid < 3) s.list[listed + tid] = 0;
-            __syncthreads();
-            for (int i = tid; i < listed; i += kThreadsPerRow) {
-                const uint64_t key = s.list[i];
-                const int above = keys_above(s.list, listed, key);
-                if (above < k) s.chosen[0][above] = place_of(key);
-            }
-            __syncthreads();
-            const uint32_t least = segment[s.chosen[0][k - 1]];
-            constexpr int kAtOnce = 4;
-            for (int c = warp; c < k; c += kRowWarps * kAtOnce) {
-                Raw8<T> raw[kAtOnce];
-                int place[kAtOnce];
-#pragma unroll
-                for (int u = 0; u < kAtOnce; ++u) {
-                    const int at = c + u * kRowWarps;
-                    place[u] = at < k ? s.chosen[0][at] * kSegment + lane * 8 : row.end;  // the row's end: none
-                    raw[u] = row.unit(place[u]);
-                }
-#pragma unroll
-                for (int u = 0; u < kAtOnce; ++u) {
-                    float v[8];
-                    raw[u].unpack(v);
-                    uint32_t reach = 0;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const bool inside = place[u] + e >= row.lead && place[u] + e < row.end;
-                        reach |= (inside && order_of(v[e]) >= least ? 1u : 0u) << e;
-                    }
-                    if (reach) {
-                        int at = atomicAdd(&s.m, __popc(reach));
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (reach >> e & 1) {
-                                if (at < kListed) s.list[at] = key_of(order_of(v[e]), place[u] + e);
-                                ++at;
-                            }
-                    }
-                }
-            }
-            __syncthreads();
-            if (s.m <= kListed - 4) return s.m;
+        for (int bit = 31; bit >= 0; --bit) {
+            const uint32_t next = least | 1u << bit;
+            int reach = 0;
+            for (int i = lane; i < n; i += 32) reach += value[i] >= next;
+            reach = __reduce_add_sync(0xffffffffu, reach);
+            if (reach >= k) least = next;
+            if (reach == k) break;
         }
     }
-    // The long way, for rows with many equal logits and for short ones: the k
-    // segments, then their k units of eight, then their k elements.
-    const int segments = select_exact(segment, n, k, s.chosen[0], s);
-    for (int c = warp; c < segments; c += kRowWarps) {
+    int above = 0;
+    for (int i = lane; i < n; i += 32) above += value[i] > least;
+    int ties = min(n, k) - __reduce_add_sync(0xffffffffu, above), at = 0;
+    const uint32_t below = (1u << lane) - 1;
+    for (int i = lane; i - lane < n; i += 32) {
+        const uint32_t v = i < n ? value[i] : 0;
+        const uint32_t same = __ballot_sync(0xffffffffu, i < n && v == least);
+        const bool take = i < n && (v > least || (v == least && __popc(same & below) < ties));
+        const uint32_t taken = __ballot_sync(0xffffffffu, take);
+        if (take) chosen[at + __popc(taken & below)] = i;
+        at += __popc(taken);
+        ties -= min(ties, __popc(same));
+    }
+    __syncwarp();
+    return at;
+}
+
+// For rows with many equal logits, or where they rise over long stretches: the k segments,
+// then their k units of eight columns, then their k elements.
+template <typename T> __device__ __noinline__ int select_slowly(const Row<T> row, float* segment, int n, int k, const Selection s) {
+    const int lane = threadIdx.x & 31;
+    uint32_t* const order = reinterpret_cast<uint32_t*>(segment);
+    for (int i = lane; i < n; i += 32) order[i] = order_of(segment[i]);
+    const int segments = select_exact(order, n, k, s.chosen, lane);
+    for (int c = 0; c < segments; ++c) {
         float v[8];
-        const int place = s.chosen[0][c] * kSegment + lane * 8;
+        const int place = s.chosen[c] * kSegment + lane * 8;
         row.unit(place).unpack(v);
         uint32_t most = 0;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (place + e >= row.lead && place + e < row.end) most = max(most, order_of(v[e]));
-        s.unit[c * 32 + lane] = most;
+        s.stage[c * 32 + lane] = most;
     }
-    const int units = select_exact(s.unit, segments * 32, k, s.chosen[1], s);
-    if (tid < units) s.chosen[1][tid] = s.chosen[0][s.chosen[1][tid] >> 5] * 32 + (s.chosen[1][tid] & 31);
-    __syncthreads();
-    for (int i = tid; i < units * 8; i += kThreadsPerRow) {
-        const int place = s.chosen[1][i >> 3] * 8 + (i & 7);
-        s.unit[i] = place >= row.lead && place < row.end ? order_of(to_f(row.first[place])) : 0;
+    int* const units = s.chosen + DRS_MAX_ALTERNATIVES;
+    const int m = select_exact(s.stage, segments * 32, k, units, lane);
+    for (int i = lane; i < m; i += 32) units[i] = s.chosen[units[i] / 32] * 32 + units[i] % 32;
+    __syncwarp();
+    for (int i = lane; i < m * 8; i += 32) {
+        const int place = units[i >> 3] * 8 + (i & 7);
+        s.stage[i] = place >= row.lead && place < row.end ? order_of(to_f(row.first[place])) : 0;
     }
-    const int found = select_exact(s.unit, units * 8, k, s.chosen[0], s);
-    if (tid < found) {
-        const int i = s.chosen[0][tid];
-        s.list[tid] = s.unit[i] ? key_of(s.unit[i], s.chosen[1][i >> 3] * 8 + (i & 7)) : 0;
+    const int found = select_exact(s.stage, m * 8, k, s.chosen, lane);
+    for (int i = lane; i < found; i += 32) {
+        const int j = s.chosen[i];
+        s.list[i] = s.stage[j] ? key_of(s.stage[j], units[j >> 3] * 8 + (j & 7)) : 0;
     }
-    __syncthreads();
     return found;
+}
+
+// The row's k largest logits into s.list, in no order: how many keys, at least k.
+// segment: its n segments' largest, with room up to a multiple of 128. s.counts are 0 before. By the
+// team, with a barrier at its end.
+template <int kWarps, typename T>
+__device__ __forceinline__ int select_top(const Row<T>& row, float* segment, int n, int k, const Selection& s) {
+    constexpr float kLowest = -0x1.fffffep127f;  // all but -inf and NaN reach it
+    constexpr int kThreads = kWarps * 32;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int segments = n;       // looked at
+    float least = kLowest;  // what reaches it is taken
+    bool slowly = false;
+    if (n > k) {
+        const int quads = (n + 127) / 128;
+        for (int i = n + tid; i < quads * 128; i += kThreads) segment[i] = -INFINITY;
+        team_sync<kWarps>();
+        const float4* const quad = reinterpret_cast<const float4*>(segment);
+        const float bound = fmaxf(reached_by(quad, quads, k, lane), kLowest);
+        // 32 values per lane at a time: a bit for each that reaches the bound
+        for (int i0 = warp; i0 < quads; i0 += 8 * kWarps) {
+            uint32_t reach = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int at = i0 + i * kWarps;
+                if (at >= quads) break;
+                const float4 v = quad[at * 32 + lane];
+                reach |= (v.x >= bound ? 1u : 0u) << (4 * i) | (v.y >= bound ? 2u : 0u) << (4 * i) |
+                         (v.z >= bound ? 4u : 0u) << (4 * i) | (v.w >= bound ? 8u : 0u) << (4 * i);
+            }
+            int at = places_for<kWarps>(__popc(reach), &s.counts[0], lane);
+            for (; reach; reach &= reach - 1, ++at) {
+                const int bit = __ffs(reach) - 1, place = ((i0 + bit / 4 * kWarps) * 32 + lane) * 4 + bit % 4;
+                if (at < kListed) s.list[at] = key_of(order_of(segment[place]), place);
+            }
+        }
+        team_sync<kWarps>();
+        const int listed = s.counts[0];
+        slowly = listed > kListed;
+        if (!slowly) {
+            rank_keys<kWarps>(s.list, listed, [&](uint64_t key, int above) {
+                if (above < k) s.chosen[above] = place_of(key);
+            });
+            segments = min(listed, k);
+            team_sync<kWarps>();
+            if (listed >= k) least = segment[s.chosen[k - 1]];
+        }
+    } else {
+        for (int i = tid; i < n; i += kThreads) s.chosen[i] = i;
+        float* const unit = reinterpret_cast<float*>(s.stage);
+        for (int c = warp; c < (n + 3) / 4 * 4; c += kWarps)  // a lane's in its own float4s
+            unit[(c / 4 * 32 + lane) * 4 + c % 4] = c < n ? Eight<T>::largest(row.unit(c * kSegment + lane * 8)) : -INFINITY;
+        team_sync<kWarps>();
+        if (n * 32 >= k) least = fmaxf(reached_by(reinterpret_cast<const float4*>(unit), (n + 3) / 4, k, lane), kLowest);
+        team_sync<kWarps>();
+    }
+    if (!slowly) {
+        // Each warp has its share of the segments: their words that hold something to take, then these in turn
+        // by a lane each.
+        constexpr int kBytes = kSegment * static_cast<int>(sizeof(T)), kAtOnce = kStageBytes / kBytes;
+        constexpr int kHalves = sizeof(T) / 2;
+        static_assert(kAtOnce * 32 <= 128, "words");
+        char* const stage = reinterpret_cast<char*>(s.stage) + warp * kStageBytes;
+        uint8_t* const words = s.words + warp * 128;
+        const uint32_t to = smem_u32(stage) + lane * 16;
+        const auto word_at = [&](int segment_at, int lane_at) {
+            Raw8<T> raw;
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+                raw.w[h] = reinterpret_cast<const uint4*>(stage)[(segment_at * kHalves + h) * 32 + lane_at];
+            return raw;
+        };
+        for (int c0 = warp; c0 < segments; c0 += kAtOnce * kWarps) {
+            // this lane's of the segments at once
+            const int own = lane < kAtOnce && c0 + lane * kWarps < segments ? s.chosen[c0 + lane * kWarps] : -1;
+            const T* const line = row.first + lane * static_cast<int>(16 / sizeof(T));
+            if (__all_sync(0xffffffffu, own < 0 || row.whole(own * kSegment, kSegment))) {
+#pragma unroll
+                for (int c = 0; c < kAtOnce; ++c) {
+                    const int segment_at = __shfl_sync(0xffffffffu, own, c);
+                    if (segment_at >= 0)
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h)
+                            copy16(to + c * kBytes + h * 512, line + segment_at * kSegment + h * 128);
+                }
+            } else {
+                for (int c = 0; c < kAtOnce; ++c) {
+                    const int segment_at = __shfl_sync(0xffffffffu, own, c);
+                    const int place = segment_at * kSegment + lane * static_cast<int>(16 / sizeof(T));
+                    if (segment_at >= 0)
+                        for (int h = 0; h < kHalves; ++h) store_shared16(to + c * kBytes + h * 512, row.word(place + h * 128));
+                }
+            }
+            copies_commit();
+            copies_wait<0>();
+            __syncwarp();
+            uint32_t lanes = 0;  // of this lane's segment, those whose words hold something
+#pragma unroll
+            for (int c = 0; c < kAtOnce; ++c) {
+                const uint32_t some = __ballot_sync(0xffffffffu, Eight<T>::largest(word_at(c, lane)) >= least);
+                if (lane == c) lanes = some;
+            }
+            if (own < 0) lanes = 0;
+            const int mine = __popc(lanes), upto = warp_scan_inclusive(mine, lane);
+            const int count = __shfl_sync(0xffffffffu, upto, 31);
+            for (int at = upto - mine; lanes; lanes &= lanes - 1) words[at++] = static_cast<uint8_t>(lane * 32 + __ffs(lanes) - 1);
+            __syncwarp();
+            for (int i = lane; i - lane < count; i += 32) {
+                const int word = i < count ? words[i] : 0;
+                const int place = __shfl_sync(0xffffffffu, own, word / 32) * kSegment;
+                float v[8];
+                word_at(word / 32, word % 32).unpack(v);
+                uint32_t reach = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) reach |= (v[e] >= least ? 1u : 0u) << e;
+                if (i >= count) reach = 0;
+                int at = places_for<kWarps>(__popc(reach), &s.counts[1], lane);
+                for (; reach; reach &= reach - 1, ++at) {
+                    const int in = place_in_segment<T>(word % 32, __ffs(reach) - 1);
+                    const T x = reinterpret_cast<const T*>(stage)[word / 32 * kSegment + in];
+                    if (at < kListed) s.list[at] = key_of(order_of(to_f(x)), place + in);
+                }
+            }
+            __syncwarp();
+        }
+        team_sync<kWarps>();
+        slowly = s.counts[1] > kListed;
+    }
+    if (slowly || s.counts[1] < k) {
+        team_sync<kWarps>();  // everyone has read the counter
+        if (warp == 0) {
+            int found = s.counts[1];
+            if (slowly) {
+                found = select_slowly(row, segment, n, k, s);
+            } else {
+                // Fewer than k above -inf: the first columns at -inf (or NaN) follow.
+                for (int place = row.lead + lane; found < k && place - lane < row.end; place += 32) {
+                    const bool take = place < row.end && !(to_f(row.first[place]) > -INFINITY);
+                    const uint32_t taken = __ballot_sync(0xffffffffu, take);
+                    const int at = found + __popc(taken & ((1u << lane) - 1));
+                    if (take && at < kListed) s.list[at] = key_of(order_of(-INFINITY), place);
+                    found += __popc(taken);
+                }
+            }
+            if (lane == 0) s.counts[1] = found;
+        }
+        team_sync<kWarps>();
+    }
+    return s.counts[1];
 }
 
 // ------------------------------------------------------------- sums
@@ -352,204 +592,386 @@ __device__ __forceinline__ Sums together(Sums s, bool have, float c) {
     return Sums{top, warp_sum(s.sum * f), warp_sum(f * fmaf(d, s.sum, s.weighted)), warp_sum(s.above)};
 }
 
-// The sums of a thread's part of a row; top and reference are the warp's.
-struct RunningSums {
-    float top = -INFINITY, reference = -INFINITY, bound = -INFINITY;  // bound: where the reference moves
-    float base = 0.0f;                                                // the reference, 0 before there is one
+// The sums of a thread's part of a row; top and reference are the warp's. The
+// reference is kept as an exponent, shift = M c rounded: t = x c - shift takes
+// one rounding, and what shift is off by moves all exponents alike and is
+// known (x c - shift at x = M). Where that is too much (shift above 2^24: tiny
+// temperatures, huge logits) or the floor leaves the type's range, the warp
+// begins again with kCareful: t is (x - M) c, held element by element.
+template <typename T, bool kCareful> struct RunningSums {
+    float top = -INFINITY, bound = -INFINITY;  // bound: where the reference moves
+    float base = 0.0f;                         // careful: M, else M c rounded; 0 before there is one
+    bool none = true;
     uint64_t sum = 0, weighted = 0;
+    Floor<T> floor;
 
-    // The reference moves to the largest so far.
-    __device__ __forceinline__ void move(float c) {
-        const float d = shift_of(reference, top, c), f = ex2_approx(d);
+    __device__ __forceinline__ RunningSums(float c) { floor.set(kLeastExponent / c); }
+
+    // The exponent by which the sums move to those relative to `to`.
+    __device__ __forceinline__ float distance(float to, float c) const {
+        if (none) return 0.0f;
+        return max_nan(kCareful ? (base - to) * c : -fmaf(to, c, -base), -1000.0f);
+    }
+
+    // The reference moves to the largest so far; false: not without care.
+    __device__ __forceinline__ bool move(float c) {
+        const float next = kCareful ? top : top * c;
+        if (!kCareful && !(fabsf(next) < 0x1p24f && floor.set(top + kLeastExponent / c))) return false;
+        const float d = none ? 0.0f : max_nan(kCareful ? (base - next) * c : base - next, -1000.0f);
+        const float f = ex2_approx(d);
         const uint64_t f2 = pack2(f, f);
         weighted = mul2(f2, fma2(pack2(d, d), sum, weighted));
         sum = mul2(f2, sum);
-        reference = base = top;
+        base = next;
         bound = top + kSlack / c;
+        none = false;
+        return true;
     }
 
-    // Eight columns per lane; most: the warp's largest.
-    template <typename T> __device__ __forceinline__ void add(const Raw8<T>& raw, float most, float c) {
-        top = fmaxf(top, most);
-        if (most > bound) move(c);
-        const uint64_t base2 = pack2(base, base), c2 = pack2(c, c);
-        float v[8];
-        raw.unpack(v);
+    // A block: its own sums first, which keeps small terms that would be lost in the row's.
+    __device__ __forceinline__ void add(const Raw8<T> (&raw)[kParts<T>], float c) {
+        const uint64_t c2 = pack2(c, c), base2 = kCareful ? pack2(base, base) : pack2(-base, -base);
+        uint64_t part = 0, weight = 0;
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-            float t0, t1;
-            unpack2(mul2(sub2(pack2(v[e], v[e + 1]), base2), c2), t0, t1);
-            t0 = max_nan(t0, kLeastExponent);
-            t1 = max_nan(t1, kLeastExponent);
-            const uint64_t p = pack2(ex2_flushed(t0), ex2_flushed(t1));
-            sum = add2(sum, p);
-            weighted = fma2(p, pack2(t0, t1), weighted);
+        for (int p = 0; p < kParts<T>; ++p) {
+            float v[8];
+            if constexpr (kCareful) raw[p].unpack(v);
+            else floor.raise(raw[p]).unpack(v);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                const uint64_t x = pack2(v[e], v[e + 1]);
+                float t0, t1;
+                unpack2(kCareful ? mul2(sub2(x, base2), c2) : fma2(x, c2, base2), t0, t1);
+                t0 = kCareful ? max_nan(t0, kLeastExponent) : Floor<T>::raise(t0);
+                t1 = kCareful ? max_nan(t1, kLeastExponent) : Floor<T>::raise(t1);
+                const uint64_t q = pack2(ex2_flushed(t0), ex2_flushed(t1)), t = pack2(t0, t1);
+                part = p + e == 0 ? q : add2(part, q);
+                weight = p + e == 0 ? mul2(q, t) : fma2(q, t, weight);
+            }
         }
+        sum = add2(sum, part);
+        weighted = add2(weighted, weight);
     }
 
+    // The warp's sums, on every lane.
     __device__ __forceinline__ Sums value(float c, int above) const {
         float s0, s1, w0, w1;
         unpack2(sum, s0, s1);
         unpack2(weighted, w0, w1);
-        const float d = shift_of(reference, top, c), f = ex2_approx(d);
-        return Sums{top, f * (s0 + s1), f * fmaf(d, s0 + s1, w0 + w1), above};
+        const float d = distance(top, c), f = ex2_approx(d);
+        return Sums{top, warp_sum(f * (s0 + s1)), warp_sum(f * fmaf(d, s0 + s1, w0 + w1)), warp_sum(above)};
     }
 };
 
-// The sums of the row's segments [first, end). kTop: their largest go to `segment`.
-template <typename T, bool kTop>
-__device__ __forceinline__ Sums row_sums(const Row<T>& row, int first, int end, float c, T own, float* segment) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    RunningSums sums;
+// What a warp does with the blocks of a row that come to it: sums, the token's rank, and (kTop) the segments'
+// largest into `segment`.
+template <typename T, bool kTop, bool kCareful> struct RowReader {
+    RunningSums<T, kCareful> sums;
+    float c, own_value;
+    T own;
+    float* segment;
     int above = 0;
-    for (int i = first + warp * kTile; i < end; i += kRowWarps * kTile) {
-        typename Eight<T>::Count exceed = Eight<T>::zero();
-        if (i + kTile <= end && row.whole(i * kSegment, kTile * kSegment)) {
-            Raw8<T> raw[kTile];
-            const T* const from = row.first + i * kSegment + lane * 8;
+
+    __device__ __forceinline__ RowReader(float c, T own, float* segment)
+        : sums(c), c(c), own_value(to_f(own)), own(own), segment(segment) {}
+
+    // false: not without care
+    __device__ __forceinline__ bool add(const Raw8<T> (&raw)[kParts<T>], int block) {
+        float most = -INFINITY;
 #pragma unroll
-            for (int u = 0; u < kTile; ++u) raw[u].load(from + u * kSegment);
-#pragma unroll
-            for (int u = 0; u < kTile; ++u) {
-                const float most = warp_max(Eight<T>::largest(raw[u]));
-                if (kTop && lane == 0) segment[i + u] = most;
-                sums.add(raw[u], most, c);
-                Eight<T>::count(raw[u], own, exceed);
-            }
-        } else {
-#pragma unroll 1
-            for (int u = i; u < min(i + kTile, end); ++u) {
-                const Raw8<T> raw = row.unit(u * kSegment + lane * 8);
-                const float most = warp_max(Eight<T>::largest(raw));
-                if (kTop && lane == 0) segment[u] = most;
-                sums.add(raw, most, c);
-                Eight<T>::count(raw, own, exceed);
-            }
+        for (int p = 0; p < kParts<T>; ++p) {
+            const float largest = warp_max(Eight<T>::largest(raw[p]));
+            if (kTop && (threadIdx.x & 31) == 0) segment[block * kParts<T> + p] = largest;
+            most = fmaxf(most, largest);
         }
-        above += Eight<T>::total(exceed);
+        sums.top = fmaxf(sums.top, most);
+        if (most > sums.bound && !sums.move(c)) return false;
+        sums.add(raw, c);
+        if (most > own_value) {
+            typename Eight<T>::Count exceed = Eight<T>::zero();
+#pragma unroll
+            for (int p = 0; p < kParts<T>; ++p) Eight<T>::count(raw[p], own, exceed);
+            above += Eight<T>::total(exceed);
+        }
+        return true;
     }
-    return sums.value(c, above);
+};
+
+// ------------------------------------------------------------- the row's results
+
+// What a row's warps need to know of it.
+template <typename T> struct Task {
+    Row<T> row;
+    T own;
+    float inverse, c;
+    __device__ __forceinline__ Task(const LogprobParams& a, int r, int id)
+        : row(static_cast<const T*>(a.logits) + r * a.row_stride, a.vocab), own(row.first[row.lead + max(id, 0)]) {
+        inverse = a.temps ? 1.0f / fmaxf(a.temps[r / a.canvas_len], kTempFloor) : 1.0f;
+        c = inverse * kLog2e;
+    }
+};
+
+// The row's token, -1 where it is passed over.
+__device__ __forceinline__ int id_of(const LogprobParams& a, int r) {
+    const int64_t id = a.id_bits == 64 ? static_cast<const int64_t*>(a.ids)[r] : static_cast<const int32_t*>(a.ids)[r];
+    return id >= 0 && id < a.vocab ? static_cast<int>(id) : -1;
 }
 
-// ------------------------------------------------------------- the kernel
+// A block by plain loads.
+template <typename T> __device__ __forceinline__ void load_block(const Row<T>& row, int block, Raw8<T> (&raw)[kParts<T>]) {
+    uint4 w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        w[h] = row.word(block * kBlock<T> + h * (kBlock<T> / 2) + static_cast<int>(threadIdx.x & 31) * static_cast<int>(16 / sizeof(T)));
+    segments_of(w, raw);
+}
 
+// Blocks first, first + step, ... below end of a row by plain loads, with care.
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kThreadsPerRow, 4) logprob_kernel(const LogprobParams a) {
-    extern __shared__ uint32_t s_segment[];  // the row's segments' largest: values, then their orders
-    __shared__ Selection s_select;
-    __shared__ uint64_t s_cta[kMaxRowCluster][2];  // the cluster's CTAs' sums
-    __shared__ Sums s_warp[kRowWarps];
-    __shared__ float s_norm[2];
+__device__ __noinline__ Sums careful_sums(const Task<T> task, int first, int step, int end, float* segment) {
+    RowReader<T, kTop, true> reader(task.c, task.own, segment);
+    for (int i = first; i < end; i += step) {
+        Raw8<T> raw[kParts<T>];
+        load_block(task.row, i, raw);
+        reader.add(raw, i);
+    }
+    return reader.sums.value(task.c, reader.above);
+}
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int csize = a.cluster, k = a.k;
-    const int rank = csize > 1 ? static_cast<int>(cluster_rank()) : 0;
-    const int64_t r = blockIdx.x / csize;
-    const int64_t id = a.id_bits == 64 ? static_cast<const int64_t*>(a.ids)[r] : static_cast<const int32_t*>(a.ids)[r];
-    if (id < 0 || id >= a.vocab) {  // the same for the whole cluster
-        if (rank == 0) {
-            if (tid == 0) {
-                a.out_logprob[r] = 0.0f;
-                if (a.out_entropy) a.out_entropy[r] = 0.0f;
-                if (a.out_rank) a.out_rank[r] = 0;
-                if (a.out_norm) a.out_norm[2 * r] = a.out_norm[2 * r + 1] = 0.0f;
-            }
-            for (int i = tid; i < k; i += kThreadsPerRow) {
-                a.out_ids[r * k + i] = -1;
-                a.out_logprobs[r * k + i] = -INFINITY;
-            }
+// Adds the blocks among [first, end) of a row that reach over its ends to a warp's sums.
+template <bool kTop, typename T>
+__device__ __forceinline__ void add_edges(const Task<T>& task, int first, int end, float* segment, Sums& sums) {
+    const int whole_first = max(task.row.whole_first(), first), whole_end = min(task.row.whole_end(), end);
+    const int lane = threadIdx.x & 31;
+    if (first < whole_first) {
+        const Sums more = careful_sums<T, kTop>(task, first, 1, min(whole_first, end), segment);
+        sums = together(lane == 0 ? sums : more, lane < 2, task.c);
+    }
+    if (whole_end < end && whole_end >= whole_first) {
+        const Sums more = careful_sums<T, kTop>(task, whole_end, 1, end, segment);
+        sums = together(lane == 0 ? sums : more, lane < 2, task.c);
+    }
+}
+
+// The warp's blocks first, first + kStep, ... (count of them), which come through the ring.
+template <bool kTop, typename T, int kStep, typename F>
+__device__ __forceinline__ Sums ring_sums(Ring<T, kStep>& ring, const Task<T>& task, int first, int count, float* segment, F all_fetched) {
+    RowReader<T, kTop, false> reader(task.c, task.own, segment);
+    bool fine = true;
+    for (int n = 0, i = first; n < count; ++n, i += kStep) {
+        uint4 w[2];
+        Raw8<T> raw[kParts<T>];
+        ring.take(w);
+        segments_of(w, raw);
+        if (fine) fine = reader.add(raw, i);
+        if (ring.left == 0) all_fetched(ring);
+        ring.fetch_next();
+    }
+    return fine ? reader.sums.value(task.c, reader.above)
+                : careful_sums<T, kTop>(task, first, kStep, first + (count - 1) * kStep + 1, segment);
+}
+
+// How many of the numbers first, first + step, ... lie below end.
+__device__ __forceinline__ int steps_below(int first, int step, int end) { return max(0, (end - first + step - 1) / step); }
+
+// A row that is passed over, by one warp.
+template <bool kTop> __device__ __forceinline__ void pass_over(const LogprobParams& a, int64_t r) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
+        a.out_logprob[r] = 0.0f;
+        if (a.out_entropy) a.out_entropy[r] = 0.0f;
+        if (a.out_rank) a.out_rank[r] = 0;
+        if (a.out_norm) a.out_norm[2 * r] = a.out_norm[2 * r + 1] = 0.0f;
+    }
+    if (kTop)
+        for (int i = lane; i < a.k; i += 32) {
+            a.out_ids[r * a.k + i] = -1;
+            a.out_logprobs[r * a.k + i] = -INFINITY;
         }
+}
+
+// The row's outputs from its sums and segments, by the team.
+template <int kWarps, bool kTop, typename T>
+__device__ __forceinline__ void finish(const LogprobParams& a, int64_t r, const Task<T>& task, const Sums& sums, float* segment,
+                                       const Selection& s) {
+    const float log_sum = sums.sum == 0.0f ? -INFINITY : logf(sums.sum);
+    if (threadIdx.x == 0) {
+        a.out_logprob[r] = (to_f(task.own) - sums.top) * task.inverse - log_sum;
+        if (a.out_entropy) a.out_entropy[r] = sums.sum == 0.0f ? 0.0f : log_sum - sums.weighted / sums.sum * kLn2;
+        if (a.out_rank) a.out_rank[r] = 1 + sums.above;
+        if (a.out_norm) a.out_norm[2 * r] = sums.top, a.out_norm[2 * r + 1] = log_sum;
+    }
+    if constexpr (kTop) {
+        const int found = select_top<kWarps>(task.row, segment, task.row.blocks() * kParts<T>, a.k, s);
+        rank_keys<kWarps>(s.list, found, [&](uint64_t key, int above) {
+            if (above >= a.k) return;
+            a.out_ids[r * a.k + above] = place_of(key) - task.row.lead;
+            a.out_logprobs[r * a.k + above] =
+                (value_of(static_cast<uint32_t>(key >> 32)) - sums.top) * task.inverse - log_sum;
+        });
+    }
+}
+
+// Dynamic shared memory: the warps' rings, a selection's (kTop), the segments' largest (kTop).
+constexpr size_t kRingBytes = kDepth * kBlockBytes;
+__host__ __device__ constexpr size_t shared_before(int warps, int k) {
+    return warps * kRingBytes + (k > 0 ? Selection::bytes(warps, k) : 0);
+}
+__host__ __device__ constexpr size_t shared_bytes(int warps, int k, int segments) {
+    return shared_before(warps, k) + (k > 0 ? static_cast<size_t>(segments + 127) / 128 * 512 : 0);
+}
+
+// ------------------------------------------------------------- many rows
+
+// A team of kWarps warps, a CTA, takes rows in turn.
+template <int kWarps, bool kTop, typename T>
+__global__ void __launch_bounds__(kWarps * 32, kResident / kWarps) logprob_kernel(const LogprobParams a) {
+    extern __shared__ __align__(16) float s_memory[];
+    __shared__ Sums s_warp[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Selection select(s_memory + kWarps * kRingBytes / 4, kWarps);
+    float* const segment = s_memory + shared_before(kWarps, kTop ? a.k : 0) / 4;
+    const int rows = static_cast<int>(a.rows), step = static_cast<int>(gridDim.x);
+    Ring<T, kWarps> ring(s_memory);
+    int id = id_of(a, blockIdx.x), next_id = rows - static_cast<int>(blockIdx.x) > step ? id_of(a, blockIdx.x + step) : -1;
+    Task<T> task(a, blockIdx.x, id);
+    bool fetched = false;  // the row's first blocks are on their way
+    for (int r = blockIdx.x; r < rows; r += step) {
+        const Task<T> next(a, rows - r > step ? r + step : r, next_id);  // its loads come back while this row is read
+        const int next_next_id = rows - r > 2 * step ? id_of(a, r + 2 * step) : -1;
+        const int first = task.row.whole_first() + warp, next_first = next.row.whole_first() + warp;
+        const int count = steps_below(first, kWarps, task.row.whole_end());
+        const int next_count = steps_below(next_first, kWarps, next.row.whole_end());
+        if (id >= 0) {
+            if (!fetched) {
+                ring.point_at(task.row, first, count);
+                ring.fill();
+            }
+            fetched = false;
+            const bool go_on = next_id >= 0 && count >= kDepth;
+            Sums sums = ring_sums<kTop>(ring, task, first, count, segment, [&](Ring<T, kWarps>& g) {
+                if (go_on && !fetched) {
+                    g.point_at(next.row, next_first, next_count);
+                    fetched = true;
+                }
+            });
+            if (warp == kWarps - 1) add_edges<kTop>(task, 0, task.row.blocks(), segment, sums);
+            if constexpr (kWarps > 1) {
+                if (lane == 0) s_warp[warp] = sums;
+                if (kTop && threadIdx.x == 0) select.counts[0] = select.counts[1] = 0;
+                __syncthreads();
+                sums = together(s_warp[lane % kWarps], lane < kWarps, task.c);
+            } else {
+                if (kTop && lane == 0) select.counts[0] = select.counts[1] = 0;
+                __syncwarp();
+            }
+            finish<kWarps, kTop>(a, r, task, sums, segment, select);
+            team_sync<kWarps>();
+        } else {
+            if (warp == 0) pass_over<kTop>(a, r);
+            fetched = false;
+        }
+        id = next_id;
+        next_id = next_next_id;
+        task = next;
+    }
+}
+
+// ------------------------------------------------------------- few rows
+
+// A cluster takes a row; its first CTA finishes it.
+template <bool kTop, typename T>
+__global__ void __launch_bounds__(256, kResident / 8) logprob_cluster_kernel(const LogprobParams a) {
+    constexpr int kWarps = 8;
+    extern __shared__ __align__(16) float s_memory[];
+    __shared__ uint64_t s_cta[kMaxRowCluster][2];  // the CTAs' sums
+    __shared__ Sums s_warp[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = static_cast<int>(cluster_rank());
+    const Selection select(s_memory + kWarps * kRingBytes / 4, kWarps);
+    float* const segment = s_memory + shared_before(kWarps, kTop ? a.k : 0) / 4;
+    const int r = static_cast<int>(blockIdx.x / a.cluster);
+    cluster_arrive();
+    // the first blocks are on their way before the token is known
+    const Row<T> row(static_cast<const T*>(a.logits) + r * a.row_stride, a.vocab);
+    const int first = min(rank * a.part, row.blocks()), end = min(first + a.part, row.blocks());
+    Ring<T, kWarps> ring(s_memory);
+    const int at = max(first, row.whole_first()) + warp, count = steps_below(at, kWarps, min(end, row.whole_end()));
+    ring.point_at(row, at, count);
+    ring.fill();
+    const int id = id_of(a, r);
+    if (id < 0) {  // the same for the whole cluster
+        copies_wait<0>();
+        if (rank == 0 && warp == 0) pass_over<kTop>(a, r);
+        cluster_wait();
         return;
     }
-    if (csize > 1) cluster_arrive();
-    const T* const x = static_cast<const T*>(a.logits) + r * a.row_stride;
-    const Row<T> row(x, a.vocab);
-    const T own = x[id];
-    const float inverse = a.temps ? 1.0f / fmaxf(a.temps[r / a.canvas_len], kTempFloor) : 1.0f;
-    const float c = inverse * kLog2e;
-
-    const int segments = (row.end + kSegment - 1) / kSegment;
-    const int first = min(rank * a.part, segments), end = min(first + a.part, segments);
-    Sums sums = row_sums<T, kTop>(row, first, end, c, own, reinterpret_cast<float*>(s_segment));
-    sums.sum = warp_sum(sums.sum);
-    sums.weighted = warp_sum(sums.weighted);
-    sums.above = warp_sum(sums.above);
+    const Task<T> task(a, r, id);
+    Sums sums = ring_sums<kTop>(ring, task, at, count, segment, [](Ring<T, kWarps>&) {});
+    if (warp == kWarps - 1) add_edges<kTop>(task, first, end, segment, sums);
     if (lane == 0) s_warp[warp] = sums;
-    if (kTop && tid == 0) s_select.n = s_select.m = 0;
+    if (kTop && tid == 0) select.counts[0] = select.counts[1] = 0;
     __syncthreads();
-    if (kTop && rank == 0)
-        for (int i = first + tid; i < end; i += kThreadsPerRow) s_segment[i] = order_of(__uint_as_float(s_segment[i]));
-    if (csize > 1) {  // the first CTA takes it from here
-        cluster_wait();
-        if (rank != 0) {
-            if (kTop)
-                for (int i = first + tid; i < end; i += kThreadsPerRow)
-                    store_remote32(&s_segment[i], 0, order_of(__uint_as_float(s_segment[i])));
-        }
-        if (warp == 0) {
-            sums = together(s_warp[lane % kRowWarps], lane < kRowWarps, c);
-            if (lane == 0) {
-                store_remote(&s_cta[rank][0], 0, pack2(sums.top, sums.sum));
-                store_remote(&s_cta[rank][1], 0, pack2(sums.weighted, __int_as_float(sums.above)));
-            }
-        }
-        cluster_sync_all();
-        if (rank != 0) return;
-    } else if (kTop) {
-        __syncthreads();
-    }
+    cluster_wait();
+    if (kTop && rank != 0)
+        for (int i = first * kParts<T> + tid; i < end * kParts<T>; i += kWarps * 32)
+            store_remote32(&segment[i], 0, __float_as_uint(segment[i]));
     if (warp == 0) {
-        if (csize > 1) {
-            const int from = lane % kMaxRowCluster;
-            unpack2(s_cta[from][0], sums.top, sums.sum);
-            float above;
-            unpack2(s_cta[from][1], sums.weighted, above);
-            sums.above = __float_as_int(above);
-            sums = together(sums, lane < csize, c);
-        } else {
-            sums = together(s_warp[lane % kRowWarps], lane < kRowWarps, c);
-        }
+        sums = together(s_warp[lane % kWarps], lane < kWarps, task.c);
         if (lane == 0) {
-            const float log_sum = sums.sum == 0.0f ? -INFINITY : logf(sums.sum);
-            a.out_logprob[r] = (to_f(own) - sums.top) * inverse - log_sum;
-            if (a.out_entropy) a.out_entropy[r] = sums.sum == 0.0f ? 0.0f : log_sum - sums.weighted / sums.sum * kLn2;
-            if (a.out_rank) a.out_rank[r] = 1 + sums.above;
-            if (a.out_norm) a.out_norm[2 * r] = sums.top, a.out_norm[2 * r + 1] = log_sum;
-            s_norm[0] = sums.top;
-            s_norm[1] = log_sum;
+            store_remote(&s_cta[rank][0], 0, pack2(sums.top, sums.sum));
+            store_remote(&s_cta[rank][1], 0, pack2(sums.weighted, __int_as_float(sums.above)));
         }
     }
-    if (!kTop) return;
-    const int found = select_top(row, s_segment, segments, k, s_select);  // a barrier comes before s_norm's use
-    if (tid < 3) s_select.list[found + tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < found; i += kThreadsPerRow) {
-        const uint64_t key = s_select.list[i];
-        const int above = keys_above(s_select.list, found, key);
-        if (above < k && key) {
-            a.out_ids[r * k + above] = place_of(key) - row.lead;
-            a.out_logprobs[r * k + above] = (value_of(static_cast<uint32_t>(key >> 32)) - s_norm[0]) * inverse - s_norm[1];
-        }
-    }
+    cluster_sync_all();
+    if (rank != 0) return;
+    const int from = lane % kMaxRowCluster;
+    float above;
+    unpack2(s_cta[from][0], sums.top, sums.sum);
+    unpack2(s_cta[from][1], sums.weighted, above);
+    sums.above = __float_as_int(above);
+    sums = together(sums, lane < a.cluster, task.c);
+    finish<kWarps, kTop>(a, r, task, sums, segment, select);
 }
 
-template <typename T> drs_status launch_logprobs(LogprobParams a, int64_t rows, cudaStream_t stream) {
+// ------------------------------------------------------------- launches
+
+using LogprobKernel = void (*)(LogprobParams);
+
+template <typename T> LogprobKernel logprob_kernel_of(int warps, bool top) {
+    if (warps == 1) return top ? logprob_kernel<1, true, T> : logprob_kernel<1, false, T>;
+    if (warps == 2) return top ? logprob_kernel<2, true, T> : logprob_kernel<2, false, T>;
+    if (warps == 4) return top ? logprob_kernel<4, true, T> : logprob_kernel<4, false, T>;
+    return top ? logprob_kernel<8, true, T> : logprob_kernel<8, false, T>;
+}
+
+template <typename T> drs_status launch_logprobs(LogprobParams a, bool vec, cudaStream_t stream) {
     const int sms = sm_count();
     if (sms <= 0) return DRS_ERR_CUDA;
-    const int64_t segments = ceil_div(a.vocab + 16 / sizeof(T) - 1, kSegment);
-    const int64_t resident = int64_t{sms} * 4;
-    int cluster = 1;
-    while (cluster < kMaxRowCluster &&
-           segments > 32 * cluster && rows * cluster * 2 <= resident - (cluster < 8 ? sms / 2 : sms * 3 / 2))
+    a.blocks = static_cast<int32_t>(ceil_div(a.vocab + (vec ? 0 : 16 / sizeof(T) - 1), kBlock<T>));
+    const int segments = a.blocks * kParts<T>;
+    int cluster = 1, warps = 8;
+    while (cluster < kMaxRowCluster && a.vocab > 8192 * cluster &&
+           a.rows * cluster * 2 <= int64_t{sms} * 4 - (cluster < 8 ? sms / 2 : sms * 3 / 2))
         cluster *= 2;
+    if (getenv("LPC")) cluster = atoi(getenv("LPC"));
+    if (getenv("LPT")) warps = atoi(getenv("LPT"));
+    if (cluster > 1) warps = 8;
     a.cluster = cluster;
-    a.part = static_cast<int32_t>(ceil_div(segments, cluster));
-    const auto kernel = a.k > 0 ? logprob_kernel<T, true> : logprob_kernel<T, false>;
-    if (cluster > 8 && !prepare_kernel(reinterpret_cast<const void*>(kernel), 0, true)) return DRS_ERR_CUDA;
+    a.part = static_cast<int32_t>(ceil_div(a.blocks, cluster));
+    const bool top = a.k > 0;
+    const size_t smem = shared_bytes(warps, a.k, segments);
+    const int per_sm = static_cast<int>(kSmemPerSm / (smem + kSmemReserved + 512));
+    const int64_t teams = int64_t{sms} * (per_sm < kResident / warps ? per_sm : kResident / warps);
+    const LogprobKernel kernel =
+        cluster > 1 ? (top ? logprob_cluster_kernel<true, T> : logprob_cluster_kernel<false, T>) : logprob_kernel_of<T>(warps, top);
+    const size_t large = smem > 46 * 1024 ? smem : 0;  // beyond what every launch may have, beside the static memory
+    if ((large || cluster > 8) && !prepare_kernel(reinterpret_cast<const void*>(kernel), large, cluster > 8))
+        return DRS_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(rows * cluster));
-    cfg.blockDim = dim3(kThreadsPerRow);
-    cfg.dynamicSmemBytes = a.k > 0 ? segments * sizeof(uint32_t) : 0;
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster > 1 ? a.rows * cluster : a.rows < teams ? a.rows : teams));
+    cfg.blockDim = dim3(warps * 32);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -557,7 +979,7 @@ template <typename T> drs_status launch_logprobs(LogprobParams a, int64_t rows, 
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, a));
 }
 
@@ -589,10 +1011,12 @@ extern "C" drs_status drs_token_logprobs(const void* logits, drs_dtype dtype, in
     a.out_norm = out_norm;
     a.out_ids = out_ids;
     a.out_logprobs = out_logprobs;
+    a.rows = rows;
     a.row_stride = row_stride;
     a.canvas_len = canvas_len;
     a.vocab = static_cast<int32_t>(vocab);
     a.k = k;
     a.id_bits = id_bits;
-    return with_dtype(dtype, [&](auto t) { return launch_logprobs<decltype(t)>(a, rows, static_cast<cudaStream_t>(stream)); });
+    const bool vec = aligned(logits, 16) && row_stride * dtype_bytes(dtype) % 16 == 0;
+    return with_dtype(dtype, [&](auto t) { return launch_logprobs<decltype(t)>(a, vec, static_cast<cudaStream_t>(stream)); });
 }
