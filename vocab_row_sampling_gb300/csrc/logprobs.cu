@@ -71,41 +71,40 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// The largest of eight elements (NaN left out), and how many exceed a value,
-// counted over a tile: 16-bit elements in pairs of 16-bit sums (whole numbers
-// of at most 4 per segment in each half).
+// The largest of eight elements (NaN left out), and how many exceed a value. 16-bit elements are compared in
+// pairs, whose results 0 or 0xFFFF in each half are added up as one number: with n_low and n_high of
+// them it is 65536 (n_low - n_high) - n_low modulo 2^32, and holds up to 65535 of each.
 template <typename T> struct Eight;
 template <> struct Eight<float> {
-    using Count = int;
     __device__ static float largest(const Raw8<float>& r) {
         float v[8];
         r.unpack(v);
         return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
     }
-    __device__ static Count zero() { return 0; }
-    __device__ static void count(const Raw8<float>& r, float own, Count& n) {
+    __device__ static void count(const Raw8<float>& r, float own, uint32_t& n) {
         float v[8];
         r.unpack(v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) n += v[e] > own;
+        for (int e = 0; e < 8; ++e) n += v[e] > own ? 1 : 0;
     }
-    __device__ static int total(Count n) { return n; }
+    __device__ static int total(uint32_t n) { return static_cast<int>(n); }
 };
 template <typename T, typename T2> struct EightHalves {
-    using Count = T2;
     __device__ static T2 pair(uint32_t w) { return *reinterpret_cast<const T2*>(&w); }
     __device__ static float largest(const Raw8<T>& r) {
         const T2 m = __hmax2(__hmax2(pair(r.w[0].x), pair(r.w[0].y)), __hmax2(pair(r.w[0].z), pair(r.w[0].w)));
         return fmaxf(to_f(m.x), to_f(m.y));
     }
-    __device__ static Count zero() { return pair(0); }
-    __device__ static void count(const Raw8<T>& r, T own, Count& n) {
+    __device__ static void count(const Raw8<T>& r, T own, uint32_t& n) {
         T2 o;
         o.x = o.y = own;
-        n = __hadd2(n, __hadd2(__hadd2(__hgt2(pair(r.w[0].x), o), __hgt2(pair(r.w[0].y), o)),
-                               __hadd2(__hgt2(pair(r.w[0].z), o), __hgt2(pair(r.w[0].w), o))));
+        n += __hgt2_mask(pair(r.w[0].x), o) + __hgt2_mask(pair(r.w[0].y), o);
+        n += __hgt2_mask(pair(r.w[0].z), o) + __hgt2_mask(pair(r.w[0].w), o);
     }
-    __device__ static int total(Count n) { return static_cast<int>(to_f(n.x) + to_f(n.y)); }
+    __device__ static int total(uint32_t n) {
+        const uint32_t low = -n & 0xFFFFu;
+        return static_cast<int>(low + (low - (n + low >> 16) & 0xFFFFu));
+    }
 };
 template <> struct Eight<__nv_bfloat16> : EightHalves<__nv_bfloat16, __nv_bfloat162> {};
 template <> struct Eight<__half> : EightHalves<__half, __half2> {};
@@ -121,11 +120,12 @@ template <> __device__ constexpr float largest_finite<__half>() { return 65504.0
 // kLeastExponent or below, finite. 16-bit elements are raised to it in pairs, before
 // they are taken apart, fp32 exponents one by one.
 template <typename T> struct Floor {
+    static constexpr bool kPaired = false;
     __device__ bool set(float) { return true; }
     __device__ __forceinline__ const Raw8<T>& raise(const Raw8<T>& r) const { return r; }
-    __device__ static __forceinline__ float raise(float t) { return max_nan(t, kLeastExponent); }
 };
 template <typename T, typename T2> struct FloorHalves {
+    static constexpr bool kPaired = true;
     T2 least;
     // false: below the type's range
     __device__ __forceinline__ bool set(float v) {
@@ -141,7 +141,6 @@ template <typename T, typename T2> struct FloorHalves {
         const T2 v = __hmax2_nan(*reinterpret_cast<const T2*>(&w), least);
         return *reinterpret_cast<const uint32_t*>(&v);
     }
-    __device__ static __forceinline__ float raise(float t) { return t; }
 };
 template <> struct Floor<__nv_bfloat16> : FloorHalves<__nv_bfloat16, __nv_bfloat162> {};
 template <> struct Floor<__half> : FloorHalves<__half, __half2> {};
@@ -206,11 +205,20 @@ __device__ __forceinline__ int place_of(uint64_t key) { return static_cast<int>(
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
+// Two words, half a block apart.
+__device__ __forceinline__ void copy_halves(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n\tcp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;" ::"r"(to),
+                 "l"(from), "n"(kBlockBytes / 2)
+                 : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int n> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory"); }
-__device__ __forceinline__ uint4 load_shared16(uint32_t from) {
+template <int offset> __device__ __forceinline__ uint4 load_shared16(uint32_t from) {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(from), "n"(offset)
+                 : "memory");
     return v;
 }
 __device__ __forceinline__ void store_shared16(uint32_t to, uint4 v) {
@@ -234,8 +242,7 @@ template <typename T, int kStep> struct Ring {
     }
     __device__ __forceinline__ void fetch(uint32_t to) {
         if (left > 0) {
-            copy16(base + to, from);
-            copy16(base + to + kBlockBytes / 2, from + kBlockBytes / 2);
+            copy_halves(base + to, from);
             from += kStep * kBlockBytes;
             --left;
         }
@@ -248,8 +255,8 @@ template <typename T, int kStep> struct Ring {
     }
     __device__ __forceinline__ void take(uint4 (&w)[2]) {
         copies_wait<kDepth - 1>();
-        w[0] = load_shared16(base + slot);
-        w[1] = load_shared16(base + slot + kBlockBytes / 2);
+        w[0] = load_shared16<0>(base + slot);
+        w[1] = load_shared16<kBlockBytes / 2>(base + slot);
     }
     __device__ __forceinline__ void fetch_next() {
         fetch(slot);
@@ -640,11 +647,15 @@ template <typename T, bool kCareful> struct RunningSums {
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 const uint64_t x = pack2(v[e], v[e + 1]);
+                uint64_t t = kCareful ? mul2(sub2(x, base2), c2) : fma2(x, c2, base2);
                 float t0, t1;
-                unpack2(kCareful ? mul2(sub2(x, base2), c2) : fma2(x, c2, base2), t0, t1);
-                t0 = kCareful ? max_nan(t0, kLeastExponent) : Floor<T>::raise(t0);
-                t1 = kCareful ? max_nan(t1, kLeastExponent) : Floor<T>::raise(t1);
-                const uint64_t q = pack2(ex2_flushed(t0), ex2_flushed(t1)), t = pack2(t0, t1);
+                unpack2(t, t0, t1);
+                if constexpr (kCareful || !Floor<T>::kPaired) {
+                    t0 = max_nan(t0, kLeastExponent);
+                    t1 = max_nan(t1, kLeastExponent);
+                    t = pack2(t0, t1);
+                }
+                const uint64_t q = pack2(ex2_flushed(t0), ex2_flushed(t1));
                 part = p + e == 0 ? q : add2(part, q);
                 weight = p + e == 0 ? mul2(q, t) : fma2(q, t, weight);
             }
@@ -670,7 +681,7 @@ template <typename T, bool kTop, bool kCareful> struct RowReader {
     float c, own_value;
     T own;
     float* segment;
-    int above = 0;
+    uint32_t above = 0;
 
     __device__ __forceinline__ RowReader(float c, T own, float* segment)
         : sums(c), c(c), own_value(to_f(own)), own(own), segment(segment) {}
@@ -685,16 +696,19 @@ template <typename T, bool kTop, bool kCareful> struct RowReader {
             most = fmaxf(most, largest);
         }
         sums.top = fmaxf(sums.top, most);
-        if (most > sums.bound && !sums.move(c)) return false;
+        if (most > sums.bound) {  // seldom: the barrier keeps it a branch
+            __syncwarp();
+            if (!sums.move(c)) return false;
+        }
         sums.add(raw, c);
         if (most > own_value) {
-            typename Eight<T>::Count exceed = Eight<T>::zero();
+            __syncwarp();
 #pragma unroll
-            for (int p = 0; p < kParts<T>; ++p) Eight<T>::count(raw[p], own, exceed);
-            above += Eight<T>::total(exceed);
+            for (int p = 0; p < kParts<T>; ++p) Eight<T>::count(raw[p], own, above);
         }
         return true;
     }
+    __device__ __forceinline__ Sums value() const { return sums.value(c, Eight<T>::total(above)); }
 };
 
 // ------------------------------------------------------------- the row's results
@@ -735,7 +749,7 @@ __device__ __noinline__ Sums careful_sums(const Task<T> task, int first, int ste
         load_block(task.row, i, raw);
         reader.add(raw, i);
     }
-    return reader.sums.value(task.c, reader.above);
+    return reader.value();
 }
 
 // Adds the blocks among [first, end) of a row that reach over its ends to a warp's sums.
@@ -753,22 +767,37 @@ __device__ __forceinline__ void add_edges(const Task<T>& task, int first, int en
     }
 }
 
-// The warp's blocks first, first + kStep, ... (count of them), which come through the ring.
+// The warp's blocks first, first + kStep, ... (count of them), which come through the ring; before the last kDepth
+// of them all have been fetched, and `go_on` may point it at the next row's.
 template <bool kTop, typename T, int kStep, typename F>
-__device__ __forceinline__ Sums ring_sums(Ring<T, kStep>& ring, const Task<T>& task, int first, int count, float* segment, F all_fetched) {
+__device__ __forceinline__ Sums ring_sums(Ring<T, kStep>& ring, const Task<T>& task, int first, int count, float* segment, F go_on) {
     RowReader<T, kTop, false> reader(task.c, task.own, segment);
     bool fine = true;
-    for (int n = 0, i = first; n < count; ++n, i += kStep) {
+    int n = 0;
+    for (int end = max(count - kDepth, 0);; end = count) {
+        for (; n < end; ++n) {
+            uint4 w[2];
+            Raw8<T> raw[kParts<T>];
+            ring.take(w);
+            segments_of(w, raw);
+            if (!reader.add(raw, first + n * kStep)) {
+                fine = false;
+                break;
+            }
+            ring.fetch_next();
+        }
+        if (!fine || end == count) break;
+        go_on(ring);
+    }
+    if (fine) return reader.value();
+    for (;; ++n) {  // what is on its way, and the fetches ahead
+        if (n == count) break;
+        if (n == max(count - kDepth, 0)) go_on(ring);
         uint4 w[2];
-        Raw8<T> raw[kParts<T>];
         ring.take(w);
-        segments_of(w, raw);
-        if (fine) fine = reader.add(raw, i);
-        if (ring.left == 0) all_fetched(ring);
         ring.fetch_next();
     }
-    return fine ? reader.sums.value(task.c, reader.above)
-                : careful_sums<T, kTop>(task, first, kStep, first + (count - 1) * kStep + 1, segment);
+    return careful_sums<T, kTop>(task, first, kStep, first + (count - 1) * kStep + 1, segment);
 }
 
 // How many of the numbers first, first + step, ... lie below end.
@@ -848,9 +877,8 @@ __global__ void __launch_bounds__(kWarps * 32, kResident / kWarps) logprob_kerne
                 ring.fill();
             }
             fetched = false;
-            const bool go_on = next_id >= 0 && count >= kDepth;
             Sums sums = ring_sums<kTop>(ring, task, first, count, segment, [&](Ring<T, kWarps>& g) {
-                if (go_on && !fetched) {
+                if (next_id >= 0 && count >= kDepth) {
                     g.point_at(next.row, next_first, next_count);
                     fetched = true;
                 }
