@@ -24,7 +24,7 @@
 namespace drs {
 namespace {
 
-constexpr int kResident = 32;  // warps per SM
+constexpr int kResident = 24;  // warps per SM
 constexpr int kMaxRowCluster = 16;
 constexpr int kListed = 256;  // candidates of the short way
 constexpr int kSegment = 256;         // columns whose largest is kept: eight per lane of a warp
@@ -979,9 +979,9 @@ template <typename T> drs_status launch_logprobs(LogprobParams a, bool vec, cuda
     a.blocks = static_cast<int32_t>(ceil_div(a.vocab + (vec ? 0 : 16 / sizeof(T) - 1), kBlock<T>));
     const int segments = a.blocks * kParts<T>;
     int cluster = 1, warps = 8;
-    while (cluster < kMaxRowCluster && a.vocab > 8192 * cluster &&
-           a.rows * cluster * 2 <= int64_t{sms} * 4 - (cluster < 8 ? sms / 2 : sms * 3 / 2))
-        cluster *= 2;
+    while (cluster < kMaxRowCluster && a.vocab > 8192 * cluster && a.rows * cluster * 2 <= 2 * sms) cluster *= 2;
+    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T)), most = sizeof(T) == 2 ? 128 * 1024 : 64 * 1024;
+    while (warps > 1 && a.rows * warps > int64_t{sms} * kResident && bytes * 2 <= most * warps) warps /= 2;
     if (getenv("LPC")) cluster = atoi(getenv("LPC"));
     if (getenv("LPT")) warps = atoi(getenv("LPT"));
     if (cluster > 1) warps = 8;
