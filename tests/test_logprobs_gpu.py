@@ -37,6 +37,31 @@ def test_kinds_of_rows(dtype, kind, rows, vocab, k):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("kind", ["plain", "ties", "equal", "masked", "rising"])
+@pytest.mark.parametrize("rows", [5, 40, 300, 470, 700, 1000, 2300, 3700])
+def test_numbers_of_rows(dtype, kind, rows):
+    """Rows by clusters and by teams of 8, 4, 2 and 1 warps, several in turn, rows that are passed over among them."""
+    for vocab, k, pad in ((1500, 20, 1), (13000, 64, 0)) if rows < 1500 else ((1500, 64, 0), (5003, 20, 1)):
+        logits, ids = logits_of(kind, rows, vocab, TYPES[dtype], rows, pad), ids_of(rows, vocab, rows)
+        if rows == 700:
+            ids[:650] = -1
+        check_logprobs(drs().token_logprobs(logits, ids, k), logits, ids, k)
+
+
+@pytest.mark.parametrize("temp", [400.0, 1e4, 1e30, 3e38])
+def test_large_temperatures_under_masks(temp):
+    """The floor of the exponents leaves the type's range; whole parts of the rows are -inf."""
+    temps = torch.tensor([temp], device="cuda")
+    for dtype in TYPES.values():
+        for rows, vocab in ((6, 30000), (400, 9000)):
+            logits, ids = logits_of("plain", rows, vocab, dtype, 1), ids_of(rows, vocab, 1)
+            logits[:, : vocab * 3 // 4] = -INF
+            logits[1] = -INF
+            out = drs().token_logprobs(logits, ids, 8, temps, rows)
+            check_logprobs(out, logits, ids, 8, temps, rows)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("vocab", [520, 4100, 50001])
 @pytest.mark.parametrize("pad,offset", [(1, 0), (0, 1), (8, 8), (3, 5), (24, 0), (7, 3)])
 def test_strides_and_offsets(dtype, vocab, pad, offset):

@@ -10,14 +10,25 @@
 // passes it by more than 2^8 in the exponent; S and W then move along:
 // S' = 2^d S, W' = 2^d (W + d S) with d = (M - M') c.
 //
-// One read of the row. Warps take segments of 256 or 512 columns and keep each
-// segment's largest logit in shared memory. The k largest logits lie in the k
-// segments whose largest logits come first (by value, then by column): any
-// logit of another segment has k before it, one in each of these. So only k
-// segments are looked at again, from L2, and of these only what reaches the
-// k-th segment's largest.
+// One read of the row. Warps take blocks of two (fp32: one) segments of 256
+// columns and keep each segment's largest logit in shared memory. The k
+// largest logits lie in the k segments whose largest logits come first (by
+// value, then by column): any logit of another segment has k before it, one in
+// each of these. So only k segments are looked at again, from L2, and of these
+// only what reaches the k-th segment's largest.
+//
+// Many rows: a team of 1 to 8 warps, a CTA, takes rows in turn; its next blocks,
+// the next row's among them, come by asynchronous copies while it computes.
+// Few rows: a cluster of up to 16 CTAs takes a row and its first CTA selects.
+//
+// Bound by memory for large batches, by instructions close behind: 16-bit rows
+// take about 6.5 issued per column and lane (an exponential, a product and three sums
+// each) and 24 warps of 80 registers per SM hide more than 32 of 64 (4096 x
+// 262144 bf16 rows with 20 alternatives 339 us against 371; without
+// alternatives 6.8 TB/s). Measured: those 339 us, 6.2 TB/s; 256 x 262144 fp32 47 us,
+// 5.7 TB/s; 1003 x 50001 fp16 with 5 alternatives 28 us; one row of 262144 bf16 7.0
+// us with 20 alternatives, 4.0 without: launch, the read's latency, a cluster's barrier.
 #include <climits>
-#include <cstdlib>
 
 #include "token_common.cuh"
 
@@ -26,15 +37,19 @@ namespace {
 
 constexpr int kResident = 24;  // warps per SM
 constexpr int kMaxRowCluster = 16;
-constexpr int kListed = 256;  // candidates of the short way
-constexpr int kSegment = 256;         // columns whose largest is kept: eight per lane of a warp
-constexpr int kBlockBytes = 1024;     // what a warp takes at once: two 16-byte words per lane
-constexpr int kDepth = 4;             // blocks on their way to a warp
-constexpr int kStageBytes = 2048;     // what a warp looks at again at once
+constexpr int kListed = 256;       // candidates of the short way
+constexpr int kSegment = 256;      // columns whose largest is kept: eight per lane of a warp
+constexpr int kBlockBytes = 1024;  // what a warp takes at once: two 16-byte words per lane
+// Blocks on their way to a warp. us for 2432 x 262144 bf16 rows without alternatives with 2, 3, 4 and 5 (32 warps per
+// SM): 211, 206, 199, 202; in registers instead of shared memory 234 with 2.
+constexpr int kDepth = 4;
 // Exponents (base 2) below this give 0; held there so that 0 times an
 // infinite exponent does not arise in W.
 constexpr float kLeastExponent = -200.0f;
 constexpr float kSlack = 8.0f;  // exponents above the reference before it moves
+
+// Bytes that a warp of a team looks at again at once: four segments, two of fp32 in small teams, whose memory counts.
+__host__ __device__ constexpr int stage_bytes(int warps, int element) { return element == 4 && warps >= 4 ? 4096 : 2048; }
 
 // Segments in a block, and its columns.
 template <typename T> constexpr int kParts = sizeof(T) == 2 ? 2 : 1;
@@ -273,7 +288,7 @@ template <typename T> __device__ __forceinline__ int place_in_segment(int lane, 
     return sizeof(T) == 2 ? lane * 8 + e : lane * 4 + e % 4 + e / 4 * 128;
 }
 
-// ------------------------------------------------------------- selection, by one warp
+// ------------------------------------------------------------- selection
 
 __device__ __forceinline__ float warp_min(float v) {
     float r;
@@ -296,8 +311,8 @@ struct Selection {
     uint8_t* words;
     uint32_t* stage;
 
-    __host__ __device__ static constexpr size_t bytes(int warps, int k) {
-        const size_t stage = size_t{kStageBytes} * warps, units = size_t{128} * k;
+    __host__ __device__ static constexpr size_t bytes(int warps, int k, int element) {
+        const size_t stage = static_cast<size_t>(stage_bytes(warps, element)) * warps, units = size_t{128} * k;
         return kListed * 8 + 2 * DRS_MAX_ALTERNATIVES * 4 + 16 + 128 * warps + (stage > units ? stage : units);
     }
     __device__ Selection(float* memory, int warps) {
@@ -486,10 +501,10 @@ __device__ __forceinline__ int select_top(const Row<T>& row, float* segment, int
     if (!slowly) {
         // Each warp has its share of the segments: their words that hold something to take, then these in turn
         // by a lane each.
-        constexpr int kBytes = kSegment * static_cast<int>(sizeof(T)), kAtOnce = kStageBytes / kBytes;
+        constexpr int kBytes = kSegment * static_cast<int>(sizeof(T)), kStage = stage_bytes(kWarps, sizeof(T)), kAtOnce = kStage / kBytes;
         constexpr int kHalves = sizeof(T) / 2;
         static_assert(kAtOnce * 32 <= 128, "words");
-        char* const stage = reinterpret_cast<char*>(s.stage) + warp * kStageBytes;
+        char* const stage = reinterpret_cast<char*>(s.stage) + warp * kStage;
         uint8_t* const words = s.words + warp * 128;
         const uint32_t to = smem_u32(stage) + lane * 16;
         const auto word_at = [&](int segment_at, int lane_at) {
@@ -669,6 +684,7 @@ template <typename T, bool kCareful> struct RunningSums {
         float s0, s1, w0, w1;
         unpack2(sum, s0, s1);
         unpack2(weighted, w0, w1);
+        if (none) w0 = s0, w1 = s1;  // 0, or NaN: without a reference the floor may be -inf, which 0 is multiplied by
         const float d = distance(top, c), f = ex2_approx(d);
         return Sums{top, warp_sum(f * (s0 + s1)), warp_sum(f * fmaf(d, s0 + s1, w0 + w1)), warp_sum(above)};
     }
@@ -843,11 +859,11 @@ __device__ __forceinline__ void finish(const LogprobParams& a, int64_t r, const 
 
 // Dynamic shared memory: the warps' rings, a selection's (kTop), the segments' largest (kTop).
 constexpr size_t kRingBytes = kDepth * kBlockBytes;
-__host__ __device__ constexpr size_t shared_before(int warps, int k) {
-    return warps * kRingBytes + (k > 0 ? Selection::bytes(warps, k) : 0);
+__host__ __device__ constexpr size_t shared_before(int warps, int k, int element) {
+    return warps * kRingBytes + (k > 0 ? Selection::bytes(warps, k, element) : 0);
 }
-__host__ __device__ constexpr size_t shared_bytes(int warps, int k, int segments) {
-    return shared_before(warps, k) + (k > 0 ? static_cast<size_t>(segments + 127) / 128 * 512 : 0);
+__host__ __device__ constexpr size_t shared_bytes(int warps, int k, int element, int segments) {
+    return shared_before(warps, k, element) + (k > 0 ? static_cast<size_t>(segments + 127) / 128 * 512 : 0);
 }
 
 // ------------------------------------------------------------- many rows
@@ -859,12 +875,18 @@ __global__ void __launch_bounds__(kWarps * 32, kResident / kWarps) logprob_kerne
     __shared__ Sums s_warp[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const Selection select(s_memory + kWarps * kRingBytes / 4, kWarps);
-    float* const segment = s_memory + shared_before(kWarps, kTop ? a.k : 0) / 4;
+    float* const segment = s_memory + shared_before(kWarps, kTop ? a.k : 0, sizeof(T)) / 4;
     const int rows = static_cast<int>(a.rows), step = static_cast<int>(gridDim.x);
     Ring<T, kWarps> ring(s_memory);
+    bool fetched = true;  // the row's first blocks are on their way: here before its token is known
+    {
+        const Row<T> row(static_cast<const T*>(a.logits) + blockIdx.x * a.row_stride, a.vocab);
+        const int first = row.whole_first() + warp;
+        ring.point_at(row, first, steps_below(first, kWarps, row.whole_end()));
+        ring.fill();
+    }
     int id = id_of(a, blockIdx.x), next_id = rows - static_cast<int>(blockIdx.x) > step ? id_of(a, blockIdx.x + step) : -1;
     Task<T> task(a, blockIdx.x, id);
-    bool fetched = false;  // the row's first blocks are on their way
     for (int r = blockIdx.x; r < rows; r += step) {
         const Task<T> next(a, rows - r > step ? r + step : r, next_id);  // its loads come back while this row is read
         const int next_next_id = rows - r > 2 * step ? id_of(a, r + 2 * step) : -1;
@@ -877,13 +899,16 @@ __global__ void __launch_bounds__(kWarps * 32, kResident / kWarps) logprob_kerne
                 ring.fill();
             }
             fetched = false;
+            // what reaches over the row's ends, while the first blocks are on their way
+            Sums edges{-INFINITY, 0.0f, 0.0f, 0};
+            if (warp == kWarps - 1) add_edges<kTop>(task, 0, task.row.blocks(), segment, edges);
             Sums sums = ring_sums<kTop>(ring, task, first, count, segment, [&](Ring<T, kWarps>& g) {
                 if (next_id >= 0 && count >= kDepth) {
                     g.point_at(next.row, next_first, next_count);
                     fetched = true;
                 }
             });
-            if (warp == kWarps - 1) add_edges<kTop>(task, 0, task.row.blocks(), segment, sums);
+            if (warp == kWarps - 1) sums = together(lane == 0 ? sums : edges, lane < 2, task.c);
             if constexpr (kWarps > 1) {
                 if (lane == 0) s_warp[warp] = sums;
                 if (kTop && threadIdx.x == 0) select.counts[0] = select.counts[1] = 0;
@@ -897,6 +922,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident / kWarps) logprob_kerne
             team_sync<kWarps>();
         } else {
             if (warp == 0) pass_over<kTop>(a, r);
+            copies_wait<0>();
             fetched = false;
         }
         id = next_id;
@@ -917,7 +943,7 @@ __global__ void __launch_bounds__(256, kResident / 8) logprob_cluster_kernel(con
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = static_cast<int>(cluster_rank());
     const Selection select(s_memory + kWarps * kRingBytes / 4, kWarps);
-    float* const segment = s_memory + shared_before(kWarps, kTop ? a.k : 0) / 4;
+    float* const segment = s_memory + shared_before(kWarps, kTop ? a.k : 0, sizeof(T)) / 4;
     const int r = static_cast<int>(blockIdx.x / a.cluster);
     cluster_arrive();
     // the first blocks are on their way before the token is known
@@ -935,8 +961,10 @@ __global__ void __launch_bounds__(256, kResident / 8) logprob_cluster_kernel(con
         return;
     }
     const Task<T> task(a, r, id);
+    Sums edges{-INFINITY, 0.0f, 0.0f, 0};
+    if (warp == kWarps - 1) add_edges<kTop>(task, first, end, segment, edges);
     Sums sums = ring_sums<kTop>(ring, task, at, count, segment, [](Ring<T, kWarps>&) {});
-    if (warp == kWarps - 1) add_edges<kTop>(task, first, end, segment, sums);
+    if (warp == kWarps - 1) sums = together(lane == 0 ? sums : edges, lane < 2, task.c);
     if (lane == 0) s_warp[warp] = sums;
     if (kTop && tid == 0) select.counts[0] = select.counts[1] = 0;
     __syncthreads();
@@ -978,17 +1006,24 @@ template <typename T> drs_status launch_logprobs(LogprobParams a, bool vec, cuda
     if (sms <= 0) return DRS_ERR_CUDA;
     a.blocks = static_cast<int32_t>(ceil_div(a.vocab + (vec ? 0 : 16 / sizeof(T) - 1), kBlock<T>));
     const int segments = a.blocks * kParts<T>;
+    // CTAs per row: up to two per SM in all, 8192 columns each at least. us with one, 2, 4, 8 and 16 (20
+    // alternatives, bf16): 1 x 262144 19.9, 13.3, 9.8, 8.0, 7.2; 16 x 262144 21.6, 14.6, 11.0, 10.5, 11.1; 64 x
+    // 131072 14.3, 11.5, 11.2, 14.0, 18.7; 152 x 131072 15.0, 14.5, 19.4; 256 x 65536 13.8, 19.7.
     int cluster = 1, warps = 8;
     while (cluster < kMaxRowCluster && a.vocab > 8192 * cluster && a.rows * cluster * 2 <= 2 * sms) cluster *= 2;
-    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T)), most = sizeof(T) == 2 ? 128 * 1024 : 64 * 1024;
-    while (warps > 1 && a.rows * warps > int64_t{sms} * kResident && bytes * 2 <= most * warps) warps /= 2;
-    if (getenv("LPC")) cluster = atoi(getenv("LPC"));
-    if (getenv("LPT")) warps = atoi(getenv("LPT"));
+    // Warps per row: as many as leave every row a team at once, unless that is more than 64 KB of a row per warp
+    // (128 KB of 16-bit rows when there are many). us with 8, 4, 2 and 1: 300 x 65536 bf16 14.2, 16.1, 21.3, 43.5;
+    // 600 x 65536 26.5, 21.6, 24.7, 42.8; 1003 x 50001 fp16 36.2, 32.5, 30.2, 39.2; 4096 x 8192 bf16 66.9, 47.5, 39.8,
+    // 33.9; 1024 x 262144 bf16 91.5, 99.2, 107.3, 161.9; 4096 x 262144 350, 343, 358, 430; 2048 x 131072 fp32 166, 170,
+    // 201, 180.
+    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T)), resident = int64_t{sms} * kResident;
+    const int64_t share = sizeof(T) == 2 && a.rows * 2 > resident ? 128 * 1024 : 64 * 1024;  // of a warp, at most
+    while (warps > 1 && a.rows * warps > resident && bytes * 2 <= share * warps) warps /= 2;
     if (cluster > 1) warps = 8;
     a.cluster = cluster;
     a.part = static_cast<int32_t>(ceil_div(a.blocks, cluster));
     const bool top = a.k > 0;
-    const size_t smem = shared_bytes(warps, a.k, segments);
+    const size_t smem = shared_bytes(warps, a.k, sizeof(T), segments);
     const int per_sm = static_cast<int>(kSmemPerSm / (smem + kSmemReserved + 512));
     const int64_t teams = int64_t{sms} * (per_sm < kResident / warps ? per_sm : kResident / warps);
     const LogprobKernel kernel =
