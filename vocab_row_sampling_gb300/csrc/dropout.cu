@@ -3,15 +3,24 @@
 //
 // The mask is a function of (seed, global row, column): 16 bits of
 // Philox4x32-10 per element, eight elements to a counter. It is never stored;
-// the gradient computes it again.
+// the gradient computes it again. 32 bits per element would take twice the
+// rounds: about 15 integer instructions per element, which at 4 bytes moved per element
+// is all that the SMs issue at the memory's rate; 16 bits leave q at multiples of
+// 2^-16, and the scale is that of the rounded q.
+//
+// Bound by memory: x and the residual are read once, out is written once. Measured:
+// 65536 x 4096 bf16 with a residual 224 us, 7.2 TB/s; 32768 x 4096 bf16 79 us, 6.8
+// TB/s; 256 x 2048 2.1 us, the launch. Rows off 16-byte boundaries issue about
+// 25 instructions per column and are bound by them: 30000 x 4095 122 us, 6.1 TB/s.
 #include <cmath>
+#include <type_traits>
 
 #include "token_common.cuh"
 
 namespace drs {
 namespace {
 
-constexpr int kDropoutThreads = 128;
+constexpr int kDropoutThreads = 128;  // 65536 x 4096: 223 us with 64, 224 with 128, 223 with 256
 // The counter's second word, which is 0 in the sampler's noise: the two draw
 // different numbers from one seed.
 constexpr uint32_t kDropoutTag = 0x64726F70u;
@@ -34,29 +43,18 @@ __device__ __forceinline__ PhiloxKey dropout_key(const DropoutParams& a) {
 }
 
 // The eight elements' 16-bit numbers, two to a word, the lower half first, for
-// n rows in step: they share the rounds' keys.
-template <int n> __device__ __forceinline__ void dropout_words(PhiloxKey key, const uint64_t (&row)[n], uint32_t group,
-                                                               uint4 (&w)[n]) {
+// n counters in step: they share the rounds' keys.
+template <int n>
+__device__ __forceinline__ void dropout_words(PhiloxKey key, const uint64_t (&row)[n], const uint32_t (&group)[n], uint4 (&w)[n]) {
 #pragma unroll
     for (int i = 0; i < n; ++i)
-        w[i] = make_uint4(group, kDropoutTag, static_cast<uint32_t>(row[i]), static_cast<uint32_t>(row[i] >> 32));
+        w[i] = make_uint4(group[i], kDropoutTag, static_cast<uint32_t>(row[i]), static_cast<uint32_t>(row[i] >> 32));
 #pragma unroll
     for (int round = 0; round < 10; ++round) {
 #pragma unroll
         for (int i = 0; i < n; ++i) w[i] = philox_round(w[i], key);
         key = philox_next(key);
     }
-}
-
-// The bits of the kept among eight elements.
-__device__ __forceinline__ uint32_t kept_bits(const uint4& w, uint32_t limit) {
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t u = word_of(w, i);
-        bits |= (u << 16 >= limit ? 1u : 0u) << (2 * i) | (u >= limit ? 1u : 0u) << (2 * i + 1);
-    }
-    return bits;
 }
 
 // v = residual + kept ? v scale : 0, in fp32.
@@ -85,9 +83,11 @@ __global__ void __launch_bounds__(kDropoutThreads) dropout_kernel(const DropoutP
     Raw8<X> x[kRows];
     Raw8<Y> residual[kResidual ? kRows : 1];
     uint64_t row[kRows];
+    uint32_t groups[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int64_t r = r0 + i * static_cast<int64_t>(blockDim.y);
+        groups[i] = static_cast<uint32_t>(group);
         row[i] = static_cast<uint64_t>(a.row0 + r);
         x[i] = Raw8<X>{};
         if (r >= a.rows) continue;
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kDropoutThreads) dropout_kernel(const DropoutP
             residual[i].load(static_cast<const Y*>(a.residual) + r * a.residual_stride + group * 8);
     }
     uint4 w[kRows];
-    dropout_words(dropout_key(a), row, static_cast<uint32_t>(group), w);
+    dropout_words(dropout_key(a), row, groups, w);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int64_t r = r0 + i * static_cast<int64_t>(blockDim.y);
@@ -109,90 +109,121 @@ __global__ void __launch_bounds__(kDropoutThreads) dropout_kernel(const DropoutP
     }
 }
 
-// Other rows. A lane has the mask of eight columns from a multiple of 8 on, and
-// writes eight from a 16-byte boundary of its row of `out` on: these reach into the
-// next lane's mask. A group of `lanes` lanes (a power of two, 8 to 32) has lanes - 1
-// such units of a row; the one behind the last whole unit is written
-// element by element, like the columns before the first.
-template <typename X, typename Y, bool kResidual>
-__global__ void __launch_bounds__(kDropoutThreads) dropout_odd_kernel(const DropoutParams a, int lanes) {
-    constexpr int kRows = 2;
-    const int lane = threadIdx.x & (lanes - 1);
-    const int64_t line = static_cast<int64_t>(blockIdx.x) * (kDropoutThreads / lanes) + threadIdx.x / lanes;
-    const int64_t r0 = line / a.columns * kRows;
-    const int unit = static_cast<int>(line % a.columns) * (lanes - 1) + lane;
-    const bool writes = lane < lanes - 1;
-    Any8<X> x[kRows];
-    Any8<Y> residual[kResidual ? kRows : 1];
-    uint64_t row[kRows];
-    int head[kRows], left[kRows];  // columns before the first unit; columns from this unit's first to the row's end
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int64_t r = r0 + i;
-        row[i] = static_cast<uint64_t>(a.row0 + r);
-        const Y* const out = static_cast<const Y*>(a.out) + r * a.out_stride;
-        head[i] = min(static_cast<int>((-reinterpret_cast<uintptr_t>(out) & 15) / sizeof(Y)), a.width);
-        left[i] = r < a.rows && writes ? a.width - head[i] - unit * 8 : 0;
-        if (left[i] < 8) continue;
-        const int col = a.width - left[i];
-        if (a.x) x[i].load(static_cast<const X*>(a.x) + r * a.x_stride, col, a.width);
-        else x[i] = Any8<X>{};
-        if constexpr (kResidual)
-            residual[i].load(static_cast<const Y*>(a.residual) + r * a.residual_stride, col, a.width);
-    }
-    uint4 w[kRows];
-    dropout_words(dropout_key(a), row, static_cast<uint32_t>(unit), w);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int64_t r = r0 + i;
-        uint32_t bits = kept_bits(w[i], a.limit);
-        const uint32_t own = bits;
-        bits = (bits | __shfl_down_sync(0xffffffffu, bits, 1, lanes) << 8) >> head[i];
-        const X* const from = static_cast<const X*>(a.x) + r * a.x_stride;
-        const Y* const add = static_cast<const Y*>(a.residual) + r * a.residual_stride;
+// Columns before the first 16-byte boundary of a row of `out`.
+template <typename Y> __device__ __forceinline__ int columns_before(const Y* out, int width) {
+    return min(static_cast<int>((-reinterpret_cast<uintptr_t>(out) & 15) / sizeof(Y)), width);
+}
+
+// Other rows. A lane has the numbers of sixteen columns from a multiple of 16
+// on, and writes sixteen from a 16-byte boundary of its row of `out` on, as two
+// eights: their numbers are put together from its own and the next lane's. A
+// group of `lanes` lanes (a power of two, 8 to 32) has lanes - 1 such units of a
+// row. The columns before the first unit and behind the last whole eight, 14 at
+// most, are written one by one by CTAs of their own behind the others.
+// kAlike: the rows of all arrays lie alike within 16-byte words (such as
+// contiguous ones of one type and odd width), so that a word of one meets a word
+// of each other; else the words of x and residual are put together.
+template <typename X, typename Y, bool kResidual, bool kAlike>
+__global__ void __launch_bounds__(kDropoutThreads) dropout_odd_kernel(const DropoutParams a, int lanes, unsigned unit_blocks) {
+    if (blockIdx.x >= unit_blocks) {
+        const int64_t r = static_cast<int64_t>(blockIdx.x - unit_blocks) * (kDropoutThreads / 16) + threadIdx.x / 16;
+        if (r >= a.rows) return;
+        const int e = threadIdx.x % 16;
         Y* const out = static_cast<Y*>(a.out) + r * a.out_stride;
-        const auto one = [&](int j, bool kept) {
-            const float rest = kResidual ? to_f(add[j]) : 0.0f;
-            out[j] = from_f<Y>(kept && a.x ? fmaf(to_f(from[j]), a.scale, rest) : rest);
-        };
-        if (left[i] >= 8) {
-            float v[8], rest[8];
-            x[i].unpack(v);
-            if constexpr (kResidual) residual[i].unpack(rest);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float base = kResidual ? rest[e] : 0.0f;
-                v[e] = bits >> e & 1 ? (kResidual ? fmaf(v[e], a.scale, base) : v[e] * a.scale) : base;
-            }
-            store8_stream(out + (a.width - left[i]), v);
-        } else {
-            for (int e = 0; e < left[i]; ++e) one(a.width - left[i] + e, bits >> e & 1);
-        }
-        if (unit == 0 && r < a.rows)
-            for (int j = 0; j < head[i]; ++j) one(j, own >> j & 1);
+        const int head = columns_before(out, a.width), tail = head + (a.width - head) / 8 * 8;
+        const int col = e < 8 ? e : tail + e - 8;
+        if (e < 8 ? e >= head : col >= a.width) return;
+        const float x = a.x ? to_f((static_cast<const X*>(a.x) + r * a.x_stride)[col]) : 0.0f;
+        const float base = kResidual ? to_f((static_cast<const Y*>(a.residual) + r * a.residual_stride)[col]) : 0.0f;
+        const uint64_t row[1] = {static_cast<uint64_t>(a.row0 + r)};
+        const uint32_t group[1] = {static_cast<uint32_t>(col / 8)};
+        uint4 w[1];
+        dropout_words(dropout_key(a), row, group, w);
+        const uint32_t u = word_of(w[0], col % 8 / 2);
+        out[col] = from_f<Y>((col % 2 ? u : u << 16) >= a.limit ? fmaf(x, a.scale, base) : base);
+        return;
     }
+    const int lane = threadIdx.x & (lanes - 1);
+    const int64_t r = static_cast<int64_t>(blockIdx.x / a.columns) * (kDropoutThreads / lanes) + threadIdx.x / lanes;
+    const int unit = static_cast<int>(blockIdx.x % a.columns) * (lanes - 1) + lane;
+    Y* const out = static_cast<Y*>(a.out) + r * a.out_stride;
+    const int head = columns_before(out, a.width), col = head + unit * 16;
+    const bool writes = r < a.rows && lane < lanes - 1;
+    using Words = std::conditional_t<kAlike, Raw8<X>, Any8<X>>;
+    using ResidualWords = std::conditional_t<kAlike, Raw8<Y>, Any8<Y>>;
+    Words x[2];
+    ResidualWords residual[kResidual ? 2 : 1];
+    const X* const from = static_cast<const X*>(a.x) + r * a.x_stride;
+    const Y* const rest = static_cast<const Y*>(a.residual) + r * a.residual_stride;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        x[h] = Words{};
+        if (!writes || col + 8 * h + 8 > a.width) continue;
+        if constexpr (kAlike) {
+            if (a.x) x[h].load(from + (col + 8 * h));
+            if constexpr (kResidual) residual[h].load(rest + (col + 8 * h));
+        } else {
+            if (a.x) x[h].load(from, col + 8 * h, a.width);
+            if constexpr (kResidual) residual[h].load(rest, col + 8 * h, a.width);
+        }
+    }
+    const uint64_t row[2] = {static_cast<uint64_t>(a.row0 + r), static_cast<uint64_t>(a.row0 + r)};
+    const uint32_t group[2] = {static_cast<uint32_t>(2 * unit), static_cast<uint32_t>(2 * unit + 1)};
+    uint4 w[2];
+    dropout_words(dropout_key(a), row, group, w);
+    const uint4 next = make_uint4(__shfl_down_sync(0xffffffffu, w[0].x, 1, lanes), __shfl_down_sync(0xffffffffu, w[0].y, 1, lanes),
+                                  __shfl_down_sync(0xffffffffu, w[0].z, 1, lanes), __shfl_down_sync(0xffffffffu, w[0].w, 1, lanes));
+    w[0] = joined(w[0], w[1], 2 * head);
+    w[1] = joined(w[1], next, 2 * head);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (!writes || col + 8 * h + 8 > a.width) continue;
+        float v[8], add[8];
+        x[h].unpack(v);
+        if constexpr (kResidual) residual[h].unpack(add);
+        dropped<kResidual>(v, add, w[h], a.limit, a.scale);
+        store8_stream(out + col + 8 * h, v);
+    }
+}
+
+template <typename X, typename Y, bool kResidual, int kRows> drs_status launch_rows(DropoutParams a, cudaStream_t stream) {
+    const int groups = a.width / 8;
+    a.columns = static_cast<int32_t>(ceil_div(groups, kDropoutThreads));
+    int x = static_cast<int>(ceil_div(groups, a.columns));
+    if (x > 32) x = (x + 31) / 32 * 32;
+    const dim3 block(x, kDropoutThreads / x);
+    const int64_t blocks = ceil_div(a.rows, block.y * kRows) * a.columns;
+    if (blocks > INT32_MAX) return DRS_ERR_UNSUPPORTED;
+    dropout_kernel<X, Y, kResidual, kRows><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
+    return cuda_status(cudaGetLastError());
 }
 
 template <typename X, typename Y, bool kResidual>
 drs_status launch_dropout(DropoutParams a, bool vec, cudaStream_t stream) {
     if (vec) {
-        constexpr int kRows = 4;
-        const int groups = a.width / 8;
-        a.columns = static_cast<int32_t>(ceil_div(groups, kDropoutThreads));
-        int x = static_cast<int>(ceil_div(groups, a.columns));
-        if (x > 32) x = (x + 31) / 32 * 32;
-        const dim3 block(x, kDropoutThreads / x);
-        const int64_t blocks = ceil_div(a.rows, block.y * kRows) * a.columns;
-        if (blocks > INT32_MAX) return DRS_ERR_UNSUPPORTED;
-        dropout_kernel<X, Y, kResidual, kRows><<<static_cast<unsigned>(blocks), block, 0, stream>>>(a);
-    } else {
-        const int units = a.width / 8 + 1;  // a partial one among them
-        const int lanes = units < 8 ? 8 : units < 16 ? 16 : 32;
-        a.columns = static_cast<int32_t>(ceil_div(units, lanes - 1));
-        const int64_t blocks = ceil_div(ceil_div(a.rows, 2) * a.columns, kDropoutThreads / lanes);
-        if (blocks > INT32_MAX) return DRS_ERR_UNSUPPORTED;
-        dropout_odd_kernel<X, Y, kResidual><<<static_cast<unsigned>(blocks), kDropoutThreads, 0, stream>>>(a, lanes);
+        // us with two and four rows per thread (bf16): 256 x 2048 2.1, 2.3; 1000 x 1024 2.5, 2.7; 2048 x 1024 4.0, 4.0;
+        // 32768 x 4096 84.2, 79.7.
+        const bool many = a.rows * (a.width / 8) > int64_t{1} << 18;
+        return many ? launch_rows<X, Y, kResidual, 4>(a, stream) : launch_rows<X, Y, kResidual, 2>(a, stream);
     }
+    const int units = (a.width / 8 + 1) / 2;
+    const int lanes = units < 8 ? 8 : units < 16 ? 16 : 32;
+    a.columns = static_cast<int32_t>(ceil_div(units, lanes - 1));
+    const int64_t unit_blocks = ceil_div(a.rows, kDropoutThreads / lanes) * a.columns;
+    const int64_t blocks = unit_blocks + ceil_div(a.rows, kDropoutThreads / 16);
+    if (blocks > INT32_MAX) return DRS_ERR_UNSUPPORTED;
+    // us for 30000 x 4095 and 5003 x 1283 16-bit elements with a residual: 122 and 9.3 where the arrays lie alike, 148
+    // and 10.7 by the words put together.
+    auto kernel = dropout_odd_kernel<X, Y, kResidual, false>;
+    if constexpr (std::is_same_v<X, Y>) {
+        const auto alike = [&](const void* p, int64_t stride) {
+            return (reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(a.out)) % 16 == 0 &&
+                   (stride - a.out_stride) * static_cast<int64_t>(sizeof(Y)) % 16 == 0;
+        };
+        if ((!a.x || alike(a.x, a.x_stride)) && (!kResidual || alike(a.residual, a.residual_stride)))
+            kernel = dropout_odd_kernel<X, Y, kResidual, true>;
+    }
+    kernel<<<static_cast<unsigned>(blocks), kDropoutThreads, 0, stream>>>(a, lanes, static_cast<unsigned>(unit_blocks));
     return cuda_status(cudaGetLastError());
 }
 
