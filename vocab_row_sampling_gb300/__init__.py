@@ -490,11 +490,39 @@ def drs_embed_tokens_grad(grad_out, ids, scale: float, accumulate: bool, grad_ta
     _check(st, "drs_embed_tokens_grad")
 
 
-def _temps(temps, rows: int, canvas_len: int, gpu: int):
+# The scoring operators and dropout check the same in fewer calls: their smallest
+# kernels take 2 us, and every question to a tensor 0.07 to 0.1.
+
+def _matrix(t, name: str, shape, gpu: int):
+    """(address, type's code, row stride) of a tensor of this 2-D shape with
+    unit column stride on this GPU."""
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        code = _dtype_code(t, name)
+    if t.shape != shape or t.get_device() != gpu or gpu < 0:
+        raise ValueError(f"{name}: {tuple(shape)} on {f'cuda:{gpu}' if gpu >= 0 else 'a CUDA device'} expected, got "
+                         f"{tuple(t.shape)} on {t.device}")
+    rows, columns = shape
+    step, unit = t.stride()
+    if unit != 1 and columns > 1 and rows > 0:
+        raise ValueError(f"{name}: unit column stride expected, got strides {t.stride()}")
+    return t.data_ptr(), code, step if rows > 1 and columns > 0 else max(step, columns)
+
+
+def _shape2(t, name: str):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: 2-D expected, got {tuple(shape)}")
+    return shape
+
+
+def _ids_and_temps(ids, temps, rows: int, canvas_len: int, gpu: int):
     import torch
+    bits = 64 if ids.dtype is torch.int64 else _id_bits(ids)
     if canvas_len < 1:
         raise ValueError(f"canvas_len: at least 1 expected, got {canvas_len}")
-    return None if temps is None else _vector(temps, "temps", torch.float32, -(-rows // canvas_len), gpu)
+    return (_vector(ids, "ids", ids.dtype, rows, gpu), bits,
+            None if temps is None else _vector(temps, "temps", torch.float32, -(-rows // canvas_len), gpu))
 
 
 def drs_token_logprobs(logits, ids, temps, canvas_len: int, out_logprob, out_entropy, out_rank, out_norm, out_ids,
@@ -504,27 +532,30 @@ def drs_token_logprobs(logits, ids, temps, canvas_len: int, out_logprob, out_ent
     out_norm may be None, out_ids and out_logprobs too (k = 0)."""
     import torch
     f32, i32 = torch.float32, torch.int32
-    _no_history(logits, out_logprob, "drs_token_logprobs", "the logits' gradient is token_logprobs_grad")
-    stride = _rows(logits, "logits")
-    gpu = logits.get_device()
-    rows, vocab = logits.shape
-    k = 0
-    if out_ids is not None:
+    if logits.requires_grad or out_logprob.requires_grad:
+        _no_history(logits, out_logprob, "drs_token_logprobs", "the logits' gradient is token_logprobs_grad")
+    shape, gpu = _shape2(logits, "logits"), logits.get_device()
+    rows, vocab = shape
+    ptr, code, stride = _matrix(logits, "logits", shape, gpu)
+    k, top_ids, top_logprobs = 0, None, None
+    if out_ids is not None and out_logprobs is not None:
         if out_ids.dim() != 2:
             raise ValueError(f"out_ids: [{rows}, k] expected, got {tuple(out_ids.shape)}")
         k = out_ids.shape[1]
-    if (out_ids is None) != (out_logprobs is None):
+        top_ids = _vector(out_ids, "out_ids", i32, rows * k, gpu)
+        top_logprobs = _vector(out_logprobs, "out_logprobs", f32, rows * k, gpu)
+    elif out_ids is not None or out_logprobs is not None:
         raise ValueError("out_ids and out_logprobs: both or neither expected")
+    ids_ptr, bits, temps_ptr = _ids_and_temps(ids, temps, rows, canvas_len, gpu)
     st = load().drs_token_logprobs(
-        logits.data_ptr(), _dtype_code(logits, "logits"), rows, vocab, stride,
-        _vector(ids, "ids", ids.dtype, rows, gpu), _id_bits(ids), _temps(temps, rows, canvas_len, gpu), canvas_len, k,
+        ptr, code, rows, vocab, stride, ids_ptr, bits, temps_ptr, canvas_len, k,
         _vector(out_logprob, "out_logprob", f32, rows, gpu),
         None if out_entropy is None else _vector(out_entropy, "out_entropy", f32, rows, gpu),
         None if out_rank is None else _vector(out_rank, "out_rank", i32, rows, gpu),
-        None if out_norm is None else _vector(out_norm, "out_norm", f32, 2 * rows, gpu),
-        None if out_ids is None else _vector(out_ids, "out_ids", i32, rows * k, gpu),
-        None if out_ids is None else _vector(out_logprobs, "out_logprobs", f32, rows * k, gpu), _raw_stream(stream, gpu))
-    _check(st, "drs_token_logprobs")
+        None if out_norm is None else _vector(out_norm, "out_norm", f32, 2 * rows, gpu), top_ids, top_logprobs,
+        _raw_stream(stream, gpu))
+    if st != DRS_OK:
+        _check(st, "drs_token_logprobs")
 
 
 def drs_token_logprobs_grad(logits, ids, temps, canvas_len: int, norm, entropy, grad_logprob, grad_entropy, grad,
@@ -534,70 +565,70 @@ def drs_token_logprobs_grad(logits, ids, temps, canvas_len: int, norm, entropy, 
     without grad_entropy too."""
     import torch
     f32 = torch.float32
-    _no_history(logits, grad, "drs_token_logprobs_grad", "there is no second derivative")
-    stride = _rows(logits, "logits")
-    gpu = logits.get_device()
-    grad_stride = _rows(grad, "grad", gpu)
-    rows, vocab = logits.shape
-    if grad.shape != logits.shape:
-        raise ValueError(f"grad: {(rows, vocab)} expected, got {tuple(grad.shape)}")
+    if logits.requires_grad or grad.requires_grad:
+        _no_history(logits, grad, "drs_token_logprobs_grad", "there is no second derivative")
+    shape, gpu = _shape2(logits, "logits"), logits.get_device()
+    rows, vocab = shape
+    ptr, code, stride = _matrix(logits, "logits", shape, gpu)
+    grad_ptr, grad_code, grad_stride = _matrix(grad, "grad", shape, gpu)
+    ids_ptr, bits, temps_ptr = _ids_and_temps(ids, temps, rows, canvas_len, gpu)
     st = load().drs_token_logprobs_grad(
-        logits.data_ptr(), _dtype_code(logits, "logits"), rows, vocab, stride,
-        _vector(ids, "ids", ids.dtype, rows, gpu), _id_bits(ids), _temps(temps, rows, canvas_len, gpu), canvas_len,
-        _vector(norm, "norm", f32, 2 * rows, gpu), None if entropy is None else _vector(entropy, "entropy", f32, rows, gpu),
+        ptr, code, rows, vocab, stride, ids_ptr, bits, temps_ptr, canvas_len, _vector(norm, "norm", f32, 2 * rows, gpu),
+        None if entropy is None else _vector(entropy, "entropy", f32, rows, gpu),
         None if grad_logprob is None else _vector(grad_logprob, "grad_logprob", f32, rows, gpu),
         None if grad_entropy is None else _vector(grad_entropy, "grad_entropy", f32, rows, gpu),
-        grad.data_ptr(), _dtype_code(grad, "grad"), grad_stride, _raw_stream(stream, gpu))
-    _check(st, "drs_token_logprobs_grad")
+        grad_ptr, grad_code, grad_stride, _raw_stream(stream, gpu))
+    if st != DRS_OK:
+        _check(st, "drs_token_logprobs_grad")
 
 
 def _seed(seed, gpu: int):
-    """(host seed, address of the device's): an int, or an int64 or uint64 tensor of one element on the GPU."""
+    """(host seed, address of the device's): a whole number, or an int64 or
+    uint64 tensor of one element on the GPU."""
     if isinstance(seed, int):
         return seed & (2**64 - 1), None
     import torch
-    if seed.dtype not in (torch.int64, torch.uint64):
-        raise ValueError(f"seed: an int or one int64 on the GPU expected, got {seed.dtype}")
-    return 0, _vector(seed, "seed", seed.dtype, 1, gpu)
+    dtype = getattr(seed, "dtype", None)
+    if dtype is not torch.int64 and dtype is not torch.uint64:
+        raise ValueError(f"seed: an int or one int64 on the GPU expected, got {type(seed).__name__} {dtype}")
+    return 0, _vector(seed, "seed", dtype, 1, gpu)
 
 
 def drs_dropout(x, residual, p: float, seed, row0: int, out, stream=None):
     """Launch drs_dropout: x and out [rows, width], residual None or of out's
     type and shape; seed an int or an int64 tensor of one element on the GPU."""
-    _no_history(x, out, "drs_dropout", "the gradient is dropout_grad")
-    gpu = x.get_device()
-    x_stride, out_stride = _rows(x, "x"), _rows(out, "out", gpu)
-    rows, width = x.shape
-    if out.shape != x.shape:
-        raise ValueError(f"out: {(rows, width)} expected, got {tuple(out.shape)}")
+    if x.requires_grad or out.requires_grad:
+        _no_history(x, out, "drs_dropout", "the gradient is dropout_grad")
+    shape, gpu = _shape2(x, "x"), x.get_device()
+    x_ptr, x_code, x_stride = _matrix(x, "x", shape, gpu)
+    out_ptr, out_code, out_stride = _matrix(out, "out", shape, gpu)
     residual_ptr, residual_stride = None, 0
     if residual is not None:
-        _no_history(residual, out, "drs_dropout", "the residual's gradient is the output's")
-        residual_ptr, residual_stride = residual.data_ptr(), _rows(residual, "residual", gpu)
-        if residual.dtype is not out.dtype or residual.shape != out.shape:
-            raise ValueError(f"residual: {out.dtype} {(rows, width)} expected, got {residual.dtype} "
-                             f"{tuple(residual.shape)}")
+        if residual.requires_grad:
+            _no_history(residual, out, "drs_dropout", "the residual's gradient is the output's")
+        residual_ptr, residual_code, residual_stride = _matrix(residual, "residual", shape, gpu)
+        if residual_code != out_code:
+            raise ValueError(f"residual: {out.dtype} expected, got {residual.dtype}")
     key, device_key = _seed(seed, gpu)
-    st = load().drs_dropout(x.data_ptr(), _dtype_code(x, "x"), rows, width, x_stride, residual_ptr, residual_stride, p,
-                            key, device_key, row0, out.data_ptr(), _dtype_code(out, "out"), out_stride,
-                            _raw_stream(stream, gpu))
-    _check(st, "drs_dropout")
+    st = load().drs_dropout(x_ptr, x_code, shape[0], shape[1], x_stride, residual_ptr, residual_stride, p, key, device_key,
+                            row0, out_ptr, out_code, out_stride, _raw_stream(stream, gpu))
+    if st != DRS_OK:
+        _check(st, "drs_dropout")
 
 
 def drs_dropout_grad(grad_out, p: float, seed, row0: int, grad_x, stream=None):
     """Launch drs_dropout_grad: grad_out and grad_x [rows, width] (each fp32,
     bf16 or fp16); seed as drs_dropout."""
-    _no_history(grad_out, grad_x, "drs_dropout_grad", "the gradient of a gradient is dropout_grad again")
-    gpu = grad_out.get_device()
-    grad_stride, x_stride = _rows(grad_out, "grad_out"), _rows(grad_x, "grad_x", gpu)
-    rows, width = grad_out.shape
-    if grad_x.shape != grad_out.shape:
-        raise ValueError(f"grad_x: {(rows, width)} expected, got {tuple(grad_x.shape)}")
+    if grad_out.requires_grad or grad_x.requires_grad:
+        _no_history(grad_out, grad_x, "drs_dropout_grad", "the gradient of a gradient is dropout_grad again")
+    shape, gpu = _shape2(grad_out, "grad_out"), grad_out.get_device()
+    grad_ptr, grad_code, grad_stride = _matrix(grad_out, "grad_out", shape, gpu)
+    x_ptr, x_code, x_stride = _matrix(grad_x, "grad_x", shape, gpu)
     key, device_key = _seed(seed, gpu)
-    st = load().drs_dropout_grad(grad_out.data_ptr(), _dtype_code(grad_out, "grad_out"), rows, width, grad_stride, p,
-                                 key, device_key, row0, grad_x.data_ptr(), _dtype_code(grad_x, "grad_x"), x_stride,
-                                 _raw_stream(stream, gpu))
-    _check(st, "drs_dropout_grad")
+    st = load().drs_dropout_grad(grad_ptr, grad_code, shape[0], shape[1], grad_stride, p, key, device_key, row0, x_ptr,
+                                 x_code, x_stride, _raw_stream(stream, gpu))
+    if st != DRS_OK:
+        _check(st, "drs_dropout_grad")
 
 
 KERNEL_NAMES = ("split_prep", "split_pass1", "split_merge", "split_pass2", "split_cluster",
