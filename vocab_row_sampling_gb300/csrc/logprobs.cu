@@ -24,10 +24,12 @@
 // Bound by memory for large batches, by instructions close behind: 16-bit rows
 // take about 6.5 issued per column and lane (an exponential, a product and three sums
 // each) and 24 warps of 80 registers per SM hide more than 32 of 64 (4096 x
-// 262144 bf16 rows with 20 alternatives 339 us against 371; without
-// alternatives 6.8 TB/s). Measured: those 339 us, 6.2 TB/s; 256 x 262144 fp32 47 us,
-// 5.7 TB/s; 1003 x 50001 fp16 with 5 alternatives 28 us; one row of 262144 bf16 7.0
-// us with 20 alternatives, 4.0 without: launch, the read's latency, a cluster's barrier.
+// 262144 bf16 rows with 20 alternatives 343 us against 371; without
+// alternatives 6.8 TB/s). Measured: those 343 us, 6.2 TB/s; 256 x 262144 fp32 46 us,
+// 5.7 TB/s; 1003 x 50001 fp16 with 5 alternatives 28 us, of which the rows' reading
+// takes 15 to 20, the rest the launch, the first loads and the selection; one row
+// of 262144 bf16 6.9 us with 20 alternatives, 4.0 without: launch, the read's
+// latency, a cluster's barrier.
 #include <climits>
 
 #include "token_common.cuh"
@@ -339,17 +341,16 @@ template <int kWarps> __device__ __forceinline__ int places_for(int mine, int* c
 template <int kWarps, typename F> __device__ __forceinline__ void rank_keys(const uint64_t* list, int n, F f) {
     const ulonglong2* const pairs = reinterpret_cast<const ulonglong2*>(list);
     constexpr int kThreads = kWarps * 32;
-    for (int i = threadIdx.x; i < n; i += 2 * kThreads) {  // two of them at a time
-        const uint64_t a = list[i], b = i + kThreads < n ? list[i + kThreads] : ~0ull, last = list[n - 1];
-        int above_a = (n & 1) && last > a, above_b = (n & 1) && last > b;
-#pragma unroll 4
+    const uint64_t last = n ? list[n - 1] : 0;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t key = list[i];
+        int above = (n & 1) && last > key;
+#pragma unroll 8
         for (int j = 0; j < n / 2; ++j) {
             const ulonglong2 p = pairs[j];
-            above_a += (p.x > a) + (p.y > a);
-            above_b += (p.x > b) + (p.y > b);
+            above += (p.x > key) + (p.y > key);
         }
-        f(a, above_a);
-        if (i + kThreads < n) f(b, above_b);
+        f(key, above);
     }
 }
 
@@ -445,7 +446,7 @@ template <typename T> __device__ __noinline__ int select_slowly(const Row<T> row
 }
 
 // The row's k largest logits into s.list, in no order: how many keys, at least k.
-// segment: its n segments' largest, with room up to a multiple of 128. s.counts are 0 before. By the
+// segment: its n segments' largest, with -inf up to a multiple of 128. s.counts are 0 before. By the
 // team, with a barrier at its end.
 template <int kWarps, typename T>
 __device__ __forceinline__ int select_top(const Row<T>& row, float* segment, int n, int k, const Selection& s) {
@@ -457,8 +458,6 @@ __device__ __forceinline__ int select_top(const Row<T>& row, float* segment, int
     bool slowly = false;
     if (n > k) {
         const int quads = (n + 127) / 128;
-        for (int i = n + tid; i < quads * 128; i += kThreads) segment[i] = -INFINITY;
-        team_sync<kWarps>();
         const float4* const quad = reinterpret_cast<const float4*>(segment);
         const float bound = fmaxf(reached_by(quad, quads, k, lane), kLowest);
         // 32 values per lane at a time: a bit for each that reaches the bound
@@ -835,19 +834,27 @@ template <bool kTop> __device__ __forceinline__ void pass_over(const LogprobPara
         }
 }
 
+// Before a row is read: nothing is selected yet, and the line of segments ends in -inf.
+template <int kWarps, typename T> __device__ __forceinline__ void prepare(const Row<T>& row, float* segment, const Selection& s) {
+    const int n = row.blocks() * kParts<T>;
+    for (int i = n + threadIdx.x; i < (n + 127) / 128 * 128; i += kWarps * 32) segment[i] = -INFINITY;
+    if (threadIdx.x == 0) s.counts[0] = s.counts[1] = 0;
+}
+
 // The row's outputs from its sums and segments, by the team.
 template <int kWarps, bool kTop, typename T>
 __device__ __forceinline__ void finish(const LogprobParams& a, int64_t r, const Task<T>& task, const Sums& sums, float* segment,
                                        const Selection& s) {
+    int found = 0;
+    if constexpr (kTop) found = select_top<kWarps>(task.row, segment, task.row.blocks() * kParts<T>, a.k, s);
     const float log_sum = sums.sum == 0.0f ? -INFINITY : logf(sums.sum);
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == (kWarps - 1) * 32) {
         a.out_logprob[r] = (to_f(task.own) - sums.top) * task.inverse - log_sum;
         if (a.out_entropy) a.out_entropy[r] = sums.sum == 0.0f ? 0.0f : log_sum - sums.weighted / sums.sum * kLn2;
         if (a.out_rank) a.out_rank[r] = 1 + sums.above;
         if (a.out_norm) a.out_norm[2 * r] = sums.top, a.out_norm[2 * r + 1] = log_sum;
     }
     if constexpr (kTop) {
-        const int found = select_top<kWarps>(task.row, segment, task.row.blocks() * kParts<T>, a.k, s);
         rank_keys<kWarps>(s.list, found, [&](uint64_t key, int above) {
             if (above >= a.k) return;
             a.out_ids[r * a.k + above] = place_of(key) - task.row.lead;
@@ -899,6 +906,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident / kWarps) logprob_kerne
                 ring.fill();
             }
             fetched = false;
+            if constexpr (kTop) prepare<kWarps>(task.row, segment, select);
             // what reaches over the row's ends, while the first blocks are on their way
             Sums edges{-INFINITY, 0.0f, 0.0f, 0};
             if (warp == kWarps - 1) add_edges<kTop>(task, 0, task.row.blocks(), segment, edges);
@@ -911,11 +919,9 @@ __global__ void __launch_bounds__(kWarps * 32, kResident / kWarps) logprob_kerne
             if (warp == kWarps - 1) sums = together(lane == 0 ? sums : edges, lane < 2, task.c);
             if constexpr (kWarps > 1) {
                 if (lane == 0) s_warp[warp] = sums;
-                if (kTop && threadIdx.x == 0) select.counts[0] = select.counts[1] = 0;
                 __syncthreads();
                 sums = together(s_warp[lane % kWarps], lane < kWarps, task.c);
             } else {
-                if (kTop && lane == 0) select.counts[0] = select.counts[1] = 0;
                 __syncwarp();
             }
             finish<kWarps, kTop>(a, r, task, sums, segment, select);
@@ -961,12 +967,12 @@ __global__ void __launch_bounds__(256, kResident / 8) logprob_cluster_kernel(con
         return;
     }
     const Task<T> task(a, r, id);
+    if constexpr (kTop) prepare<kWarps>(row, segment, select);
     Sums edges{-INFINITY, 0.0f, 0.0f, 0};
     if (warp == kWarps - 1) add_edges<kTop>(task, first, end, segment, edges);
     Sums sums = ring_sums<kTop>(ring, task, at, count, segment, [](Ring<T, kWarps>&) {});
     if (warp == kWarps - 1) sums = together(lane == 0 ? sums : edges, lane < 2, task.c);
     if (lane == 0) s_warp[warp] = sums;
-    if (kTop && tid == 0) select.counts[0] = select.counts[1] = 0;
     __syncthreads();
     cluster_wait();
     if (kTop && rank != 0)
@@ -1006,7 +1012,7 @@ template <typename T> drs_status launch_logprobs(LogprobParams a, bool vec, cuda
     if (sms <= 0) return DRS_ERR_CUDA;
     a.blocks = static_cast<int32_t>(ceil_div(a.vocab + (vec ? 0 : 16 / sizeof(T) - 1), kBlock<T>));
     const int segments = a.blocks * kParts<T>;
-    // CTAs per row: up to two per SM in all, 8192 columns each at least. us with one, 2, 4, 8 and 16 (20
+    // CTAs per row: up to two per SM in all, with more than 4096 columns each. us with one, 2, 4, 8 and 16 (20
     // alternatives, bf16): 1 x 262144 19.9, 13.3, 9.8, 8.0, 7.2; 16 x 262144 21.6, 14.6, 11.0, 10.5, 11.1; 64 x
     // 131072 14.3, 11.5, 11.2, 14.0, 18.7; 152 x 131072 15.0, 14.5, 19.4; 256 x 65536 13.8, 19.7.
     int cluster = 1, warps = 8;
