@@ -642,7 +642,8 @@ drs_status drs_token_logprobs(const void *logits, drs_dtype dtype, int64_t rows,
  * with p_j = e^((x_j - m) / te - ln S) from the forward call's norm, H its
  * entropy, g = grad_logprob[r] and h = grad_entropy[r]; computed in fp32 and
  * rounded once. Rows passed over in the forward call and rows that are -inf
- * everywhere get zeros; every row is written, and nothing behind vocab.
+ * everywhere (whose ln S is -inf) get zeros, rows with NaN or +inf get NaN; every
+ * row is written, and nothing behind vocab.
  *
  *   logits, ids, id_bits, temps, canvas_len   as drs_token_logprobs.
  *   norm         fp32 [rows, 2], out_norm of the forward call.

@@ -162,6 +162,32 @@ def test_seeds_on_the_gpu_and_graphs():
         assert torch.equal(out, grad) and int(seed) == at + 1
 
 
+def test_streams():
+    """Calls on other streams, at the same time, and the two outputs allocated on theirs."""
+    lib = drs()
+    x, _ = filled(500, 1003, torch.bfloat16, 1)
+    want = lib.dropout(x, 0.3, SEED)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    outs = [(lib.dropout(x, 0.3, SEED, stream=s), lib.dropout_grad(x, 0.3, SEED, stream=s)) for s in streams]
+    torch.cuda.synchronize()
+    for out, grad in outs:
+        assert torch.equal(out, want) and torch.equal(grad, want)
+
+
+def test_x_residual_and_out_are_one():
+    for width in (64, 333):
+        x, _ = filled(21, width, torch.float32, 1)
+        want = drs().dropout(x, 0.4, 9, residual=x)
+        assert torch.equal(drs().dropout(x, 0.4, 9, residual=x, out=x), want)
+
+
+@pytest.mark.parametrize("width", [1048576, 1048575])
+def test_the_widest_rows(width):
+    x, _ = filled(3, width, torch.bfloat16, 1)
+    check(drs().dropout(x, 0.3, SEED), x, 0.3, SEED)
+
+
 def test_empty_calls_and_rows_behind_the_last():
     assert drs().dropout(torch.zeros(0, 5, device="cuda"), 0.5, 1).shape == (0, 5)
     x = torch.ones(4, 100, device="cuda")

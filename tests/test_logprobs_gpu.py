@@ -211,6 +211,43 @@ def test_grad_in_place(dtype, pad, offset):
         check_grad(logits, ids_of(11, vocab, 2), TYPES[dtype], out=logits)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_grad_of_rows_with_nan_or_infinity(dtype):
+    """Rows whose sum is NaN have NaN everywhere, the others keep theirs; a row of -inf with one NaN among them."""
+    for pad in (0, 3):
+        logits, ids = logits_of("plain", 6, 600, TYPES[dtype], 4, pad), torch.tensor([3, 3, 3, 3, 3, -1], device="cuda")
+        logits[0, 7] = INF
+        logits[1, 9] = float("nan")
+        logits[2] = -INF
+        logits[2, 300] = float("nan")
+        logits[3] = -INF
+        out = drs().token_logprobs(logits, ids)
+        one = torch.ones(6, device="cuda")
+        grad = drs().token_logprobs_grad(logits, ids, out[3], one, out[1], one)
+        assert grad[:3].isnan().all() and (grad[3] == 0).all() and grad[4].isfinite().all() and (grad[5] == 0).all()
+
+
+def test_the_longest_rows_by_teams():
+    """2^21 columns, more rows than clusters take: teams whose segments need most of the shared memory."""
+    vocab = 2097152
+    for dtype in (torch.float32, torch.bfloat16):
+        logits = torch.zeros(320, vocab, dtype=dtype, device="cuda")
+        at = torch.tensor([0, 151, 304, 319], device="cuda")
+        logits[at] = logits_of("plain", 4, vocab, dtype, 1)
+        ids = torch.full((320,), -1, device="cuda")
+        ids[at] = torch.tensor([0, 77, vocab - 1, 1234567], device="cuda")
+        ids[5] = 9  # a row of zeros: all equal
+        out = drs().token_logprobs(logits, ids, 64)
+        check_logprobs([t[at] for t in out], logits[at], ids[at], 64)
+        assert torch.equal(out[4][5].long(), torch.arange(64, device="cuda")) and int(out[2][5]) == 1
+        del logits
+
+
+def test_many_short_rows():
+    logits, ids = logits_of("ties", 100003, 40, torch.float16, 1), ids_of(100003, 40, 1)
+    check_logprobs(drs().token_logprobs(logits, ids, 7), logits, ids, 7)
+
+
 def test_grad_temperatures():
     temps = torch.tensor([0.4, 0.9, 1.7], device="cuda")
     logits, ids = logits_of("plain", 11, 1500, torch.bfloat16, 1), ids_of(11, 1500, 2)

@@ -82,12 +82,6 @@ __device__ __forceinline__ float ex2_flushed(float x) {
     return y;
 }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 // The largest of eight elements (NaN left out), and how many exceed a value. 16-bit elements are compared in
 // pairs, whose results 0 or 0xFFFF in each half are added up as one number: with n_low and n_high of
 // them it is 65536 (n_low - n_high) - n_low modulo 2^32, and holds up to 65535 of each.

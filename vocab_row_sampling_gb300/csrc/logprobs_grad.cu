@@ -19,7 +19,7 @@ constexpr int kGradThreads = 128;
 // Units of eight columns per thread where rows are off 16-byte boundaries. us for 777 x 50001 bf16 into fp32 with 1,
 // 2, 3 and 4 units: 39.7, 38.8, 48.2, 43.0; into bf16 36.3, 29.2, 35.2, 31.5.
 constexpr int kOddUnits = 2;
-constexpr float kLeastExponent = -200.0f;  // 2^-200 is 0 in fp32
+constexpr float kLeastExponent = -200.0f;  // 2^-200 is 0 in fp32; -inf would give 0 times infinity
 
 struct LogprobGradParams {
     const void* logits;
@@ -47,7 +47,7 @@ struct RowTerms {
             a.id_bits == 64 ? static_cast<const int64_t*>(a.ids)[row] : static_cast<const int32_t*>(a.ids)[row];
         top = a.norm[2 * row];
         log_sum = a.norm[2 * row + 1];
-        none = token < 0 || token >= a.vocab || top == -INFINITY;
+        none = token < 0 || token >= a.vocab || log_sum == -INFINITY;
         id = none ? -1 : static_cast<int>(token);
         inverse = a.temps ? 1.0f / fmaxf(a.temps[row / a.canvas_len], kTempFloor) : 1.0f;
         g = a.grad_logprob ? a.grad_logprob[row] : 0.0f;
@@ -62,14 +62,14 @@ struct RowTerms {
     // The token's column: g (1 - p) without the difference's cancellation.
     __device__ float own(float v) const {
         const float lp = (v - top) * inverse - log_sum;
-        const float p = ex2_approx(fmaxf((v - top) * scale - shift, kLeastExponent));
-        return (h == 0.0f ? 0.0f : -h * p * (fmaxf(lp, kLeastExponent) + entropy) * inverse) - g * expm1f(lp) * inverse;
+        const float p = ex2_approx(max_nan((v - top) * scale - shift, kLeastExponent));
+        return (h == 0.0f ? 0.0f : -h * p * (max_nan(lp, kLeastExponent) + entropy) * inverse) - g * expm1f(lp) * inverse;
     }
 
     __device__ float one(float v, int col) const {
         if (none) return 0.0f;
         if (col == id) return own(v);
-        const float l = fmaxf((v - top) * scale - shift, kLeastExponent);
+        const float l = max_nan((v - top) * scale - shift, kLeastExponent);
         return ex2_approx(l) * fmaf(a1, l, a0);
     }
 
@@ -93,8 +93,8 @@ struct RowTerms {
         for (int e = 0; e < 8; e += 2) {
             float l0, l1;
             unpack2(sub2(mul2(sub2(pack2(v[e], v[e + 1]), top2), scale2), shift2), l0, l1);
-            l0 = fmaxf(l0, kLeastExponent);
-            l1 = fmaxf(l1, kLeastExponent);
+            l0 = max_nan(l0, kLeastExponent);
+            l1 = max_nan(l1, kLeastExponent);
             unpack2(mul2(pack2(ex2_approx(l0), ex2_approx(l1)), fma2(a12, pack2(l0, l1), a02)), v[e], v[e + 1]);
         }
         if (here) {
