@@ -43,17 +43,24 @@ __device__ __forceinline__ PhiloxKey dropout_key(const DropoutParams& a) {
 }
 
 // The eight elements' 16-bit numbers, two to a word, the lower half first, for
-// n counters in step: they share the rounds' keys.
+// n counters in step: philox4x32_10 of each, whose rounds' keys they share.
 template <int n>
 __device__ __forceinline__ void dropout_words(PhiloxKey key, const uint64_t (&row)[n], const uint32_t (&group)[n], uint4 (&w)[n]) {
+    constexpr uint32_t kMulA = 0xD2511F53u, kMulB = 0xCD9E8D57u;
+    constexpr uint32_t kWeylA = 0x9E3779B9u, kWeylB = 0xBB67AE85u;
 #pragma unroll
     for (int i = 0; i < n; ++i)
         w[i] = make_uint4(group[i], kDropoutTag, static_cast<uint32_t>(row[i]), static_cast<uint32_t>(row[i] >> 32));
 #pragma unroll
     for (int round = 0; round < 10; ++round) {
 #pragma unroll
-        for (int i = 0; i < n; ++i) w[i] = philox_round(w[i], key);
-        key = philox_next(key);
+        for (int i = 0; i < n; ++i) {
+            const uint64_t a = static_cast<uint64_t>(kMulA) * w[i].x, b = static_cast<uint64_t>(kMulB) * w[i].z;
+            w[i] = make_uint4(static_cast<uint32_t>(b >> 32) ^ w[i].y ^ key.k0, static_cast<uint32_t>(b),
+                              static_cast<uint32_t>(a >> 32) ^ w[i].w ^ key.k1, static_cast<uint32_t>(a));
+        }
+        key.k0 += kWeylA;
+        key.k1 += kWeylB;
     }
 }
 

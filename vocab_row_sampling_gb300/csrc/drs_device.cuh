@@ -47,25 +47,19 @@ struct PhiloxKey {
     uint32_t k0, k1;
 };
 
-__device__ __forceinline__ uint4 philox_round(uint4 c, PhiloxKey key) {
-    constexpr uint32_t kMulA = 0xD2511F53u, kMulB = 0xCD9E8D57u;
-    const uint32_t hi_a = __umulhi(kMulA, c.x);
-    const uint32_t lo_a = kMulA * c.x;
-    const uint32_t hi_b = __umulhi(kMulB, c.z);
-    const uint32_t lo_b = kMulB * c.z;
-    return make_uint4(hi_b ^ c.y ^ key.k0, lo_b, hi_a ^ c.w ^ key.k1, lo_a);
-}
-
-// The next round's key.
-__device__ __forceinline__ PhiloxKey philox_next(PhiloxKey key) {
-    return PhiloxKey{key.k0 + 0x9E3779B9u, key.k1 + 0xBB67AE85u};
-}
-
 __device__ __forceinline__ uint4 philox4x32_10(uint4 c, PhiloxKey key) {
+    constexpr uint32_t kMulA = 0xD2511F53u, kMulB = 0xCD9E8D57u;
+    constexpr uint32_t kWeylA = 0x9E3779B9u, kWeylB = 0xBB67AE85u;
+    uint32_t k0 = key.k0, k1 = key.k1;
 #pragma unroll
     for (int round = 0; round < 10; ++round) {
-        c = philox_round(c, key);
-        key = philox_next(key);
+        const uint32_t hi_a = __umulhi(kMulA, c.x);
+        const uint32_t lo_a = kMulA * c.x;
+        const uint32_t hi_b = __umulhi(kMulB, c.z);
+        const uint32_t lo_b = kMulB * c.z;
+        c = make_uint4(hi_b ^ c.y ^ k0, lo_b, hi_a ^ c.w ^ k1, lo_a);
+        k0 += kWeylA;
+        k1 += kWeylB;
     }
     return c;
 }
