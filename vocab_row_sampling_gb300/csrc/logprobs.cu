@@ -705,13 +705,9 @@ template <typename T, bool kTop, bool kCareful> struct RowReader {
             most = fmaxf(most, largest);
         }
         sums.top = fmaxf(sums.top, most);
-        if (most > sums.bound) {  // seldom: the barrier keeps it a branch
-            __syncwarp();
-            if (!sums.move(c)) return false;
-        }
+        if (most > sums.bound && !sums.move(c)) return false;
         sums.add(raw, c);
         if (most > own_value) {
-            __syncwarp();
 #pragma unroll
             for (int p = 0; p < kParts<T>; ++p) Eight<T>::count(raw[p], own, above);
         }
