@@ -1002,19 +1002,23 @@ template <typename T> drs_status launch_logprobs(LogprobParams a, bool vec, cuda
     if (sms <= 0) return DRS_ERR_CUDA;
     a.blocks = static_cast<int32_t>(ceil_div(a.vocab + (vec ? 0 : 16 / sizeof(T) - 1), kBlock<T>));
     const int segments = a.blocks * kParts<T>;
-    // CTAs per row: up to two per SM in all, with more than 4096 columns each. us with one, 2, 4, 8 and 16 (20
-    // alternatives, bf16): 1 x 262144 19.9, 13.3, 9.8, 8.0, 7.2; 16 x 262144 21.6, 14.6, 11.0, 10.5, 11.1; 64 x
-    // 131072 14.3, 11.5, 11.2, 14.0, 18.7; 152 x 131072 15.0, 14.5, 19.4; 256 x 65536 13.8, 19.7.
+    // CTAs per row: as many as are resident at once, with more than 4096 columns each. us with one, 2, 4, 8 and 16
+    // (20 alternatives, bf16): 1 x 262144 19.9, 13.3, 9.8, 8.0, 7.2; 16 x 262144 21.6, 14.6, 11.0, 10.5, 11.1; 50 x
+    // 131072 14.0, 10.8, 10.3, 10.8; 110 x 262144 21.5, 19.3, 17.8; 225 x 262144 31.2, 26.6; a second wave costs
+    // more: 300 x 131072 19.7, 26.1.
+    const int64_t resident = int64_t{sms} * kResident;
     int cluster = 1, warps = 8;
-    while (cluster < kMaxRowCluster && a.vocab > 8192 * cluster && a.rows * cluster * 2 <= 2 * sms) cluster *= 2;
-    // Warps per row: as many as leave every row a team at once, unless that is more than 64 KB of a row per warp
-    // (128 KB of 16-bit rows when there are many). us with 8, 4, 2 and 1: 300 x 65536 bf16 14.2, 16.1, 21.3, 43.5;
-    // 600 x 65536 26.5, 21.6, 24.7, 42.8; 1003 x 50001 fp16 36.2, 32.5, 30.2, 39.2; 4096 x 8192 bf16 66.9, 47.5, 39.8,
-    // 33.9; 1024 x 262144 bf16 91.5, 99.2, 107.3, 161.9; 4096 x 262144 350, 343, 358, 430; 2048 x 131072 fp32 166, 170,
-    // 201, 180.
-    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T)), resident = int64_t{sms} * kResident;
-    const int64_t share = sizeof(T) == 2 && a.rows * 2 > resident ? 128 * 1024 : 64 * 1024;  // of a warp, at most
-    while (warps > 1 && a.rows * warps > resident && bytes * 2 <= share * warps) warps /= 2;
+    while (cluster < kMaxRowCluster && a.vocab > 8192 * cluster && a.rows * cluster * 2 <= resident / 8) cluster *= 2;
+    // Warps per row: as many as leave every row a team at once, but no fewer than suit the row's bytes. us with
+    // 8, 4, 2 and 1 (16-bit): 300 x 65536 14.2, 16.1, 21.3, 43.5; 600 x 65536 26.5, 21.6, 24.7, 42.8; 1003 x 50001
+    // 36.2, 32.5, 30.2, 39.2; 4096 x 8192 66.9, 47.5, 39.8, 33.9; 2500 x 20000 53.6, 42.2, 36.1, 36.2; 3000 x 60000
+    // 90.8, 82.0, 81.1, 103; 1024 x 262144 91.5, 99.2, 107, 162; 4096 x 262144 350, 343, 358, 430; fp32: 2048 x
+    // 131072 166, 170, 201, 180; 1653 x 28800 52.2, 45.8, 46.4, 52.5.
+    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T));
+    const int64_t most = sizeof(T) == 2 && a.rows * 2 > resident ? 512 * 1024 : 256 * 1024;  // of a row for four warps
+    if (a.rows * 8 > resident && bytes <= most) warps = 4;
+    if (a.rows * 4 > resident && bytes <= 128 * 1024) warps = 2;
+    if (a.rows * 2 > resident && bytes <= 40 * 1024) warps = 1;
     if (cluster > 1) warps = 8;
     a.cluster = cluster;
     a.part = static_cast<int32_t>(ceil_div(a.blocks, cluster));
