@@ -348,30 +348,50 @@ template <int kWarps, typename F> __device__ __forceinline__ void rank_keys(cons
     }
 }
 
-// A value that at least k of the 128 n values reach, or -inf (which NaN counts
-// as): the k-th largest of the largest of 32 (k <= 32) or 64 groups of them.
-__device__ __forceinline__ float reached_by(const float4* value, int n, int k, int lane) {
-    float a = -INFINITY, b = -INFINITY;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float4 v = value[i * 32 + lane];
-        a = fmaxf(a, fmaxf(v.x, v.y));
-        b = fmaxf(b, fmaxf(v.z, v.w));
-    }
-    int above_a = 0, above_b = 0;
-    if (k <= 32) {
-        a = fmaxf(a, b);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) above_a += __shfl_sync(0xffffffffu, a, i) > a;
-        return warp_min(above_a < k ? a : INFINITY);  // the smallest that fewer than k exceed
-    }
+// The k-th largest of the warp's 32 n values, -inf where there are fewer.
+template <int n> __device__ __forceinline__ float kth_of(const float (&v)[n], int k) {
+    int above[n] = {};
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        const float u = __shfl_sync(0xffffffffu, a, i), v = __shfl_sync(0xffffffffu, b, i);
-        above_a += (u > a) + (v > a);
-        above_b += (u > b) + (v > b);
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            const float u = __shfl_sync(0xffffffffu, v[j], i);
+#pragma unroll
+            for (int h = 0; h < n; ++h) above[h] += u > v[h];
+        }
     }
-    return warp_min(fminf(above_a < k ? a : INFINITY, above_b < k ? b : INFINITY));
+    float least = INFINITY;  // the smallest that fewer than k exceed
+#pragma unroll
+    for (int h = 0; h < n; ++h) least = fminf(least, above[h] < k ? v[h] : INFINITY);
+    return warp_min(least);
+}
+
+// Apart for more than 20: unrolled, these would weigh on the registers of the reading.
+__device__ __noinline__ float kth_of_64(float a, float b, int k) {
+    const float v[2] = {a, b};
+    return kth_of<2>(v, k);
+}
+__device__ __noinline__ float kth_of_128(float4 u, int k) {
+    const float v[4] = {u.x, u.y, u.z, u.w};
+    return kth_of<4>(v, k);
+}
+
+// A value that at least k of the 128 n values reach, or -inf (which NaN counts
+// as): the k-th largest of the largest of 32, 64 or 128 groups of them. With 1.6 k
+// groups or more not many more than k reach it: of 1024 about 31 for k = 20 and
+// 43 for k = 32 (130 with 32 groups: the smallest of them all).
+__device__ __forceinline__ float reached_by(const float4* value, int n, int k, int lane) {
+    float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float4 u = value[i * 32 + lane];
+        v = make_float4(fmaxf(v.x, u.x), fmaxf(v.y, u.y), fmaxf(v.z, u.z), fmaxf(v.w, u.w));
+    }
+    if (k > 40) return kth_of_128(v, k);
+    const float a = fmaxf(v.x, v.y), b = fmaxf(v.z, v.w);
+    if (k > 20) return kth_of_64(a, b, k);
+    const float one[1] = {fmaxf(a, b)};
+    return kth_of<1>(one, k);
 }
 
 // The k largest of n numbers, equal ones by index, as indices in ascending
@@ -485,6 +505,7 @@ __device__ __forceinline__ int select_top(const Row<T>& row, float* segment, int
     } else {
         for (int i = tid; i < n; i += kThreads) s.chosen[i] = i;
         float* const unit = reinterpret_cast<float*>(s.stage);
+#pragma unroll 2
         for (int c = warp; c < (n + 3) / 4 * 4; c += kWarps)  // a lane's in its own float4s
             unit[(c / 4 * 32 + lane) * 4 + c % 4] = c < n ? Eight<T>::largest(row.unit(c * kSegment + lane * 8)) : -INFINITY;
         team_sync<kWarps>();
