@@ -116,9 +116,13 @@ __global__ void __launch_bounds__(kDropoutThreads) dropout_kernel(const DropoutP
     }
 }
 
-// Columns before the first 16-byte boundary of a row of `out`.
+// Where units of eight columns of `out` begin: on 16-byte boundaries, fp32 ones on 32-byte ones, so that
+// a lane writes whole sectors (KKK).
+template <typename Y> constexpr int kBoundary = sizeof(Y) == 4 ? 32 : 16;
+
+// Columns before the first boundary of a row of `out`: at most 7.
 template <typename Y> __device__ __forceinline__ int columns_before(const Y* out, int width) {
-    return min(static_cast<int>((-reinterpret_cast<uintptr_t>(out) & 15) / sizeof(Y)), width);
+    return min(static_cast<int>((-reinterpret_cast<uintptr_t>(out) & (kBoundary<Y> - 1)) / sizeof(Y)), width);
 }
 
 // Other rows. A lane has the numbers of sixteen columns from a multiple of 16

@@ -463,7 +463,7 @@ template <typename T> __device__ __noinline__ int select_slowly(const Row<T> row
 // segment: its n segments' largest, with -inf up to a multiple of 128. s.counts are 0 before. By the
 // team, with a barrier at its end.
 template <int kWarps, typename T>
-__device__ __forceinline__ int select_top(const Row<T>& row, float* segment, int n, int k, const Selection& s) {
+__device__ __noinline__ int select_top(const Row<T> row, float* segment, int n, int k, const Selection s) {
     constexpr float kLowest = -0x1.fffffep127f;  // all but -inf and NaN reach it
     constexpr int kThreads = kWarps * 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

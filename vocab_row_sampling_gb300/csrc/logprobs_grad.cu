@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_odd_kernel(const Lo
     const int chunk = static_cast<int>(blockIdx.x % a.chunks);
     const T* const x = static_cast<const T*>(a.logits) + row * a.row_stride;
     G* const out = static_cast<G*>(a.grad) + row * a.grad_stride;
-    const int head = min(static_cast<int>((-reinterpret_cast<uintptr_t>(out) & 15) / sizeof(G)), a.vocab);
+    constexpr int kBoundary = sizeof(G) == 4 ? 32 : 16;
+    const int head = min(static_cast<int>((-reinterpret_cast<uintptr_t>(out) & (kBoundary - 1)) / sizeof(G)), a.vocab);
     const int tail = head + (a.vocab - head) / 8 * 8;  // the first column behind the units
     const int first = head + chunk * (kGradThreads * kOddUnits * 8) + threadIdx.x * 8;
     Any8<T> raw[kOddUnits];
