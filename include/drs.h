@@ -626,7 +626,8 @@ drs_status drs_embed_tokens_grad(const void *grad_out, drs_dtype grad_dtype, int
  * that the type allows. Returns DRS_ERR_INVALID_ARG for sizes out of range
  * (k > vocab among them), an unknown type, a stride below vocab, a null or
  * unaligned pointer; DRS_ERR_UNSUPPORTED for vocab > DRS_MAX_VOCAB,
- * k > DRS_MAX_ALTERNATIVES or rows > DRS_MAX_SCORE_ROWS.
+ * k > DRS_MAX_ALTERNATIVES or rows > DRS_MAX_SCORE_ROWS; DRS_ERR_CUDA for few
+ * long rows on a device that grants no clusters of 16 CTAs.
  */
 drs_status drs_token_logprobs(const void *logits, drs_dtype dtype, int64_t rows, int64_t vocab,
                               int64_t row_stride, const void *ids, int32_t id_bits,

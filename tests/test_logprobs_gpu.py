@@ -48,6 +48,16 @@ def test_numbers_of_rows(dtype, kind, rows):
         check_logprobs(drs().token_logprobs(logits, ids, k), logits, ids, k)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,vocab", [(3, 100000), (60, 30011), (700, 20000), (2500, 3000)])
+def test_temperatures_of_all_sizes_in_a_batch(dtype, rows, vocab):
+    """Rows that need care from the start, on the way (huge logits) and not at all, in turn for one team."""
+    temps = torch.tensor([0.0, 1.0, 1e-4, 0.02, 3.0, 1e-7, 0.7], device="cuda").repeat(-(-rows // 7))[:rows]
+    for kind in ("ties", "far", "masked"):
+        logits, ids = logits_of(kind, rows, vocab, TYPES[dtype], rows, 1), ids_of(rows, vocab, 1)
+        check_logprobs(drs().token_logprobs(logits, ids, 9, temps), logits, ids, 9, temps)
+
+
 @pytest.mark.parametrize("temp", [400.0, 1e4, 1e30, 3e38])
 def test_large_temperatures_under_masks(temp):
     """The floor of the exponents leaves the type's range; whole parts of the rows are -inf."""

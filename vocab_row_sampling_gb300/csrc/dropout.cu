@@ -26,7 +26,7 @@ constexpr int kDropoutThreads = 128;  // 65536 x 4096: 223 us with 64, 224 with 
 constexpr uint32_t kDropoutTag = 0x64726F70u;
 
 struct DropoutParams {
-    const void* x;  // NULL: everything is dropped
+    const void* x;
     const void* residual;
     void* out;
     const uint64_t* device_seed;
@@ -96,9 +96,8 @@ __global__ void __launch_bounds__(kDropoutThreads) dropout_kernel(const DropoutP
         const int64_t r = r0 + i * static_cast<int64_t>(blockDim.y);
         groups[i] = static_cast<uint32_t>(group);
         row[i] = static_cast<uint64_t>(a.row0 + r);
-        x[i] = Raw8<X>{};
         if (r >= a.rows) continue;
-        if (a.x) x[i].load(static_cast<const X*>(a.x) + r * a.x_stride + group * 8);
+        x[i].load(static_cast<const X*>(a.x) + r * a.x_stride + group * 8);
         if constexpr (kResidual)
             residual[i].load(static_cast<const Y*>(a.residual) + r * a.residual_stride + group * 8);
     }
@@ -116,8 +115,26 @@ __global__ void __launch_bounds__(kDropoutThreads) dropout_kernel(const DropoutP
     }
 }
 
+// The sixteen numbers from the head-th of those of a, b and c on, into a and b.
+__device__ __forceinline__ void shift_numbers(uint4& a, uint4& b, const uint4& c, int head) {
+    uint32_t w[12] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+    if (head & 4) {
+#pragma unroll
+        for (int i = 0; i < 10; ++i) w[i] = w[i + 2];
+    }
+    if (head & 2) {
+#pragma unroll
+        for (int i = 0; i < 9; ++i) w[i] = w[i + 1];
+    }
+    const int bits = (head & 1) * 16;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], bits);
+    a = make_uint4(w[0], w[1], w[2], w[3]);
+    b = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
 // Where units of eight columns of `out` begin: on 16-byte boundaries, fp32 ones on 32-byte ones, so that
-// a lane writes whole sectors (KKK).
+// a lane writes whole sectors.
 template <typename Y> constexpr int kBoundary = sizeof(Y) == 4 ? 32 : 16;
 
 // Columns before the first boundary of a row of `out`: at most 7.
@@ -144,7 +161,7 @@ __global__ void __launch_bounds__(kDropoutThreads) dropout_odd_kernel(const Drop
         const int head = columns_before(out, a.width), tail = head + (a.width - head) / 8 * 8;
         const int col = e < 8 ? e : tail + e - 8;
         if (e < 8 ? e >= head : col >= a.width) return;
-        const float x = a.x ? to_f((static_cast<const X*>(a.x) + r * a.x_stride)[col]) : 0.0f;
+        const float x = to_f((static_cast<const X*>(a.x) + r * a.x_stride)[col]);
         const float base = kResidual ? to_f((static_cast<const Y*>(a.residual) + r * a.residual_stride)[col]) : 0.0f;
         const uint64_t row[1] = {static_cast<uint64_t>(a.row0 + r)};
         const uint32_t group[1] = {static_cast<uint32_t>(col / 8)};
@@ -168,13 +185,12 @@ __global__ void __launch_bounds__(kDropoutThreads) dropout_odd_kernel(const Drop
     const Y* const rest = static_cast<const Y*>(a.residual) + r * a.residual_stride;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        x[h] = Words{};
         if (!writes || col + 8 * h + 8 > a.width) continue;
         if constexpr (kAlike) {
-            if (a.x) x[h].load(from + (col + 8 * h));
+            x[h].load(from + (col + 8 * h));
             if constexpr (kResidual) residual[h].load(rest + (col + 8 * h));
         } else {
-            if (a.x) x[h].load(from, col + 8 * h, a.width);
+            x[h].load(from, col + 8 * h, a.width);
             if constexpr (kResidual) residual[h].load(rest, col + 8 * h, a.width);
         }
     }
@@ -184,8 +200,7 @@ __global__ void __launch_bounds__(kDropoutThreads) dropout_odd_kernel(const Drop
     dropout_words(dropout_key(a), row, group, w);
     const uint4 next = make_uint4(__shfl_down_sync(0xffffffffu, w[0].x, 1, lanes), __shfl_down_sync(0xffffffffu, w[0].y, 1, lanes),
                                   __shfl_down_sync(0xffffffffu, w[0].z, 1, lanes), __shfl_down_sync(0xffffffffu, w[0].w, 1, lanes));
-    w[0] = joined(w[0], w[1], 2 * head);
-    w[1] = joined(w[1], next, 2 * head);
+    shift_numbers(w[0], w[1], next, head);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if (!writes || col + 8 * h + 8 > a.width) continue;
@@ -231,7 +246,7 @@ drs_status launch_dropout(DropoutParams a, bool vec, cudaStream_t stream) {
             return (reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(a.out)) % 16 == 0 &&
                    (stride - a.out_stride) * static_cast<int64_t>(sizeof(Y)) % 16 == 0;
         };
-        if ((!a.x || alike(a.x, a.x_stride)) && (!kResidual || alike(a.residual, a.residual_stride)))
+        if (alike(a.x, a.x_stride) && (!kResidual || alike(a.residual, a.residual_stride)))
             kernel = dropout_odd_kernel<X, Y, kResidual, true>;
     }
     kernel<<<static_cast<unsigned>(blocks), kDropoutThreads, 0, stream>>>(a, lanes, static_cast<unsigned>(unit_blocks));
@@ -266,9 +281,16 @@ drs_status dropout(const void* x, drs_dtype dtype, int64_t rows, int64_t width, 
     a.row0 = row0;
     a.width = static_cast<int32_t>(width);
     const uint32_t dropped = static_cast<uint32_t>(std::floor(static_cast<double>(p) * 65536.0 + 0.5));
-    if (dropped == 65536) a.x = nullptr;
+    if (dropped == 65536) {  // nothing of x is left
+        if (!residual)
+            return cuda_status(cudaMemset2DAsync(out, static_cast<size_t>(out_stride) * dtype_bytes(out_dtype), 0,
+                                                 static_cast<size_t>(width) * dtype_bytes(out_dtype),
+                                                 static_cast<size_t>(rows), stream));
+        return dropout(residual, out_dtype, rows, width, residual_stride, nullptr, 0, 0.0f, seed, device_seed, row0, out,
+                       out_dtype, out_stride, stream);
+    }
     a.limit = dropped << 16;
-    a.scale = dropped < 65536 ? static_cast<float>(65536.0 / (65536.0 - dropped)) : 0.0f;
+    a.scale = static_cast<float>(65536.0 / (65536.0 - dropped));
     const auto on_boundaries = [&](const void* q, int64_t stride, drs_dtype t) {
         return aligned(q, 16) && stride * dtype_bytes(t) % 16 == 0;
     };

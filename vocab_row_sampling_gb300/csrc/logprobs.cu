@@ -22,13 +22,13 @@
 // Few rows: a cluster of up to 16 CTAs takes a row and its first CTA selects.
 //
 // Bound by memory for large batches, by instructions close behind: 16-bit rows
-// take about 6.5 issued per column and lane (an exponential, a product and three sums
-// each) and 24 warps of 80 registers per SM hide more than 32 of 64 (4096 x
-// 262144 bf16 rows with 20 alternatives 343 us against 371; without
-// alternatives 6.8 TB/s). Measured: those 343 us, 6.2 TB/s; 256 x 262144 fp32 46 us,
-// 5.7 TB/s; 1003 x 50001 fp16 with 5 alternatives 28 us, of which the rows' reading
+// take about 8 issued per column (an exponential, a product and three sums
+// each), and 24 warps of 80 registers per SM do better than 32 of 64 (4096 x
+// 262144 bf16 rows with 20 alternatives 339 us against 371). Measured: these
+// 336 us, 6.3 TB/s (315, 6.7 TB/s, without alternatives); 256 x 262144 fp32 46 us,
+// 5.7 TB/s; 1003 x 50001 fp16 with 5 alternatives 27 us, of which the rows' reading
 // takes 15 to 20, the rest the launch, the first loads and the selection; one row
-// of 262144 bf16 6.9 us with 20 alternatives, 4.0 without: launch, the read's
+// of 262144 bf16 7.0 us with 20 alternatives, 4.0 without: launch, the read's
 // latency, a cluster's barrier.
 #include <climits>
 
@@ -459,7 +459,8 @@ template <typename T> __device__ __noinline__ int select_slowly(const Row<T> row
     return found;
 }
 
-// The row's k largest logits into s.list, in no order: how many keys, at least k.
+// The row's k largest logits into s.list, in no order: how many keys, at least k. Apart from the
+// reading, whose registers it would take (4096 x 262144 bf16 348 us within, 336 apart).
 // segment: its n segments' largest, with -inf up to a multiple of 128. s.counts are 0 before. By the
 // team, with a barrier at its end.
 template <int kWarps, typename T>
@@ -795,9 +796,9 @@ __device__ __forceinline__ void add_edges(const Task<T>& task, int first, int en
 
 // The warp's blocks first, first + kStep, ... (count of them), which come through the ring; before the last kDepth
 // of them all have been fetched, and `go_on` may point it at the next row's.
-template <bool kTop, typename T, int kStep, typename F>
+template <bool kTop, bool kCareful, typename T, int kStep, typename F>
 __device__ __forceinline__ Sums ring_sums(Ring<T, kStep>& ring, const Task<T>& task, int first, int count, float* segment, F go_on) {
-    RowReader<T, kTop, false> reader(task.c, task.own, segment);
+    RowReader<T, kTop, kCareful> reader(task.c, task.own, segment);
     bool fine = true;
     int n = 0;
     for (int end = max(count - kDepth, 0);; end = count) {
@@ -806,7 +807,7 @@ __device__ __forceinline__ Sums ring_sums(Ring<T, kStep>& ring, const Task<T>& t
             Raw8<T> raw[kParts<T>];
             ring.take(w);
             segments_of(w, raw);
-            if (!reader.add(raw, first + n * kStep)) {
+            if (!reader.add(raw, first + n * kStep) && !kCareful) {
                 fine = false;
                 break;
             }
@@ -824,6 +825,14 @@ __device__ __forceinline__ Sums ring_sums(Ring<T, kStep>& ring, const Task<T>& t
         ring.fetch_next();
     }
     return careful_sums<T, kTop>(task, first, kStep, first + (count - 1) * kStep + 1, segment);
+}
+
+// With care from the start where temperatures leave no doubt (0, say); beyond it only logits above 4096 do.
+constexpr float kCarefulFrom = 4096.0f;  // c
+template <bool kTop, typename T, int kStep, typename F>
+__device__ __forceinline__ Sums row_sums(Ring<T, kStep>& ring, const Task<T>& task, int first, int count, float* segment, F go_on) {
+    if (task.c < kCarefulFrom) return ring_sums<kTop, false>(ring, task, first, count, segment, go_on);
+    return ring_sums<kTop, true>(ring, task, first, count, segment, go_on);
 }
 
 // How many of the numbers first, first + step, ... lie below end.
@@ -921,7 +930,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident / kWarps) logprob_kerne
             // what reaches over the row's ends, while the first blocks are on their way
             Sums edges{-INFINITY, 0.0f, 0.0f, 0};
             if (warp == kWarps - 1) add_edges<kTop>(task, 0, task.row.blocks(), segment, edges);
-            Sums sums = ring_sums<kTop>(ring, task, first, count, segment, [&](Ring<T, kWarps>& g) {
+            Sums sums = row_sums<kTop>(ring, task, first, count, segment, [&](Ring<T, kWarps>& g) {
                 if (next_id >= 0 && count >= kDepth) {
                     g.point_at(next.row, next_first, next_count);
                     fetched = true;
@@ -981,7 +990,7 @@ __global__ void __launch_bounds__(256, kResident / 8) logprob_cluster_kernel(con
     if constexpr (kTop) prepare<kWarps>(row, segment, select);
     Sums edges{-INFINITY, 0.0f, 0.0f, 0};
     if (warp == kWarps - 1) add_edges<kTop>(task, first, end, segment, edges);
-    Sums sums = ring_sums<kTop>(ring, task, at, count, segment, [](Ring<T, kWarps>&) {});
+    Sums sums = row_sums<kTop>(ring, task, at, count, segment, [](Ring<T, kWarps>&) {});
     if (warp == kWarps - 1) sums = together(lane == 0 ? sums : edges, lane < 2, task.c);
     if (lane == 0) s_warp[warp] = sums;
     __syncthreads();

@@ -8,8 +8,8 @@
 // Bound by memory: the logits are read once and the gradient is written once,
 // nothing in between is kept; about ten instructions per column beside them. p
 // comes from the stored norm, so that no row has to be summed up again. Measured: 4096 x
-// 262144 bf16 603 us, 7.1 TB/s; 777 x 50001 bf16 into fp32 (rows off 16-byte
-// boundaries, with the entropy's part) 39 us, 6.0 TB/s; 128 x 8192 2.9 us, the launch.
+// 262144 bf16 598 us, 7.1 TB/s; 777 x 50001 bf16 into fp32 (rows off 16-byte
+// boundaries, with the entropy's part) 38 us, 6.1 TB/s; 128 x 8192 2.9 us, the launch.
 #include "token_common.cuh"
 
 namespace drs {
