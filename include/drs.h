@@ -690,8 +690,8 @@ drs_status drs_token_logprobs_grad(const void *logits, drs_dtype dtype, int64_t 
  *               (of the same type and stride) or residual (of the same
  *               stride) itself, and does not overlap them otherwise.
  *
- * One launch, no workspace. rows == 0 is a no-op. Returns
- * DRS_ERR_INVALID_ARG for sizes out of range, p outside [0, 1], an unknown
+ * One launch (q = 1 without a residual: a fill), no workspace. rows == 0 is
+ * a no-op. Returns DRS_ERR_INVALID_ARG for sizes out of range, p outside [0, 1], an unknown
  * type, a stride below width, a null or unaligned pointer;
  * DRS_ERR_UNSUPPORTED for width > DRS_MAX_WIDTH or too many rows for one
  * launch (2^31 - 1 blocks).

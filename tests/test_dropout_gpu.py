@@ -42,7 +42,7 @@ def filled(rows, width, dtype, seed, pad=0, offset=0):
 def check(got, x, p, seed, residual=None, row0=0):
     mask, keep = kept(*x.shape, p, seed, row0)
     mask = torch.as_tensor(mask).cuda()
-    ref = torch.where(mask, x.double() / keep if keep else 0.0, 0.0)
+    ref = torch.where(mask, x.double() / keep if keep else 0.0, 0.0)  # what is dropped has no part in it
     tol = 2 * U * ref.abs()
     if residual is not None:
         ref = ref + residual.double()
@@ -85,6 +85,47 @@ def test_probabilities(p):
     residual, _ = filled(17, 1000, torch.float32, 2)
     check(drs().dropout(x, p, SEED), x, p, SEED)
     check(drs().dropout(x, p, SEED, residual=residual), x, p, SEED, residual)
+
+
+@pytest.mark.parametrize("p", [1.0, 1 - 2.0**-18, 0.0])
+@pytest.mark.parametrize("pad,offset", [(8, 8), (3, 5)])
+def test_all_and_nothing_dropped_in_strided_rows(p, pad, offset):
+    for dtype in TYPES.values():
+        x, _ = filled(9, 203, torch.float32, 1, pad, offset)
+        x[0, 0] = float("nan") if p else 1.0
+        residual, _ = filled(9, 203, dtype, 2, pad, offset)
+        out, whole = rows_in_buffer(9, 203, dtype, pad, offset)
+        check(drs().dropout(x, p, SEED, residual=residual, out=out), x, p, SEED, residual)
+        assert torch.isnan(whole[:, 203:]).all()
+        check(drs().dropout_grad(x, p, SEED, out=out), x, p, SEED)
+        assert torch.isnan(whole[:, 203:]).all()
+
+
+@pytest.mark.parametrize("p", [1.0, 0.25])
+def test_rows_that_lie_2_gib_apart(p):
+    stride = 2**30 + 8
+    whole = torch.empty(2 * stride + 203, dtype=torch.bfloat16, device="cuda")
+    out = whole.as_strided((3, 203), (stride, 1))
+    out.fill_(float("nan"))
+    beyond = whole.as_strided((2, 16), (stride, 1), 203)
+    beyond.fill_(5.0)
+    x, _ = filled(3, 203, torch.float32, 1)
+    check(drs().dropout(x, p, SEED, out=out), x, p, SEED)
+    out.fill_(float("nan"))
+    check(drs().dropout_grad(x, p, SEED, out=out), x, p, SEED)
+    assert (beyond == 5.0).all()
+
+
+def test_all_dropped_in_a_graph():
+    x, _ = filled(9, 203, torch.bfloat16, 1, 3, 5)
+    out, whole = rows_in_buffer(9, 203, torch.bfloat16, 3, 5)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        drs().dropout(x, 1.0, SEED, out=out)
+    for _ in range(2):
+        out.fill_(3.0)
+        graph.replay()
+        assert (out == 0).all() and torch.isnan(whole[:, 203:]).all()
 
 
 def test_the_share_dropped():

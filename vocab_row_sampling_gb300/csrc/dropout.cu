@@ -32,7 +32,7 @@ struct DropoutParams {
     const uint64_t* device_seed;
     uint64_t seed;
     int64_t rows, x_stride, residual_stride, out_stride, row0;
-    int32_t width, columns;  // columns: CTAs (or, for odd rows, groups of lanes) along a row
+    int32_t width, columns;  // columns: CTAs along a row
     uint32_t limit;          // of 2^32: 16-bit numbers below its upper half are dropped
     float scale;
 };
@@ -253,6 +253,21 @@ drs_status launch_dropout(DropoutParams a, bool vec, cudaStream_t stream) {
     return cuda_status(cudaGetLastError());
 }
 
+// Zeros in `rows` rows of `bytes` bytes. The runtime's pitched calls take pitches up to 2^31 - 1; an array of
+// wider ones has few rows.
+drs_status clear_rows(void* out, int64_t pitch, int64_t bytes, int64_t rows, cudaStream_t stream) {
+    if (rows == 1 || pitch == bytes) return cuda_status(cudaMemsetAsync(out, 0, static_cast<size_t>(rows * bytes), stream));
+    if (pitch <= INT32_MAX)
+        return cuda_status(cudaMemset2DAsync(out, static_cast<size_t>(pitch), 0, static_cast<size_t>(bytes),
+                                             static_cast<size_t>(rows), stream));
+    for (int64_t r = 0; r < rows; ++r) {
+        const drs_status st =
+            cuda_status(cudaMemsetAsync(static_cast<char*>(out) + r * pitch, 0, static_cast<size_t>(bytes), stream));
+        if (st != DRS_OK) return st;
+    }
+    return DRS_OK;
+}
+
 drs_status dropout(const void* x, drs_dtype dtype, int64_t rows, int64_t width, int64_t x_stride,
                    const void* residual, int64_t residual_stride, float p, uint64_t seed,
                    const uint64_t* device_seed, int64_t row0, void* out, drs_dtype out_dtype, int64_t out_stride,
@@ -282,10 +297,7 @@ drs_status dropout(const void* x, drs_dtype dtype, int64_t rows, int64_t width, 
     a.width = static_cast<int32_t>(width);
     const uint32_t dropped = static_cast<uint32_t>(std::floor(static_cast<double>(p) * 65536.0 + 0.5));
     if (dropped == 65536) {  // nothing of x is left
-        if (!residual)
-            return cuda_status(cudaMemset2DAsync(out, static_cast<size_t>(out_stride) * dtype_bytes(out_dtype), 0,
-                                                 static_cast<size_t>(width) * dtype_bytes(out_dtype),
-                                                 static_cast<size_t>(rows), stream));
+        if (!residual) return clear_rows(out, out_stride * dtype_bytes(out_dtype), width * dtype_bytes(out_dtype), rows, stream);
         return dropout(residual, out_dtype, rows, width, residual_stride, nullptr, 0, 0.0f, seed, device_seed, row0, out,
                        out_dtype, out_stride, stream);
     }
