@@ -49,6 +49,16 @@ def test_numbers_of_rows(dtype, kind, rows):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,vocab,k", [(500, 140001, 5), (600, 262144, 64), (1100, 70001, 20), (3300, 4099, 7), (4300, 4099, 7),
+                                          (2500, 15700, 61), (2500, 16000, 62), (1000, 16100, 63), (3000, 15900, 63)])
+def test_where_the_teams_change(dtype, rows, vocab, k):
+    """Numbers of rows at which other sizes of teams take them, and a few segments fewer than alternatives."""
+    logits = logits_of("ties" if k > 60 else "plain", rows, vocab, TYPES[dtype], vocab)
+    ids = ids_of(rows, vocab, 3)
+    check_logprobs(drs().token_logprobs(logits, ids, k), logits, ids, k)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("rows,vocab", [(3, 100000), (60, 30011), (700, 20000), (2500, 3000)])
 def test_temperatures_of_all_sizes_in_a_batch(dtype, rows, vocab):
     """Rows that need care from the start, on the way (huge logits) and not at all, in turn for one team."""

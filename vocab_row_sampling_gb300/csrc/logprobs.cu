@@ -30,6 +30,7 @@
 // takes 15 to 20, the rest the launch, the first loads and the selection; one row
 // of 262144 bf16 7.0 us with 20 alternatives, 4.0 without: launch, the read's
 // latency, a cluster's barrier.
+#include <algorithm>
 #include <climits>
 
 #include "token_common.cuh"
@@ -308,7 +309,8 @@ struct Selection {
     uint32_t* stage;
 
     __host__ __device__ static constexpr size_t bytes(int warps, int k, int element) {
-        const size_t stage = static_cast<size_t>(stage_bytes(warps, element)) * warps, units = size_t{128} * k;
+        const size_t stage = static_cast<size_t>(stage_bytes(warps, element)) * warps;
+        const size_t units = size_t{128} * ((k + 3) / 4 * 4);  // those of k segments, in fours
         return kListed * 8 + 2 * DRS_MAX_ALTERNATIVES * 4 + 16 + 128 * warps + (stage > units ? stage : units);
     }
     __device__ Selection(float* memory, int warps) {
@@ -1039,23 +1041,30 @@ template <typename T> drs_status launch_logprobs(LogprobParams a, bool vec, cuda
     const int64_t resident = int64_t{sms} * kResident;
     int cluster = 1, warps = 8;
     while (cluster < kMaxRowCluster && a.vocab > 8192 * cluster && a.rows * cluster * 2 <= resident / 8) cluster *= 2;
+    const bool top = a.k > 0;
+    const auto teams_of = [&](int w) {  // resident at once
+        const size_t smem = shared_bytes(w, a.k, sizeof(T), segments);
+        return int64_t{sms} * std::min<int64_t>(kSmemPerSm / (smem + kSmemReserved + 512), kResident / w);
+    };
     // Warps per row: as many as leave every row a team at once, but no fewer than suit the row's bytes. us with
     // 8, 4, 2 and 1 (16-bit): 300 x 65536 14.2, 16.1, 21.3, 43.5; 600 x 65536 26.5, 21.6, 24.7, 42.8; 1003 x 50001
     // 36.2, 32.5, 30.2, 39.2; 4096 x 8192 66.9, 47.5, 39.8, 33.9; 2500 x 20000 53.6, 42.2, 36.1, 36.2; 3000 x 60000
     // 90.8, 82.0, 81.1, 103; 1024 x 262144 91.5, 99.2, 107, 162; 4096 x 262144 350, 343, 358, 430; fp32: 2048 x
-    // 131072 166, 170, 201, 180; 1653 x 28800 52.2, 45.8, 46.4, 52.5.
-    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T));
+    // 131072 166, 170, 201, 180; 1653 x 28800 52.2, 45.8, 46.4, 52.5. Longer rows take fewer warps too where all
+    // rows then run at once, the first wave of larger teams leaving only a few: 600 x 262144 67.8, 57.7; fp32 500 x
+    // 131072 55.5, 48.1; 1216 x 131072 69.6, 64.6, 59.4; fp32 1003 x 65536 53.0, 59.2, 51.7. And they take two where
+    // one would leave a few rows over: 3200 x 4096 29.2 (four), 24.6, 30.9; fp32 34.6
+    // (four), 32.2, 43.5.
+    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T)), one = teams_of(1);
     const int64_t most = sizeof(T) == 2 && a.rows * 2 > resident ? 512 * 1024 : 256 * 1024;  // of a row for four warps
-    if (a.rows * 8 > resident && bytes <= most) warps = 4;
-    if (a.rows * 4 > resident && bytes <= 128 * 1024) warps = 2;
-    if (a.rows * 2 > resident && bytes <= 40 * 1024) warps = 1;
+    if (a.rows * 8 > resident && (bytes <= most || a.rows * 6 <= resident)) warps = 4;
+    if (a.rows * 4 > resident && bytes <= (a.rows * 3 <= resident ? 256 * 1024 : 128 * 1024)) warps = 2;
+    if (a.rows * 2 > resident && bytes <= 40 * 1024 && (a.rows <= one || a.rows * 5 > one * 7)) warps = 1;
     if (cluster > 1) warps = 8;
     a.cluster = cluster;
     a.part = static_cast<int32_t>(ceil_div(a.blocks, cluster));
-    const bool top = a.k > 0;
     const size_t smem = shared_bytes(warps, a.k, sizeof(T), segments);
-    const int per_sm = static_cast<int>(kSmemPerSm / (smem + kSmemReserved + 512));
-    const int64_t teams = int64_t{sms} * (per_sm < kResident / warps ? per_sm : kResident / warps);
+    const int64_t teams = teams_of(warps);
     const LogprobKernel kernel =
         cluster > 1 ? (top ? logprob_cluster_kernel<true, T> : logprob_cluster_kernel<false, T>) : logprob_kernel_of<T>(warps, top);
     const size_t large = smem > 46 * 1024 ? smem : 0;  // beyond what every launch may have, beside the static memory
