@@ -25,10 +25,10 @@
 // take about 8 issued per column (an exponential, a product and three sums
 // each), and 24 warps of 80 registers per SM do better than 32 of 64 (4096 x
 // 262144 bf16 rows with 20 alternatives 339 us against 371). Measured: these
-// 336 us, 6.3 TB/s (315, 6.7 TB/s, without alternatives); 256 x 262144 fp32 46 us,
+// 329 us, 6.4 TB/s (315, 6.7 TB/s, without alternatives); 256 x 262144 fp32 46 us,
 // 5.7 TB/s; 1003 x 50001 fp16 with 5 alternatives 27 us, of which the rows' reading
 // takes 15 to 20, the rest the launch, the first loads and the selection; one row
-// of 262144 bf16 7.0 us with 20 alternatives, 4.0 without: launch, the read's
+// of 262144 bf16 6.5 us with 20 alternatives, 3.9 without: launch, the read's
 // latency, a cluster's barrier.
 #include <algorithm>
 #include <climits>
@@ -299,54 +299,63 @@ template <int kWarps> __device__ __forceinline__ void team_sync() {
     else __syncthreads();
 }
 
-// A selection's memory: candidates' keys, segments chosen (and units), counters, each warp's words that hold
-// candidates, and the segments they look at (or the largest of units).
+// A selection's memory: candidates' keys, segments chosen (and units), counters, and the segments that the
+// warps look at (or the largest of units).
 struct Selection {
     uint64_t* list;
     int* chosen;
     int* counts;
-    uint8_t* words;
     uint32_t* stage;
 
     __host__ __device__ static constexpr size_t bytes(int warps, int k, int element) {
         const size_t stage = static_cast<size_t>(stage_bytes(warps, element)) * warps;
         const size_t units = size_t{128} * ((k + 3) / 4 * 4);  // those of k segments, in fours
-        return kListed * 8 + 2 * DRS_MAX_ALTERNATIVES * 4 + 16 + 128 * warps + (stage > units ? stage : units);
+        return kListed * 8 + 2 * DRS_MAX_ALTERNATIVES * 4 + 16 + (stage > units ? stage : units);
     }
-    __device__ Selection(float* memory, int warps) {
+    __device__ explicit Selection(float* memory) {
         list = reinterpret_cast<uint64_t*>(memory);
         chosen = reinterpret_cast<int*>(list + kListed);
         counts = chosen + 2 * DRS_MAX_ALTERNATIVES;
-        words = reinterpret_cast<uint8_t*>(counts + 4);
-        stage = reinterpret_cast<uint32_t*>(words + 128 * warps);
+        stage = reinterpret_cast<uint32_t*>(counts + 4);
     }
 };
 
-// Places for this warp's `mine` entries per lane in a list that the team counts in `count`: the lane's first.
-template <int kWarps> __device__ __forceinline__ int places_for(int mine, int* count, int lane) {
-    const int upto = warp_scan_inclusive(mine, lane);
-    int first = 0;
-    if (lane == 31) {
-        if constexpr (kWarps == 1) first = *count, *count = first + upto;
-        else if (upto) first = atomicAdd(count, upto);
-    }
-    return __shfl_sync(0xffffffffu, first, 31) + upto - mine;
+// Dynamic shared memory: the warps' rings, a selection's (kTop), the segments' largest (kTop).
+constexpr size_t kRingBytes = kDepth * kBlockBytes;
+__host__ __device__ constexpr size_t shared_before(int warps, int k, int element) {
+    return warps * kRingBytes + (k > 0 ? Selection::bytes(warps, k, element) : 0);
+}
+__host__ __device__ constexpr size_t shared_bytes(int warps, int k, int element, int segments) {
+    return shared_before(warps, k, element) + (k > 0 ? static_cast<size_t>(segments + 127) / 128 * 512 : 0);
 }
 
-// f(key, how many keys exceed it) for each of the n keys of a list, by the team.
-template <int kWarps, typename F> __device__ __forceinline__ void rank_keys(const uint64_t* list, int n, F f) {
+// Places for a thread's `mine` entries in a list that the team counts in `count`: the first. Their order differs from
+// call to call; what comes of the list does not, as it goes by the keys' ranks. (With scans of the warps in its
+// place, words that hold candidates listed before they are taken apart, and a lane to a key in the ranks: 4096 x 8192 with
+// 20 alternatives 35.3 us, 32.4 now; fp32 47.1, 41.6.)
+__device__ __forceinline__ int places_for(int mine, int* count) { return mine ? atomicAdd(count, mine) : 0; }
+
+// f(key, how many keys exceed it) for each of the n keys of a list, by the team: up to eight lanes to a key (kAlone:
+// eight).
+template <int kWarps, bool kAlone, typename F> __device__ __forceinline__ void rank_keys(const uint64_t* list, int n, F f) {
     const ulonglong2* const pairs = reinterpret_cast<const ulonglong2*>(list);
     constexpr int kThreads = kWarps * 32;
-    const uint64_t last = n ? list[n - 1] : 0;
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const uint64_t key = list[i];
-        int above = (n & 1) && last > key;
-#pragma unroll 8
-        for (int j = 0; j < n / 2; ++j) {
+    int shift = 3;
+    if constexpr (!kAlone)
+        while (shift > 0 && n << shift > kThreads) --shift;
+    const int part = threadIdx.x & ((1 << shift) - 1);
+    const uint64_t last = (n & 1) && part == 0 ? list[n - 1] : 0;
+    for (int i0 = 0; i0 < n; i0 += kThreads >> shift) {
+        const int i = i0 + (static_cast<int>(threadIdx.x) >> shift);
+        const uint64_t key = i < n ? list[i] : 0;
+        int above = last > key;
+#pragma unroll(kAlone ? 2 : 4)
+        for (int j = part; j < n / 2; j += 1 << shift) {
             const ulonglong2 p = pairs[j];
             above += (p.x > key) + (p.y > key);
         }
-        f(key, above);
+        for (int d = 1; d < 1 << shift; d <<= 1) above += __shfl_xor_sync(0xffffffffu, above, d);
+        if (i < n && part == 0) f(key, above);
     }
 }
 
@@ -394,6 +403,36 @@ __device__ __forceinline__ float reached_by(const float4* value, int n, int k, i
     if (k > 20) return kth_of_64(a, b, k);
     const float one[1] = {fmaxf(a, b)};
     return kth_of<1>(one, k);
+}
+
+// The same with 32 groups, by the team: each warp reads its share of the values, and the groups' largest are compared
+// in memory (64 floats per warp). For a team that is alone: with it, and the segments' ranks left out where one go takes
+// all listed, 16 x 262144 bf16 rows with 20 alternatives 10.2 us, 10.5 without; 16 x 46000 with 5 5.8, 6.1; but 4096 x
+// 8192, whose teams share their SM, 33.6, 32.5.
+template <int kWarps> __device__ __forceinline__ float reached_together(const float4* value, int n, int k, float* memory) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float v = -INFINITY;
+#pragma unroll 4
+    for (int i = warp; i < n; i += kWarps) {
+        const float4 u = value[i * 32 + lane];
+        v = fmaxf(v, fmaxf(fmaxf(u.x, u.y), fmaxf(u.z, u.w)));
+    }
+    if constexpr (kWarps > 1) {
+        memory[threadIdx.x] = v;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v = fmaxf(v, memory[w * 32 + lane]);
+    }
+    float* const own = memory + (kWarps + warp) * 32;
+    own[lane] = v;
+    __syncwarp();
+    int above = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 u = reinterpret_cast<const float4*>(own)[i];
+        above += (u.x > v) + (u.y > v) + (u.z > v) + (u.w > v);
+    }
+    return warp_min(above < k ? v : INFINITY);
 }
 
 // The k largest of n numbers, equal ones by index, as indices in ascending
@@ -461,14 +500,15 @@ template <typename T> __device__ __noinline__ int select_slowly(const Row<T> row
     return found;
 }
 
-// The row's k largest logits into s.list, in no order: how many keys, at least k. Apart from the
-// reading, whose registers it would take (4096 x 262144 bf16 348 us within, 336 apart).
+// The row's k largest logits into s.list, in no order: how many keys, at least k.
 // segment: its n segments' largest, with -inf up to a multiple of 128. s.counts are 0 before. By the
-// team, with a barrier at its end.
-template <int kWarps, typename T>
-__device__ __noinline__ int select_top(const Row<T> row, float* segment, int n, int k, const Selection s) {
+// team, with a barrier at its end. kAlone: nothing else runs meanwhile, so that its steps' latencies count, not its
+// instructions.
+template <int kWarps, bool kAlone, typename T>
+__device__ __forceinline__ int select_top(const Row<T>& row, float* segment, int n, int k, const Selection& s) {
     constexpr float kLowest = -0x1.fffffep127f;  // all but -inf and NaN reach it
     constexpr int kThreads = kWarps * 32;
+    constexpr int kBytes = kSegment * static_cast<int>(sizeof(T)), kStage = stage_bytes(kWarps, sizeof(T)), kAtOnce = kStage / kBytes;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int segments = n;       // looked at
     float least = kLowest;  // what reaches it is taken
@@ -476,7 +516,10 @@ __device__ __noinline__ int select_top(const Row<T> row, float* segment, int n, 
     if (n > k) {
         const int quads = (n + 127) / 128;
         const float4* const quad = reinterpret_cast<const float4*>(segment);
-        const float bound = fmaxf(reached_by(quad, quads, k, lane), kLowest);
+        const float reached = kAlone && k <= 20
+                                  ? reached_together<kWarps>(quad, quads, k, reinterpret_cast<float*>(s.stage))
+                                  : reached_by(quad, quads, k, lane);
+        const float bound = fmaxf(reached, kLowest);
         // 32 values per lane at a time: a bit for each that reaches the bound
         for (int i0 = warp; i0 < quads; i0 += 8 * kWarps) {
             uint32_t reach = 0;
@@ -488,17 +531,21 @@ __device__ __noinline__ int select_top(const Row<T> row, float* segment, int n, 
                 reach |= (v.x >= bound ? 1u : 0u) << (4 * i) | (v.y >= bound ? 2u : 0u) << (4 * i) |
                          (v.z >= bound ? 4u : 0u) << (4 * i) | (v.w >= bound ? 8u : 0u) << (4 * i);
             }
-            int at = places_for<kWarps>(__popc(reach), &s.counts[0], lane);
+            int at = places_for(__popc(reach), &s.counts[0]);
             for (; reach; reach &= reach - 1, ++at) {
                 const int bit = __ffs(reach) - 1, place = ((i0 + bit / 4 * kWarps) * 32 + lane) * 4 + bit % 4;
+                if (kAlone && at < kAtOnce * kWarps) s.chosen[at] = place;
                 if (at < kListed) s.list[at] = key_of(order_of(segment[place]), place);
             }
         }
         team_sync<kWarps>();
         const int listed = s.counts[0];
         slowly = listed > kListed;
-        if (!slowly) {
-            rank_keys<kWarps>(s.list, listed, [&](uint64_t key, int above) {
+        if (kAlone && listed <= kAtOnce * kWarps) {  // one go takes them all: no need of their ranks
+            segments = listed;
+            least = bound;
+        } else if (!slowly) {
+            rank_keys<kWarps, kAlone>(s.list, listed, [&](uint64_t key, int above) {
                 if (above < k) s.chosen[above] = place_of(key);
             });
             segments = min(listed, k);
@@ -516,19 +563,15 @@ __device__ __noinline__ int select_top(const Row<T> row, float* segment, int n, 
         team_sync<kWarps>();
     }
     if (!slowly) {
-        // Each warp has its share of the segments: their words that hold something to take, then these in turn
-        // by a lane each.
-        constexpr int kBytes = kSegment * static_cast<int>(sizeof(T)), kStage = stage_bytes(kWarps, sizeof(T)), kAtOnce = kStage / kBytes;
+        // Each warp has its share of the segments, each lane of their words.
         constexpr int kHalves = sizeof(T) / 2;
-        static_assert(kAtOnce * 32 <= 128, "words");
+        static_assert(kAtOnce * 8 <= 32, "bits");
         char* const stage = reinterpret_cast<char*>(s.stage) + warp * kStage;
-        uint8_t* const words = s.words + warp * 128;
         const uint32_t to = smem_u32(stage) + lane * 16;
-        const auto word_at = [&](int segment_at, int lane_at) {
+        const auto word_at = [&](int c) {
             Raw8<T> raw;
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h)
-                raw.w[h] = reinterpret_cast<const uint4*>(stage)[(segment_at * kHalves + h) * 32 + lane_at];
+            for (int h = 0; h < kHalves; ++h) raw.w[h] = reinterpret_cast<const uint4*>(stage)[(c * kHalves + h) * 32 + lane];
             return raw;
         };
         for (int c0 = warp; c0 < segments; c0 += kAtOnce * kWarps) {
@@ -553,36 +596,21 @@ __device__ __noinline__ int select_top(const Row<T> row, float* segment, int n, 
                 }
             }
             copies_commit();
-            copies_wait<0>();
-            __syncwarp();
-            uint32_t lanes = 0;  // of this lane's segment, those whose words hold something
+            copies_wait<0>();  // a lane reads what it has copied itself
+            uint32_t reach = 0;  // of this lane's words, eight bits for each segment
 #pragma unroll
             for (int c = 0; c < kAtOnce; ++c) {
-                const uint32_t some = __ballot_sync(0xffffffffu, Eight<T>::largest(word_at(c, lane)) >= least);
-                if (lane == c) lanes = some;
-            }
-            if (own < 0) lanes = 0;
-            const int mine = __popc(lanes), upto = warp_scan_inclusive(mine, lane);
-            const int count = __shfl_sync(0xffffffffu, upto, 31);
-            for (int at = upto - mine; lanes; lanes &= lanes - 1) words[at++] = static_cast<uint8_t>(lane * 32 + __ffs(lanes) - 1);
-            __syncwarp();
-            for (int i = lane; i - lane < count; i += 32) {
-                const int word = i < count ? words[i] : 0;
-                const int place = __shfl_sync(0xffffffffu, own, word / 32) * kSegment;
                 float v[8];
-                word_at(word / 32, word % 32).unpack(v);
-                uint32_t reach = 0;
+                word_at(c).unpack(v);
+                if (c0 + c * kWarps < segments)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) reach |= (v[e] >= least ? 1u : 0u) << e;
-                if (i >= count) reach = 0;
-                int at = places_for<kWarps>(__popc(reach), &s.counts[1], lane);
-                for (; reach; reach &= reach - 1, ++at) {
-                    const int in = place_in_segment<T>(word % 32, __ffs(reach) - 1);
-                    const T x = reinterpret_cast<const T*>(stage)[word / 32 * kSegment + in];
-                    if (at < kListed) s.list[at] = key_of(order_of(to_f(x)), place + in);
-                }
+                    for (int e = 0; e < 8; ++e) reach |= (v[e] >= least ? 1u : 0u) << (8 * c + e);
             }
-            __syncwarp();
+            for (int at = places_for(__popc(reach), &s.counts[1]); reach; reach &= reach - 1, ++at) {
+                const int bit = __ffs(reach) - 1, c = bit / 8, in = place_in_segment<T>(lane, bit % 8);
+                const T x = reinterpret_cast<const T*>(stage)[c * kSegment + in];
+                if (at < kListed) s.list[at] = key_of(order_of(to_f(x)), s.chosen[c0 + c * kWarps] * kSegment + in);
+            }
         }
         team_sync<kWarps>();
         slowly = s.counts[1] > kListed;
@@ -608,6 +636,32 @@ __device__ __noinline__ int select_top(const Row<T> row, float* segment, int n, 
         team_sync<kWarps>();
     }
     return s.counts[1];
+}
+
+// What the outputs of a row's alternatives need.
+struct TopOutputs {
+    int32_t* ids;
+    float* logprobs;
+    float top, inverse, log_sum;
+    int lead, k;
+    __device__ __forceinline__ void write(uint64_t key, int above) const {
+        if (above >= k) return;
+        ids[above] = place_of(key) - lead;
+        logprobs[above] = (value_of(static_cast<uint32_t>(key >> 32)) - top) * inverse - log_sum;
+    }
+};
+
+// Apart from the reading, whose registers it would take: 4096 x 262144 bf16 348 us within, 336 apart (with scans in the
+// lists). The outputs are written within by teams (329 us; apart as well 340), apart by clusters (one row of 262144 6.6 us
+// within, 6.4 apart).
+template <int kWarps, typename T>
+__device__ __noinline__ int select_top_apart(const Row<T> row, float* segment, int n, int k, const Selection s) {
+    return select_top<kWarps, false>(row, segment, n, k, s);
+}
+template <int kWarps, typename T>
+__device__ __noinline__ void select_alone(const Row<T> row, float* segment, int n, const Selection s, const TopOutputs out) {
+    const int found = select_top<kWarps, true>(row, segment, n, out.k, s);
+    rank_keys<kWarps, true>(s.list, found, [&](uint64_t key, int above) { out.write(key, above); });
 }
 
 // ------------------------------------------------------------- sums
@@ -782,18 +836,18 @@ __device__ __noinline__ Sums careful_sums(const Task<T> task, int first, int ste
 }
 
 // Adds the blocks among [first, end) of a row that reach over its ends to a warp's sums.
+// false: there are none.
 template <bool kTop, typename T>
-__device__ __forceinline__ void add_edges(const Task<T>& task, int first, int end, float* segment, Sums& sums) {
+__device__ __forceinline__ bool add_edges(const Task<T>& task, int first, int end, float* segment, Sums& sums) {
     const int whole_first = max(task.row.whole_first(), first), whole_end = min(task.row.whole_end(), end);
     const int lane = threadIdx.x & 31;
-    if (first < whole_first) {
-        const Sums more = careful_sums<T, kTop>(task, first, 1, min(whole_first, end), segment);
-        sums = together(lane == 0 ? sums : more, lane < 2, task.c);
-    }
-    if (whole_end < end && whole_end >= whole_first) {
+    const bool before = first < whole_first, behind = whole_end < end && whole_end >= whole_first;
+    if (before) sums = careful_sums<T, kTop>(task, first, 1, min(whole_first, end), segment);
+    if (behind) {
         const Sums more = careful_sums<T, kTop>(task, whole_end, 1, end, segment);
-        sums = together(lane == 0 ? sums : more, lane < 2, task.c);
+        sums = before ? together(lane == 0 ? sums : more, lane < 2, task.c) : more;
     }
+    return before || behind;
 }
 
 // The warp's blocks first, first + kStep, ... (count of them), which come through the ring; before the last kDepth
@@ -864,11 +918,11 @@ template <int kWarps, typename T> __device__ __forceinline__ void prepare(const 
 }
 
 // The row's outputs from its sums and segments, by the team.
-template <int kWarps, bool kTop, typename T>
+template <int kWarps, bool kTop, bool kAlone, typename T>
 __device__ __forceinline__ void finish(const LogprobParams& a, int64_t r, const Task<T>& task, const Sums& sums, float* segment,
                                        const Selection& s) {
     int found = 0;
-    if constexpr (kTop) found = select_top<kWarps>(task.row, segment, task.row.blocks() * kParts<T>, a.k, s);
+    if constexpr (kTop && !kAlone) found = select_top_apart<kWarps>(task.row, segment, task.row.blocks() * kParts<T>, a.k, s);
     const float log_sum = sums.sum == 0.0f ? -INFINITY : logf(sums.sum);
     if (threadIdx.x == (kWarps - 1) * 32) {
         a.out_logprob[r] = (to_f(task.own) - sums.top) * task.inverse - log_sum;
@@ -877,22 +931,10 @@ __device__ __forceinline__ void finish(const LogprobParams& a, int64_t r, const 
         if (a.out_norm) a.out_norm[2 * r] = sums.top, a.out_norm[2 * r + 1] = log_sum;
     }
     if constexpr (kTop) {
-        rank_keys<kWarps>(s.list, found, [&](uint64_t key, int above) {
-            if (above >= a.k) return;
-            a.out_ids[r * a.k + above] = place_of(key) - task.row.lead;
-            a.out_logprobs[r * a.k + above] =
-                (value_of(static_cast<uint32_t>(key >> 32)) - sums.top) * task.inverse - log_sum;
-        });
+        const TopOutputs out{a.out_ids + r * a.k, a.out_logprobs + r * a.k, sums.top, task.inverse, log_sum, task.row.lead, a.k};
+        if constexpr (kAlone) select_alone<kWarps>(task.row, segment, task.row.blocks() * kParts<T>, s, out);
+        else rank_keys<kWarps, false>(s.list, found, [&](uint64_t key, int above) { out.write(key, above); });
     }
-}
-
-// Dynamic shared memory: the warps' rings, a selection's (kTop), the segments' largest (kTop).
-constexpr size_t kRingBytes = kDepth * kBlockBytes;
-__host__ __device__ constexpr size_t shared_before(int warps, int k, int element) {
-    return warps * kRingBytes + (k > 0 ? Selection::bytes(warps, k, element) : 0);
-}
-__host__ __device__ constexpr size_t shared_bytes(int warps, int k, int element, int segments) {
-    return shared_before(warps, k, element) + (k > 0 ? static_cast<size_t>(segments + 127) / 128 * 512 : 0);
 }
 
 // ------------------------------------------------------------- many rows
@@ -903,7 +945,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident / kWarps) logprob_kerne
     extern __shared__ __align__(16) float s_memory[];
     __shared__ Sums s_warp[kWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const Selection select(s_memory + kWarps * kRingBytes / 4, kWarps);
+    const Selection select(s_memory + kWarps * kRingBytes / 4);
     float* const segment = s_memory + shared_before(kWarps, kTop ? a.k : 0, sizeof(T)) / 4;
     const int rows = static_cast<int>(a.rows), step = static_cast<int>(gridDim.x);
     Ring<T, kWarps> ring(s_memory);
@@ -931,14 +973,14 @@ __global__ void __launch_bounds__(kWarps * 32, kResident / kWarps) logprob_kerne
             if constexpr (kTop) prepare<kWarps>(task.row, segment, select);
             // what reaches over the row's ends, while the first blocks are on their way
             Sums edges{-INFINITY, 0.0f, 0.0f, 0};
-            if (warp == kWarps - 1) add_edges<kTop>(task, 0, task.row.blocks(), segment, edges);
+            const bool edged = warp == kWarps - 1 && add_edges<kTop>(task, 0, task.row.blocks(), segment, edges);
             Sums sums = row_sums<kTop>(ring, task, first, count, segment, [&](Ring<T, kWarps>& g) {
                 if (next_id >= 0 && count >= kDepth) {
                     g.point_at(next.row, next_first, next_count);
                     fetched = true;
                 }
             });
-            if (warp == kWarps - 1) sums = together(lane == 0 ? sums : edges, lane < 2, task.c);
+            if (edged) sums = together(lane == 0 ? sums : edges, lane < 2, task.c);
             if constexpr (kWarps > 1) {
                 if (lane == 0) s_warp[warp] = sums;
                 __syncthreads();
@@ -946,7 +988,7 @@ __global__ void __launch_bounds__(kWarps * 32, kResident / kWarps) logprob_kerne
             } else {
                 __syncwarp();
             }
-            finish<kWarps, kTop>(a, r, task, sums, segment, select);
+            finish<kWarps, kTop, false>(a, r, task, sums, segment, select);
             team_sync<kWarps>();
         } else {
             if (warp == 0) pass_over<kTop>(a, r);
@@ -970,7 +1012,7 @@ __global__ void __launch_bounds__(256, kResident / 8) logprob_cluster_kernel(con
     __shared__ Sums s_warp[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = static_cast<int>(cluster_rank());
-    const Selection select(s_memory + kWarps * kRingBytes / 4, kWarps);
+    const Selection select(s_memory + kWarps * kRingBytes / 4);
     float* const segment = s_memory + shared_before(kWarps, kTop ? a.k : 0, sizeof(T)) / 4;
     const int r = static_cast<int>(blockIdx.x / a.cluster);
     cluster_arrive();
@@ -991,9 +1033,9 @@ __global__ void __launch_bounds__(256, kResident / 8) logprob_cluster_kernel(con
     const Task<T> task(a, r, id);
     if constexpr (kTop) prepare<kWarps>(row, segment, select);
     Sums edges{-INFINITY, 0.0f, 0.0f, 0};
-    if (warp == kWarps - 1) add_edges<kTop>(task, first, end, segment, edges);
+    const bool edged = warp == kWarps - 1 && add_edges<kTop>(task, first, end, segment, edges);
     Sums sums = row_sums<kTop>(ring, task, at, count, segment, [](Ring<T, kWarps>&) {});
-    if (warp == kWarps - 1) sums = together(lane == 0 ? sums : edges, lane < 2, task.c);
+    if (edged) sums = together(lane == 0 ? sums : edges, lane < 2, task.c);
     if (lane == 0) s_warp[warp] = sums;
     __syncthreads();
     cluster_wait();
@@ -1015,7 +1057,7 @@ __global__ void __launch_bounds__(256, kResident / 8) logprob_cluster_kernel(con
     unpack2(s_cta[from][1], sums.weighted, above);
     sums.above = __float_as_int(above);
     sums = together(sums, lane < a.cluster, task.c);
-    finish<kWarps, kTop>(a, r, task, sums, segment, select);
+    finish<kWarps, kTop, true>(a, r, task, sums, segment, select);
 }
 
 // ------------------------------------------------------------- launches
