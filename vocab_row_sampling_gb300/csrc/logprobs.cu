@@ -1076,28 +1076,31 @@ template <typename T> drs_status launch_logprobs(LogprobParams a, bool vec, cuda
     if (sms <= 0) return DRS_ERR_CUDA;
     a.blocks = static_cast<int32_t>(ceil_div(a.vocab + (vec ? 0 : 16 / sizeof(T) - 1), kBlock<T>));
     const int segments = a.blocks * kParts<T>;
-    // CTAs per row: as many as are resident at once, with more than 4096 columns each. us with one, 2, 4, 8 and 16
-    // (20 alternatives, bf16): 1 x 262144 19.9, 13.3, 9.8, 8.0, 7.2; 16 x 262144 21.6, 14.6, 11.0, 10.5, 11.1; 50 x
-    // 131072 14.0, 10.8, 10.3, 10.8; 110 x 262144 21.5, 19.3, 17.8; 225 x 262144 31.2, 26.6; a second wave costs
-    // more: 300 x 131072 19.7, 26.1.
+    const bool top = a.k > 0;
+    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T));
+    // CTAs per row: as many as are resident at once, with more than 4096 columns each; with alternatives, and more CTAs
+    // than SMs, with 40 KB each, as the selection's CTA waits for all of them. us with one, 2, 4, 8 and 16 (20
+    // alternatives, bf16): 1 x 262144 18.8, 12.7, 9.2, 7.2, 6.6; 16 x 262144 20.4, 14.0, 10.5, 9.6, 10.3; 50 x 131072
+    // 13.6, 10.7, 10.2, 10.8; 100 x 20000 7.7, 8.6, 9.1; 64 x 46000 9.7, 9.1, 8.6 (without alternatives 6.5, 5.7, 5.0);
+    // 110 x 262144 21.2, 19.4, 18.0; 225 x 262144 30.6, 26.8; a second wave costs more: 300 x 131072 19.4, 25.4.
     const int64_t resident = int64_t{sms} * kResident;
     int cluster = 1, warps = 8;
-    while (cluster < kMaxRowCluster && a.vocab > 8192 * cluster && a.rows * cluster * 2 <= resident / 8) cluster *= 2;
-    const bool top = a.k > 0;
+    while (cluster < kMaxRowCluster && a.vocab > 8192 * cluster && a.rows * cluster * 2 <= resident / 8 &&
+           (!top || a.rows * cluster * 2 <= sms || bytes >= 80 * 1024 * cluster))
+        cluster *= 2;
     const auto teams_of = [&](int w) {  // resident at once
         const size_t smem = shared_bytes(w, a.k, sizeof(T), segments);
         return int64_t{sms} * std::min<int64_t>(kSmemPerSm / (smem + kSmemReserved + 512), kResident / w);
     };
     // Warps per row: as many as leave every row a team at once, but no fewer than suit the row's bytes. us with
-    // 8, 4, 2 and 1 (16-bit): 300 x 65536 14.2, 16.1, 21.3, 43.5; 600 x 65536 26.5, 21.6, 24.7, 42.8; 1003 x 50001
-    // 36.2, 32.5, 30.2, 39.2; 4096 x 8192 66.9, 47.5, 39.8, 33.9; 2500 x 20000 53.6, 42.2, 36.1, 36.2; 3000 x 60000
-    // 90.8, 82.0, 81.1, 103; 1024 x 262144 91.5, 99.2, 107, 162; 4096 x 262144 350, 343, 358, 430; fp32: 2048 x
-    // 131072 166, 170, 201, 180; 1653 x 28800 52.2, 45.8, 46.4, 52.5. Longer rows take fewer warps too where all
-    // rows then run at once, the first wave of larger teams leaving only a few: 600 x 262144 67.8, 57.7; fp32 500 x
-    // 131072 55.5, 48.1; 1216 x 131072 69.6, 64.6, 59.4; fp32 1003 x 65536 53.0, 59.2, 51.7. And they take two where
-    // one would leave a few rows over: 3200 x 4096 29.2 (four), 24.6, 30.9; fp32 34.6
-    // (four), 32.2, 43.5.
-    const int64_t bytes = a.vocab * static_cast<int64_t>(sizeof(T)), one = teams_of(1);
+    // 8, 4, 2 and 1 (16-bit): 300 x 65536 13.8, 15.1, 20.4, 40.6; 600 x 65536 25.7, 20.4, 23.5, 40.9; 1003 x 50001
+    // 37.0, 33.7, 31.7, 41.8; 4096 x 8192 62.1, 42.0, 32.6, 33.3; 2500 x 20000 51.9, 40.1, 35.6, 36.9; 3000 x 60000
+    // 88.6, 77.2, 77.5, 101; 1024 x 262144 89.6, 99.9, 103, 149; 4096 x 262144 340, 327, 344, 414; fp32: 2048 x
+    // 131072 161, 165, 198, 173; 1653 x 28800 50.4, 43.8, 44.4, 49.7. Longer rows take fewer warps too where all
+    // rows then run at once, the first wave of larger teams leaving only a few: 600 x 262144 65.0, 55.8; fp32 500 x
+    // 131072 53.8, 47.4; 1216 x 131072 67.2, 61.6, 57.5; fp32 1003 x 65536 51.4, 57.3, 49.3. And they take two where
+    // one would leave a few rows over: 3200 x 4096 28.5 (four), 23.9, 29.6; fp32 33.6 (four), 28.9, 38.1.
+    const int64_t one = teams_of(1);
     const int64_t most = sizeof(T) == 2 && a.rows * 2 > resident ? 512 * 1024 : 256 * 1024;  // of a row for four warps
     if (a.rows * 8 > resident && (bytes <= most || a.rows * 6 <= resident)) warps = 4;
     if (a.rows * 4 > resident && bytes <= (a.rows * 3 <= resident ? 256 * 1024 : 128 * 1024)) warps = 2;
