@@ -948,8 +948,8 @@ def token_logprobs(logits, ids, k: int = 0, temps=None, canvas_len: int = 1, out
     Returns `out`: (logprob, entropy, rank, norm [rows, 2], top_ids [rows, k],
     top_logprobs [rows, k]), allocated when not given. No autograd history:
     the gradient is token_logprobs_grad, which takes norm and entropy."""
-    import torch
     if out is None:
+        import torch
         dev, rows = logits.device, logits.shape[0]
         f32, i32 = dict(dtype=torch.float32, device=dev), dict(dtype=torch.int32, device=dev)
         with _allocate_on(stream):
@@ -970,8 +970,8 @@ def token_logprobs_grad(logits, ids, norm, grad_logprob, entropy=None, grad_entr
     logits, from its norm (and entropy, with grad_entropy), written into out
     [rows, vocab] (allocated in the logits' type when not given; logits
     itself is allowed), which is returned (see drs_token_logprobs_grad)."""
-    import torch
     if out is None:
+        import torch
         with _allocate_on(stream):
             out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
     drs_token_logprobs_grad(logits, ids, temps, canvas_len, norm, entropy, grad_logprob, grad_entropy, out, stream)
@@ -984,8 +984,8 @@ def dropout(x, p: float, seed, residual=None, row0: int = 0, out=None, stream=No
     of one element on the GPU), row0 and the place, and is not stored. out:
     of the residual's type, or x's, when not given. No autograd history: the
     gradient is dropout_grad."""
-    import torch
     if out is None:
+        import torch
         with _allocate_on(stream):
             out = torch.empty(x.shape, dtype=x.dtype if residual is None else residual.dtype, device=x.device)
     drs_dropout(x, residual, p, seed, row0, out, stream)
@@ -996,8 +996,8 @@ def dropout_grad(grad_out, p: float, seed, row0: int = 0, out=None, stream=None)
     """The gradient of dropout with respect to x, from the p, seed and row0 of
     the forward call, written into out (allocated in grad_out's type when not
     given; grad_out itself is allowed), which is returned."""
-    import torch
     if out is None:
+        import torch
         with _allocate_on(stream):
             out = torch.empty(grad_out.shape, dtype=grad_out.dtype, device=grad_out.device)
     drs_dropout_grad(grad_out, p, seed, row0, out, stream)
