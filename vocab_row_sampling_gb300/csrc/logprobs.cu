@@ -695,6 +695,8 @@ template <typename T, bool kCareful> struct RunningSums {
     float top = -INFINITY, bound = -INFINITY;  // bound: where the reference moves
     float base = 0.0f;                         // careful: M, else M c rounded; 0 before there is one
     bool none = true;
+    // Without a reference the floor may be -inf, by which add() multiplies 0: weighted then counts as sum, which is 0, or
+    // NaN after a NaN.
     uint64_t sum = 0, weighted = 0;
     Floor<T> floor;
 
@@ -713,6 +715,7 @@ template <typename T, bool kCareful> struct RunningSums {
         const float d = none ? 0.0f : max_nan(kCareful ? (base - next) * c : base - next, -1000.0f);
         const float f = ex2_approx(d);
         const uint64_t f2 = pack2(f, f);
+        if (none) weighted = sum;
         weighted = mul2(f2, fma2(pack2(d, d), sum, weighted));
         sum = mul2(f2, sum);
         base = next;
@@ -755,7 +758,7 @@ template <typename T, bool kCareful> struct RunningSums {
         float s0, s1, w0, w1;
         unpack2(sum, s0, s1);
         unpack2(weighted, w0, w1);
-        if (none) w0 = s0, w1 = s1;  // 0, or NaN: without a reference the floor may be -inf, which 0 is multiplied by
+        if (none) w0 = s0, w1 = s1;
         const float d = distance(top, c), f = ex2_approx(d);
         return Sums{top, warp_sum(f * (s0 + s1)), warp_sum(f * fmaf(d, s0 + s1, w0 + w1)), warp_sum(above)};
     }
