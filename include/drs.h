@@ -608,6 +608,7 @@ drs_status drs_embed_tokens_grad(const void *grad_out, drs_dtype grad_dtype, int
  *                and their log probabilities.
  * out_entropy, out_rank and out_norm may be NULL; so may out_ids and
  * out_logprobs when k is 0.
+ * ln S and the entropy are at least 0 and log probabilities at most 0.
  *
  *   logits      dtype [rows, vocab], row stride row_stride.
  *   ids         int32 or int64 [rows] (id_bits 32 or 64). A row whose id is

@@ -39,3 +39,25 @@ def test_masked_prefixes_before_the_first_reference(dtype, temp, centre, spread,
     value, tol = grad_reference(logits, ids, out[3], one, out[1], one, temps, rows, TYPES[dtype])
     close(grad[alive], value[alive], tol[alive], "gradient")
     assert (grad[~alive] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("kind", ["alone", "peaks", "ties", "far"])
+@pytest.mark.parametrize("rows,vocab", [(40, 20011), (300, 8192), (3000, 1000)])
+@pytest.mark.parametrize("temp", [None, 0.013, 0.7, 31.0])
+def test_no_log_probability_above_zero_and_no_entropy_below(dtype, kind, rows, vocab, temp):
+    """S holds the largest logit's term, 1, so that ln S >= 0, every log probability <= 0 and the entropy >= 0, by exactly
+    that much: no tolerance. Rows whose largest logit is all there is (alone: of any value, all others -inf) are
+    those where the sum's own roundings decide."""
+    logits, ids = logits_of("plain" if kind == "alone" else kind, rows, vocab, TYPES[dtype], rows), ids_of(rows, vocab, rows)
+    if kind == "alone":
+        at = torch.arange(rows, device="cuda")
+        peak = (100 * logits[:, 0].float()).to(TYPES[dtype])
+        logits.fill_(-INF)
+        logits[at, at % vocab] = peak
+        ids[::2] = (at % vocab)[::2]
+    temps = None if temp is None else torch.tensor([temp], device="cuda")
+    out = drs().token_logprobs(logits, ids, 6, temps, rows)
+    check_logprobs(out, logits, ids, 6, temps, rows)
+    logprob, entropy, _, norm, _, top = out
+    assert (logprob <= 0).all() and (entropy >= 0).all() and (norm[:, 1] >= 0).all() and (top <= 0).all()

@@ -926,10 +926,12 @@ __device__ __forceinline__ void finish(const LogprobParams& a, int64_t r, const 
                                        const Selection& s) {
     int found = 0;
     if constexpr (kTop && !kAlone) found = select_top_apart<kWarps>(task.row, segment, task.row.blocks() * kParts<T>, a.k, s);
-    const float log_sum = sums.sum == 0.0f ? -INFINITY : logf(sums.sum);
+    // The largest logit's term is 1: a sum below that is off by the roundings of its exponent alone. No log
+    // probability exceeds 0 and no entropy falls below it.
+    const float log_sum = sums.sum == 0.0f ? -INFINITY : sums.sum < 1.0f ? 0.0f : logf(sums.sum);
     if (threadIdx.x == (kWarps - 1) * 32) {
         a.out_logprob[r] = (to_f(task.own) - sums.top) * task.inverse - log_sum;
-        if (a.out_entropy) a.out_entropy[r] = sums.sum == 0.0f ? 0.0f : log_sum - sums.weighted / sums.sum * kLn2;
+        if (a.out_entropy) a.out_entropy[r] = sums.sum == 0.0f ? 0.0f : max_nan(log_sum - sums.weighted / sums.sum * kLn2, 0.0f);
         if (a.out_rank) a.out_rank[r] = 1 + sums.above;
         if (a.out_norm) a.out_norm[2 * r] = sums.top, a.out_norm[2 * r + 1] = log_sum;
     }
