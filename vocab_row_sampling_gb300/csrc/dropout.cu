@@ -97,9 +97,9 @@ __global__ void __launch_bounds__(kDropoutThreads) dropout_kernel(const DropoutP
         groups[i] = static_cast<uint32_t>(group);
         row[i] = static_cast<uint64_t>(a.row0 + r);
         if (r >= a.rows) continue;
-        x[i].load(static_cast<const X*>(a.x) + r * a.x_stride + group * 8);
+        x[i].template load<true>(static_cast<const X*>(a.x) + r * a.x_stride + group * 8);
         if constexpr (kResidual)
-            residual[i].load(static_cast<const Y*>(a.residual) + r * a.residual_stride + group * 8);
+            residual[i].template load<true>(static_cast<const Y*>(a.residual) + r * a.residual_stride + group * 8);
     }
     uint4 w[kRows];
     dropout_words(dropout_key(a), row, groups, w);
@@ -187,11 +187,11 @@ __global__ void __launch_bounds__(kDropoutThreads) dropout_odd_kernel(const Drop
     for (int h = 0; h < 2; ++h) {
         if (!writes || col + 8 * h + 8 > a.width) continue;
         if constexpr (kAlike) {
-            x[h].load(from + (col + 8 * h));
-            if constexpr (kResidual) residual[h].load(rest + (col + 8 * h));
+            x[h].template load<true>(from + (col + 8 * h));
+            if constexpr (kResidual) residual[h].template load<true>(rest + (col + 8 * h));
         } else {
-            x[h].load(from, col + 8 * h, a.width);
-            if constexpr (kResidual) residual[h].load(rest, col + 8 * h, a.width);
+            x[h].template load<true>(from, col + 8 * h, a.width);
+            if constexpr (kResidual) residual[h].template load<true>(rest, col + 8 * h, a.width);
         }
     }
     const uint64_t row[2] = {static_cast<uint64_t>(a.row0 + r), static_cast<uint64_t>(a.row0 + r)};

@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_kernel(const Logpro
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) {
         const int col = first + u * kGradThreads * 8;
-        if (col + 8 <= a.vocab) raw[u].load(x + col);
+        if (col + 8 <= a.vocab) raw[u].template load<true>(x + col);
     }
     const RowTerms terms(a, row);
 #pragma unroll
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kGradThreads) logprob_grad_odd_kernel(const Lo
 #pragma unroll
     for (int u = 0; u < kOddUnits; ++u) {
         const int col = first + u * kGradThreads * 8;
-        if (col < tail) raw[u].load(x, col, a.vocab);
+        if (col < tail) raw[u].template load<true>(x, col, a.vocab);
     }
     const RowTerms terms(a, row);
 #pragma unroll

@@ -35,12 +35,21 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// 16 bytes read once: not kept in L1.
-__device__ __forceinline__ uint4 load16_stream(const void* p) {
+// 16 bytes read once: not kept in L1. kWritten: of an array that the launch may
+// write as well (an output that is an input), for which the read-only path is
+// not defined. What a thread then stores in its place comes of these bytes, so
+// that the two need no other order.
+template <bool kWritten = false> __device__ __forceinline__ uint4 load16_stream(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+    if constexpr (kWritten) {
+        asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(p));
+    } else {
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "l"(p));
+    }
     return v;
 }
 
@@ -48,10 +57,10 @@ __device__ __forceinline__ uint4 load16_stream(const void* p) {
 // or two 16-byte words.
 template <typename T> struct Raw8 {
     uint4 w[sizeof(T) / 2];
-    __device__ __forceinline__ void load(const T* p) {
+    template <bool kWritten = false> __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
         for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-            w[i] = load16_stream(reinterpret_cast<const char*>(p) + 16 * i);
+            w[i] = load16_stream<kWritten>(reinterpret_cast<const char*>(p) + 16 * i);
     }
     __device__ __forceinline__ void unpack(float (&v)[8]) const;
 };
@@ -96,12 +105,12 @@ template <typename T> struct Raw8Shifted {
     uint4 w[sizeof(T) / 2 + 1];
     // first: the start of the word that holds the first element, `shift`
     // bytes before it
-    __device__ __forceinline__ void load(const T* first, int shift) {
+    template <bool kWritten = false> __device__ __forceinline__ void load(const T* first, int shift) {
 #pragma unroll
         for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-            w[i] = load16_stream(reinterpret_cast<const char*>(first) + 16 * i);
+            w[i] = load16_stream<kWritten>(reinterpret_cast<const char*>(first) + 16 * i);
         w[sizeof(T) / 2] = make_uint4(0, 0, 0, 0);
-        if (shift) w[sizeof(T) / 2] = load16_stream(reinterpret_cast<const char*>(first) + 8 * sizeof(T));
+        if (shift) w[sizeof(T) / 2] = load16_stream<kWritten>(reinterpret_cast<const char*>(first) + 8 * sizeof(T));
     }
     __device__ __forceinline__ void unpack(int shift, float (&v)[8]) const {
         Raw8<T> r;
@@ -113,16 +122,16 @@ template <typename T> struct Raw8Shifted {
 
 // Eight consecutive elements of a row, wherever they start: the aligned words
 // that hold them where these lie inside the row, else one by one. Elements from
-// `width` on are 0.
+// `width` on are 0. kWritten as in load16_stream.
 template <typename T> struct Any8 {
     Raw8Shifted<T> raw;
     int shift;
-    __device__ __forceinline__ void load(const T* row, int col, int width) {
+    template <bool kWritten = false> __device__ __forceinline__ void load(const T* row, int col, int width) {
         constexpr int kVec = 16 / sizeof(T);
         shift = static_cast<int>(reinterpret_cast<uintptr_t>(row + col) & 15);
         const int off = shift / static_cast<int>(sizeof(T));
         if (col >= off && col - off + (off ? kVec : 0) + 8 <= width) {
-            raw.load(row + (col - off), shift);
+            raw.template load<kWritten>(row + (col - off), shift);
         } else {
             shift = 0;
             T* const e = reinterpret_cast<T*>(raw.w);
