@@ -9,8 +9,8 @@ import pytest
 from test_cluster_start_host import without_comments
 from vocab_row_sampling_gb300 import _build
 
-# out may be x or residual; grad may be logits; out_held may be held
-IN_PLACE = ("dropout.cu", "logprobs_grad.cu", "slots.cu")
+# out may be x or residual; grad may be logits; out may be logits; out_held may be held
+IN_PLACE = ("dropout.cu", "logprobs_grad.cu", "scale.cu", "slots.cu")
 READ_ONLY = re.compile(r"\.nc\b|__ldg\s*\(|(?:\.\s*(?:template\s+)?load|\bload16_stream)\s*(?:<\s*false\s*>)?\s*\(|__restrict__")
 
 
