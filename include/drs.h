@@ -608,7 +608,10 @@ drs_status drs_embed_tokens_grad(const void *grad_out, drs_dtype grad_dtype, int
  *                and their log probabilities.
  * out_entropy, out_rank and out_norm may be NULL; so may out_ids and
  * out_logprobs when k is 0.
- * ln S and the entropy are at least 0 and log probabilities at most 0.
+ * ln S and the entropy are at least 0 and log probabilities at most 0. All is
+ * computed in fp32, quotients by te as products with 1 / te: where one logit
+ * holds nearly all of the sum, ln S and its token's log probability are right
+ * to a few steps of fp32 at 1, not of themselves.
  *
  *   logits      dtype [rows, vocab], row stride row_stride.
  *   ids         int32 or int64 [rows] (id_bits 32 or 64). A row whose id is
@@ -624,7 +627,9 @@ drs_status drs_embed_tokens_grad(const void *grad_out, drs_dtype grad_dtype, int
  * columns rank below all others, with -inf ones in column order.
  *
  * One launch, no workspace. rows == 0 is a no-op. Any stride and alignment
- * that the type allows. Returns DRS_ERR_INVALID_ARG for sizes out of range
+ * that the type allows. Masks are best made of -inf: rows that begin with long
+ * stretches of the type's lowest finite value are read twice.
+ * Returns DRS_ERR_INVALID_ARG for sizes out of range
  * (k > vocab among them), an unknown type, a stride below vocab, a null or
  * unaligned pointer; DRS_ERR_UNSUPPORTED for vocab > DRS_MAX_VOCAB,
  * k > DRS_MAX_ALTERNATIVES or rows > DRS_MAX_SCORE_ROWS; DRS_ERR_CUDA for few

@@ -947,7 +947,8 @@ def token_logprobs(logits, ids, k: int = 0, temps=None, canvas_len: int = 1, out
     entropy, rank and the k largest alternatives (see drs_token_logprobs).
     Returns `out`: (logprob, entropy, rank, norm [rows, 2], top_ids [rows, k],
     top_logprobs [rows, k]), allocated when not given. No autograd history:
-    the gradient is token_logprobs_grad, which takes norm and entropy."""
+    the logits' gradient is token_logprobs_grad, which takes norm and entropy;
+    there is none for temps."""
     if out is None:
         import torch
         dev, rows = logits.device, logits.shape[0]

@@ -24,7 +24,7 @@
 // Bound by memory for large batches, by instructions close behind: 16-bit rows
 // take about 8 issued per column (an exponential, a product and three sums
 // each), and 24 warps of 80 registers per SM do better than 32 of 64 (4096 x
-// 262144 bf16 rows with 20 alternatives 339 us against 371). Measured: these
+// 262144 bf16 rows with 20 alternatives 329 us against 416). Measured: these
 // 329 us, 6.4 TB/s (315, 6.7 TB/s, without alternatives); 256 x 262144 fp32 46 us,
 // 5.7 TB/s; 1003 x 50001 fp16 with 5 alternatives 27 us, of which the rows' reading
 // takes 15 to 20, the rest the launch, the first loads and the selection; one row
@@ -43,8 +43,10 @@ constexpr int kMaxRowCluster = 16;
 constexpr int kListed = 256;       // candidates of the short way
 constexpr int kSegment = 256;      // columns whose largest is kept: eight per lane of a warp
 constexpr int kBlockBytes = 1024;  // what a warp takes at once: two 16-byte words per lane
-// Blocks on their way to a warp. us for 2432 x 262144 bf16 rows without alternatives with 2, 3, 4 and 5 (32 warps per
-// SM): 211, 206, 199, 202; in registers instead of shared memory 234 with 2.
+// Blocks on their way to a warp. us with 2, 3, 4, 5 and 6: 4096 x 262144 bf16 rows with 20 alternatives 354, 334, 329, 332,
+// 333, 2432 without alternatives 206, 195, 190, 194, 194; 256 x 262144 fp32 55.9, 48.6, 46.3, 45.6, 45.5; 1003 x 50001
+// fp16 with 5 29.0, 27.0, 26.6, 27.5, 27.8; 4096 x 8192 fp32 46.5, 43.4, 41.6, 47.5, 47.2 (larger rings leave room for
+// fewer teams).
 constexpr int kDepth = 4;
 // Exponents (base 2) below this give 0; held there so that 0 times an
 // infinite exponent does not arise in W.
@@ -468,7 +470,9 @@ __device__ int select_exact(const uint32_t* value, int n, int k, int* chosen, in
 }
 
 // For rows with many equal logits, or where they rise over long stretches: the k segments,
-// then their k units of eight columns, then their k elements.
+// then their k units of eight columns, then their k elements, by one warp. us for 4096 x 262144 bf16 with 20 (64)
+// alternatives: sorted rows 465 (687), constant ones 500 (718), others 330 (373); one row 36, 42, 6.5 with 20; 4096 x 8192
+// 131, 155, 32.6.
 template <typename T> __device__ __noinline__ int select_slowly(const Row<T> row, float* segment, int n, int k, const Selection s) {
     const int lane = threadIdx.x & 31;
     uint32_t* const order = reinterpret_cast<uint32_t*>(segment);
@@ -886,7 +890,10 @@ __device__ __forceinline__ Sums ring_sums(Ring<T, kStep>& ring, const Task<T>& t
     return careful_sums<T, kTop>(task, first, kStep, first + (count - 1) * kStep + 1, segment);
 }
 
-// With care from the start where temperatures leave no doubt (0, say); beyond it only logits above 4096 do.
+// With care from the start where temperatures leave no doubt (0, say); beyond it only logits above 4096 do. us for 4096 x
+// 262144 bf16 with 20 alternatives: 367 with care from the start, 330 without. A warp whose first blocks hold the
+// type's lowest value throughout, as some masks do, finds out on the way and reads its share again by plain loads: 769
+// for rows that begin so, 330 where they begin with -inf or hold the lowest value here and there.
 constexpr float kCarefulFrom = 4096.0f;  // c
 template <bool kTop, typename T, int kStep, typename F>
 __device__ __forceinline__ Sums row_sums(Ring<T, kStep>& ring, const Task<T>& task, int first, int count, float* segment, F go_on) {
